@@ -439,6 +439,93 @@ int b200q_kv_append(float *const *lat_pages, float *const *rope_pages, int K, in
                     const float *rope_rows, int n, void *stream);
 
 /*
+ * ---- 8-bit activations ----
+ *
+ * Activation rows as E4M3 bytes with one f32 scale per row, for a layer whose
+ * activations move and multiply in 8 bits: the norm (or any row) is quantised
+ * as it is written, and the matmuls read the bytes.  The pages hold
+ * activations in f32 and print nothing of this kind; the formulas here are
+ * the library's own.
+ *
+ * Element types of the wide operands (x, r, h, y, res).
+ */
+enum { B200Q_T_F32 = 0, B200Q_T_F16 = 1, B200Q_T_BF16 = 2 };
+
+/* Activations of the epilogues: identity, max(v, 0), v Phi(v) with the normal
+ * distribution's Phi, v / (1 + e^-2a) with a = sqrt(2/pi) (v + 0.044715 v^3),
+ * v / (1 + e^-v). */
+enum { B200Q_ACT_NONE = 0, B200Q_ACT_RELU = 1, B200Q_ACT_GELU = 2, B200Q_ACT_GELU_TANH = 3, B200Q_ACT_SILU = 4 };
+
+/*
+ * Rows to 8 bits: per row s of S rows of D values,
+ *     ys[s] = max(max_d |x[s,d]| / 448, 2^-126),   y8[s,d] = e4m3(x[s,d] / ys[s])
+ * (448 is the largest E4M3 value; nearest, ties to even).  A row of zeros has
+ * the scale 2^-126 and zero codes.  A row that holds an infinity or a NaN gets
+ * a scale that is not finite, so every product with it is not finite either.
+ *   x      DEVICE pointer, S rows of D values of `type`, ldx >= D values
+ *          apart; aligned to its type
+ *   y8     DEVICE pointer, 16-byte aligned, S rows of D bytes, ld8 >= D bytes
+ *          apart, ld8 a multiple of 16.  Bytes D .. ld8-1 of a row are not
+ *          written (and no call reads them)
+ *   ys     DEVICE pointer to S floats
+ * y8 and ys must not overlap x.  S = 0 is a no-op.  Asynchronous on `stream`;
+ * one launch, no workspace.
+ */
+int b200q_quantize_q8(const void *x, int type, long long ldx, void *y8, long long ld8, float *ys, int S, int D,
+                      void *stream);
+
+/*
+ * RMSNorm with an optional residual, quantised as it is written:
+ *     h = x + r (r NULL: h = x),  y = h * w / sqrt(mean_d h^2 + eps)
+ *     ys[s] = max(max_d |y| / 448, 2^-126),  y8 = e4m3(y / ys[s])
+ * Everything is f32 from the first addition on: y and its scale come from the
+ * f32 sum, h is rounded to `type` only where it is stored.
+ *   x, r   DEVICE pointers to rows of D values of `type` (strides ldx, ldr)
+ *   h      DEVICE pointer receiving h (stride ldh), or NULL; it may be x or r
+ *          itself with the same stride, but must not partially overlap them
+ *   w      DEVICE pointer, D floats
+ *   y8, ys as in b200q_quantize_q8; they must not overlap x, r, h, w or each other
+ *   eps    >= 0 and finite
+ * S = 0 is a no-op.  Asynchronous on `stream`; one launch, no workspace.
+ */
+int b200q_rmsnorm_q8(const void *x, const void *r, void *h, int type, long long ldx, long long ldr, long long ldh,
+                     const float *w, void *y8, long long ld8, float *ys, int S, int D, float eps, void *stream);
+
+/*
+ * Matrix product of 8-bit rows with an epilogue:
+ *     y[s,o] = act(scale[o] * xs[s] * sum_i deq(W[o,i]) * x8[s,i] + bias[o]) + res[s,o]
+ *   t      int8, int4 or int2 tensor with per-row scales (B200Q_EINVAL for
+ *          f32 tensors and group-wise scales)
+ *   x8     DEVICE pointer, S rows of I E4M3 bytes as b200q_quantize_q8 writes
+ *          them (16-byte aligned, ld8 a multiple of 16)
+ *   xs     DEVICE pointer to S floats, the rows' scales
+ *   bias   DEVICE pointer to O floats, or NULL
+ *   act    B200Q_ACT_*
+ *   res    DEVICE pointer, S rows of O values of `type` (stride ldr), or NULL;
+ *          it may be y itself with the same stride (a residual stream updated
+ *          in place), but must not partially overlap y
+ *   y      DEVICE pointer, S rows of O values of `type` (stride ldy), written whole
+ * y must not overlap x8, xs or bias.  Numerics: the codes are exact E4M3
+ * values (int8 as 16 * high + low), so every product is exact; sums are f32;
+ * the epilogue is f32 and rounds once to `type`.  f32 results are within
+ * 1e-5 * scale * xs * sum |deq * x8| of the exact sum before the activation.
+ * S = 0 is a no-op.  Asynchronous on `stream`.
+ */
+int b200q_matmul_q8(const b200q_tensor *t, const void *x8, long long ld8, const float *xs, const float *bias, int act,
+                    const void *res, long long ldr, void *y, int type, long long ldy, int S, void *stream);
+
+/*
+ * Gated pair on 8-bit rows: both projections, the activation and their
+ * product in one call that reads x8 once,
+ *     y[s,f] = act(g) * u,   g = scale_g[f] xs[s] sum_i deq(Wg[f,i]) x8[s,i] + bias_g[f],  u likewise
+ * tg and tu have one format and one shape; bias_g and bias_u may be NULL (each
+ * by itself).  The other rules and the numerics are b200q_matmul_q8's.
+ */
+int b200q_glu_q8(const b200q_tensor *tg, const b200q_tensor *tu, const void *x8, long long ld8, const float *xs,
+                 const float *bias_g, const float *bias_u, int act, void *y, int type, long long ldy, int S,
+                 void *stream);
+
+/*
  * Self test of the bounded waits: one kernel waits, at most wait_us
  * microseconds (1 .. 10^6), on an mbarrier that nothing arrives on, gives up
  * and records B200Q_ETIMEOUT the way a kernel whose copies never land does.

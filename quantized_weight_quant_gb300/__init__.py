@@ -19,6 +19,9 @@ F32, I8, I4, I2 = 0, 1, 2, 3
 OK, EINVAL, ENOMEM, ECUDA, ETIMEOUT = 0, -1, -2, -3, -4
 PATH_AUTO, PATH_F32, PATH_TC, PATH_TCX, PATH_TCS = 0, 1, 2, 3, 4
 GROUP_MAX = 16
+T_F32, T_F16, T_BF16 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
 FORMATS = {"f32": F32, "i8": I8, "i4": I4, "i2": I2}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -67,6 +70,14 @@ def _load():
     L.b200q_mla_absorb.restype = ci
     L.b200q_kv_append.argtypes = [vp, vp, ci, ci, ci, vp, vp, ci, vp]
     L.b200q_kv_append.restype = ci
+    L.b200q_quantize_q8.argtypes = [vp, ci, cll, vp, cll, vp, ci, ci, vp]
+    L.b200q_quantize_q8.restype = ci
+    L.b200q_rmsnorm_q8.argtypes = [vp, vp, vp, ci, cll, cll, cll, vp, vp, cll, vp, ci, ci, cf, vp]
+    L.b200q_rmsnorm_q8.restype = ci
+    L.b200q_matmul_q8.argtypes = [vp, vp, cll, vp, vp, ci, vp, cll, vp, ci, cll, ci, vp]
+    L.b200q_matmul_q8.restype = ci
+    L.b200q_glu_q8.argtypes = [vp, vp, vp, cll, vp, vp, vp, ci, vp, ci, cll, ci, vp]
+    L.b200q_glu_q8.restype = ci
     L.b200q_selftest_timeout.argtypes = [ci, vp]
     L.b200q_selftest_timeout.restype = ci
     L.b200q_silu_mul.argtypes = [vp, vp, vp, cl, vp]
@@ -292,6 +303,97 @@ def rmsnorm(x, w, y, S: int, D: int, eps: float, r=None, h=None, stream=None) ->
     """y = (x + r) * w / sqrt(mean((x + r)^2) + eps) per row; h receives x + r
     when given (b200q_rmsnorm)."""
     _check(lib.b200q_rmsnorm(_dptr(x), _dptr(r), _dptr(h), _dptr(w), _dptr(y), S, D, eps, _stream(stream)))
+
+
+class Q8Rows:
+    """S activation rows of D values in 8 bits, on the device: `codes`, uint8
+    [S, ld] E4M3 bytes (ld: D rounded up to 16; bytes past D are unused), and
+    `scales`, f32 [S].  A row stands for codes * scale."""
+
+    def __init__(self, S: int, D: int, device="cuda"):
+        import torch
+        self.S, self.D = S, D
+        self.codes = torch.empty((S, -(-D // 16) * 16), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((S,), dtype=torch.float32, device=device)
+
+    def values(self):
+        """The codes as E4M3 numbers, float8_e4m3fn [S, D] (a view)."""
+        import torch
+        return self.codes[:, :self.D].view(torch.float8_e4m3fn)
+
+
+def _wide(a, S: int, D: int, name: str, type_=None):
+    """(pointer, element type, row stride) of a wide operand: a CUDA tensor
+    [S or more, D] of float32 / float16 / bfloat16 with unit column stride."""
+    import torch
+    if not isinstance(a, torch.Tensor):
+        raise TypeError("%s: expected a torch CUDA tensor" % name)
+    if not a.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor, got a %s tensor" % (name, a.device))
+    t = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}.get(a.dtype)
+    if t is None or (type_ is not None and t != type_):
+        raise ValueError("%s: element type %s not taken here" % (name, a.dtype))
+    if a.dim() != 2 or a.shape[0] < S or a.shape[1] != D:
+        raise ValueError("%s: expected [%d, %d], got %s" % (name, S, D, list(a.shape)))
+    if D > 1 and a.stride(1) != 1:
+        raise ValueError("%s: columns must be contiguous" % name)
+    return a.data_ptr(), t, (a.stride(0) if a.shape[0] > 1 else max(a.stride(0), D))
+
+
+def _q8(a, S: int, D: int):
+    """(codes pointer, row stride, scales pointer) of a Q8Rows."""
+    import torch
+    c, s = a.codes, a.scales
+    if not (c.is_cuda and s.is_cuda) or c.dtype != torch.uint8 or s.dtype != torch.float32:
+        raise ValueError("8-bit rows: expected CUDA uint8 codes and float32 scales")
+    if c.dim() != 2 or c.shape[0] < S or c.shape[1] < D or c.stride(1) != 1 or a.D != D:
+        raise ValueError("8-bit rows: expected %d rows of %d columns" % (S, D))
+    if s.dim() != 1 or s.shape[0] < S or not s.is_contiguous():
+        raise ValueError("8-bit rows: expected %d contiguous scales" % S)
+    return c.data_ptr(), (c.stride(0) if c.shape[0] > 1 else max(c.stride(0), c.shape[1])), s.data_ptr()
+
+
+def _vec(a, n: int, name: str) -> int:
+    if a is not None and getattr(a, "numel", lambda: n)() < n:
+        raise ValueError("%s: expected %d floats" % (name, n))
+    return _dptr(a)
+
+
+def quantize_q8(x, out, S: int, D: int, stream=None) -> None:
+    """Rows of x ([S, D], any row stride) to 8 bits: out is a Q8Rows
+    (b200q_quantize_q8)."""
+    xp, t, ldx = _wide(x, S, D, "x")
+    cp, ld8, sp = _q8(out, S, D)
+    _check(lib.b200q_quantize_q8(xp, t, ldx, cp, ld8, sp, S, D, _stream(stream)))
+
+
+def rmsnorm_q8(x, w, out, S: int, D: int, eps: float, r=None, h=None, stream=None) -> None:
+    """out = the 8-bit rows of (x + r) * w / sqrt(mean((x + r)^2) + eps); h
+    receives x + r when given (b200q_rmsnorm_q8)."""
+    xp, t, ldx = _wide(x, S, D, "x")
+    rp, _, ldr = _wide(r, S, D, "r", t) if r is not None else (0, t, 0)
+    hp, _, ldh = _wide(h, S, D, "h", t) if h is not None else (0, t, 0)
+    cp, ld8, sp = _q8(out, S, D)
+    _check(lib.b200q_rmsnorm_q8(xp, rp, hp, t, ldx, ldr, ldh, _vec(w, D, "w"), cp, ld8, sp, S, D, eps,
+                                _stream(stream)))
+
+
+def matmul_q8(t, xq, y, S: int, bias=None, act: int = ACT_NONE, res=None, stream=None) -> None:
+    """y = act(t . xq + bias) + res on 8-bit rows (b200q_matmul_q8).  xq: a
+    Q8Rows; y and res: [S, O] float32 / float16 / bfloat16, any row stride."""
+    cp, ld8, sp = _q8(xq, S, t.I)
+    yp, ty, ldy = _wide(y, S, t.O, "y")
+    rp, _, ldr = _wide(res, S, t.O, "res", ty) if res is not None else (0, ty, 0)
+    _check(lib.b200q_matmul_q8(_h(t), cp, ld8, sp, _vec(bias, t.O, "bias"), act, rp, ldr, yp, ty, ldy, S,
+                               _stream(stream)))
+
+
+def glu_q8(tg, tu, xq, y, S: int, act: int = ACT_SILU, bias_g=None, bias_u=None, stream=None) -> None:
+    """y = act(tg . xq + bias_g) * (tu . xq + bias_u) on 8-bit rows (b200q_glu_q8)."""
+    cp, ld8, sp = _q8(xq, S, tg.I)
+    yp, ty, ldy = _wide(y, S, tg.O, "y")
+    _check(lib.b200q_glu_q8(_h(tg), _h(tu), cp, ld8, sp, _vec(bias_g, tg.O, "bias_g"), _vec(bias_u, tg.O, "bias_u"),
+                            act, yp, ty, ldy, S, _stream(stream)))
 
 
 def selftest_timeout(wait_us: int, stream=None) -> None:

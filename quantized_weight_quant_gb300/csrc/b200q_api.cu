@@ -737,6 +737,175 @@ int b200q_kv_append(float *const *lat_pages, float *const *rope_pages, int K, in
 
 }  // extern "C"
 
+namespace {
+
+int type_bytes(int type) { return type == B200Q_T_F32 ? 4 : type == B200Q_T_F16 || type == B200Q_T_BF16 ? 2 : 0; }
+
+// Rows in device memory: S rows of `row` bytes, `ld` bytes apart.
+struct Rows {
+    const char *p;
+    size_t row, ld;
+};
+
+Rows rows_of(const void *p, long long n, long long ld, int bytes) {
+    return Rows{(const char *)p, (size_t)n * bytes, (size_t)ld * bytes};
+}
+
+// Whether two sets of S rows share a byte.  Column slices of one buffer (one
+// stride, disjoint columns) do not.
+bool rows_overlap(const Rows &a, const Rows &b, int S) {
+    if (!overlap(a.p, (size_t)(S - 1) * a.ld + a.row, b.p, (size_t)(S - 1) * b.ld + b.row)) return false;
+    if (a.ld != b.ld || S == 1) return true;
+    const Rows &lo = a.p <= b.p ? a : b, &hi = a.p <= b.p ? b : a;
+    const size_t d = (size_t)(hi.p - lo.p) % a.ld;
+    return d < lo.row || d + hi.row > a.ld;
+}
+
+Rows vec_rows(const void *p, size_t bytes) { return Rows{(const char *)p, bytes, bytes}; }
+
+bool overlaps_vec(const Rows &a, int S, const void *p, size_t bytes) {
+    return p && overlap(a.p, (size_t)(S - 1) * a.ld + a.row, p, bytes);
+}
+
+// A wide operand: type-aligned, rows at least n values apart, within 2^62 bytes.
+int check_rows(const void *p, long long n, long long ld, int type, int S, const char *name, const char *who) {
+    const int b = type_bytes(type);
+    if (!p) return fail(B200Q_EINVAL, "%s: %s must not be NULL", who, name);
+    if ((uintptr_t)p % b) return fail(B200Q_EINVAL, "%s: %s must be aligned to its type (%d bytes)", who, name, b);
+    if (ld < n) return fail(B200Q_EINVAL, "%s: the row stride of %s is %lld, below its %lld columns", who, name, ld, n);
+    if (ld > (1ll << 60) / S) return fail(B200Q_EINVAL, "%s: %s spans too much memory", who, name);
+    return B200Q_OK;
+}
+
+int check_q8(const void *c, long long ld8, const void *sc, long long n, int S, const char *who) {
+    if (!c || !sc) return fail(B200Q_EINVAL, "%s: the 8-bit rows and their scales must not be NULL", who);
+    if (!aligned16(c) || ld8 % 16)
+        return fail(B200Q_EINVAL, "%s: 8-bit rows must be 16-byte aligned, their stride a multiple of 16 (got %lld)",
+                    who, ld8);
+    if ((uintptr_t)sc % 4) return fail(B200Q_EINVAL, "%s: the row scales must be 4-byte aligned", who);
+    if (ld8 < n) return fail(B200Q_EINVAL, "%s: the 8-bit rows are %lld bytes apart, below their %lld columns", who, ld8, n);
+    if (ld8 > (1ll << 60) / S) return fail(B200Q_EINVAL, "%s: the 8-bit rows span too much memory", who);
+    return B200Q_OK;
+}
+
+int run_rows_q8(const RowsQ8 &a, void *stream, const char *who) {
+    if (a.S < 0 || a.D < 1) return fail(B200Q_EINVAL, "%s: need S >= 0 and D >= 1 (got S=%d, D=%d)", who, a.S, a.D);
+    if (!type_bytes(a.type)) return fail(B200Q_EINVAL, "%s: unknown element type %d", who, a.type);
+    if (!(a.eps >= 0.f) || a.eps > 3.0e38f) return fail(B200Q_EINVAL, "%s: eps must be finite and >= 0", who);
+    if (a.S == 0) return B200Q_OK;
+    const int b = type_bytes(a.type);
+    int rc = check_rows(a.x, a.D, a.ldx, a.type, a.S, "x", who);
+    if (!rc && a.r) rc = check_rows(a.r, a.D, a.ldr, a.type, a.S, "r", who);
+    if (!rc && a.h) rc = check_rows(a.h, a.D, a.ldh, a.type, a.S, "h", who);
+    if (!rc) rc = check_q8(a.y8, a.ld8, a.ys, a.D, a.S, who);
+    if (rc) return rc;
+    if (a.w && (uintptr_t)a.w % 4) return fail(B200Q_EINVAL, "%s: w must be 4-byte aligned", who);
+    const Rows x = rows_of(a.x, a.D, a.ldx, b), r = rows_of(a.r, a.D, a.ldr, b), h = rows_of(a.h, a.D, a.ldh, b);
+    const Rows y = rows_of(a.y8, a.D, a.ld8, 1), s = vec_rows(a.ys, (size_t)a.S * 4);
+    const size_t wb = (size_t)a.D * 4, sb = (size_t)a.S * 4;
+    if (rows_overlap(y, x, a.S) || (a.r && rows_overlap(y, r, a.S)) || (a.h && rows_overlap(y, h, a.S)) ||
+        overlaps_vec(y, a.S, a.w, wb) || overlaps_vec(y, a.S, a.ys, sb))
+        return fail(B200Q_EINVAL, "%s: the 8-bit rows must not overlap x, r, h, w or the scales", who);
+    if (overlaps_vec(x, a.S, a.ys, sb) || (a.r && overlaps_vec(r, a.S, a.ys, sb)) ||
+        (a.h && overlaps_vec(h, a.S, a.ys, sb)) || (a.w && overlap(s.p, sb, a.w, wb)))
+        return fail(B200Q_EINVAL, "%s: the scales must not overlap x, r, h or w", who);
+    if (a.h) {
+        const bool hx = a.h == a.x && (a.ldh == a.ldx || a.S == 1), hr = a.h == a.r && (a.ldh == a.ldr || a.S == 1);
+        if ((!hx && rows_overlap(h, x, a.S)) || (a.r && !hr && rows_overlap(h, r, a.S)) ||
+            overlaps_vec(h, a.S, a.w, wb))
+            return fail(B200Q_EINVAL, "%s: h may be x or r (same stride) but must not partially overlap them, or w", who);
+    }
+    cudaError_t e = launch_rows_q8(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return B200Q_OK;
+}
+
+int check_q8_tensor(const b200q_tensor *h, const char *who) {
+    int rc = check_tensor(h, who);
+    if (rc) return rc;
+    const Tensor &t = *reinterpret_cast<const Tensor *>(h);
+    if (t.fmt == B200Q_F32) return fail(B200Q_EINVAL, "%s: takes int8, int4 and int2 tensors only", who);
+    if (t.gs) return fail(B200Q_EINVAL, "%s: takes tensors with per-row scales only", who);
+    return B200Q_OK;
+}
+
+int run_mat_q8(const MatQ8 &a, void *stream, const char *who) {
+    const Tensor &t = *a.tg;
+    if (a.tu && (a.tu->fmt != t.fmt || a.tu->O != t.O || a.tu->I != t.I))
+        return fail(B200Q_EINVAL, "%s: gate and up differ in format or shape", who);
+    if (a.S < 0) return fail(B200Q_EINVAL, "%s: S must be >= 0 (got %d)", who, a.S);
+    if (!type_bytes(a.type)) return fail(B200Q_EINVAL, "%s: unknown element type %d", who, a.type);
+    if (a.act < B200Q_ACT_NONE || a.act > B200Q_ACT_SILU)
+        return fail(B200Q_EINVAL, "%s: unknown activation %d", who, a.act);
+    if (a.S == 0) return B200Q_OK;
+    const int b = type_bytes(a.type);
+    int rc = check_q8(a.x8, a.ld8, a.xs, t.I, a.S, who);
+    if (!rc) rc = check_rows(a.y, t.O, a.ldy, a.type, a.S, "y", who);
+    if (!rc && a.res) rc = check_rows(a.res, t.O, a.ldr, a.type, a.S, "res", who);
+    if (rc) return rc;
+    if ((uintptr_t)a.bias_g % 4 || (uintptr_t)a.bias_u % 4)
+        return fail(B200Q_EINVAL, "%s: the bias must be 4-byte aligned", who);
+    const Rows y = rows_of(a.y, t.O, a.ldy, b), x = rows_of(a.x8, t.I, a.ld8, 1), r = rows_of(a.res, t.O, a.ldr, b);
+    const size_t ob = (size_t)t.O * 4;
+    if (rows_overlap(y, x, a.S) || overlaps_vec(y, a.S, a.xs, (size_t)a.S * 4) || overlaps_vec(y, a.S, a.bias_g, ob) ||
+        overlaps_vec(y, a.S, a.bias_u, ob))
+        return fail(B200Q_EINVAL, "%s: y must not overlap the 8-bit rows, their scales or the bias", who);
+    if (a.res && !(a.res == a.y && (a.ldr == a.ldy || a.S == 1)) && rows_overlap(y, r, a.S))
+        return fail(B200Q_EINVAL, "%s: res may be y (same stride) but must not partially overlap it", who);
+    cudaError_t e = launch_mat_q8(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return B200Q_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int b200q_quantize_q8(const void *x, int type, long long ldx, void *y8, long long ld8, float *ys, int S, int D,
+                      void *stream) {
+    RowsQ8 a{};
+    a.x = x;
+    a.type = type;
+    a.ldx = ldx;
+    a.y8 = (uint8_t *)y8;
+    a.ld8 = ld8;
+    a.ys = ys;
+    a.S = S;
+    a.D = D;
+    return run_rows_q8(a, stream, "b200q_quantize_q8");
+}
+
+int b200q_rmsnorm_q8(const void *x, const void *r, void *h, int type, long long ldx, long long ldr, long long ldh,
+                     const float *w, void *y8, long long ld8, float *ys, int S, int D, float eps, void *stream) {
+    const char *who = "b200q_rmsnorm_q8";
+    if (S != 0 && !w) return fail(B200Q_EINVAL, "%s: w must not be NULL", who);
+    return run_rows_q8(RowsQ8{x, r, h, type, ldx, ldr, ldh, w, (uint8_t *)y8, ld8, ys, S, D, eps}, stream, who);
+}
+
+int b200q_matmul_q8(const b200q_tensor *t, const void *x8, long long ld8, const float *xs, const float *bias, int act,
+                    const void *res, long long ldr, void *y, int type, long long ldy, int S, void *stream) {
+    const char *who = "b200q_matmul_q8";
+    int rc = check_q8_tensor(t, who);
+    if (rc) return rc;
+    return run_mat_q8(MatQ8{reinterpret_cast<const Tensor *>(t), nullptr, (const uint8_t *)x8, ld8, xs, bias, nullptr,
+                            act, res, ldr, y, type, ldy, S},
+                      stream, who);
+}
+
+int b200q_glu_q8(const b200q_tensor *tg, const b200q_tensor *tu, const void *x8, long long ld8, const float *xs,
+                 const float *bias_g, const float *bias_u, int act, void *y, int type, long long ldy, int S,
+                 void *stream) {
+    const char *who = "b200q_glu_q8";
+    int rc = check_q8_tensor(tg, who);
+    if (!rc) rc = check_q8_tensor(tu, who);
+    if (rc) return rc;
+    return run_mat_q8(MatQ8{reinterpret_cast<const Tensor *>(tg), reinterpret_cast<const Tensor *>(tu),
+                            (const uint8_t *)x8, ld8, xs, bias_g, bias_u, act, nullptr, 0, y, type, ldy, S},
+                      stream, who);
+}
+
+}  // extern "C"
+
 extern "C" int b200q_selftest_timeout(int wait_us, void *stream) {
     if (wait_us < 1 || wait_us > 1000000)
         return fail(B200Q_EINVAL, "b200q_selftest_timeout: wait_us must be in [1, 1000000] (got %d)", wait_us);

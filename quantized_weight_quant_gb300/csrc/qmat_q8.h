@@ -1,0 +1,45 @@
+// Shared by the 8-bit matmul kernels: the epilogue and its element types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qwq_internal.h"
+
+namespace qwq {
+
+// v, activated.  f32 expf / tanhf / erff; for large |v| the exponentials
+// overflow or vanish to the activation's limits (silu(-inf side) -> -0).
+template <int ACT>
+__device__ __forceinline__ float act_q8(float v) {
+    if constexpr (ACT == B200Q_ACT_RELU) return v < 0.f ? 0.f : v;      // keeps a NaN
+    if constexpr (ACT == B200Q_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
+    if constexpr (ACT == B200Q_ACT_GELU_TANH)
+        return 0.5f * v * (1.f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
+    if constexpr (ACT == B200Q_ACT_SILU) return v / (1.f + expf(-v));
+    return v;
+}
+
+__device__ __forceinline__ float act_q8(float v, int act) {
+    switch (act) {
+    case B200Q_ACT_RELU: return act_q8<B200Q_ACT_RELU>(v);
+    case B200Q_ACT_GELU: return act_q8<B200Q_ACT_GELU>(v);
+    case B200Q_ACT_GELU_TANH: return act_q8<B200Q_ACT_GELU_TANH>(v);
+    case B200Q_ACT_SILU: return act_q8<B200Q_ACT_SILU>(v);
+    }
+    return v;
+}
+
+__device__ __forceinline__ float load_typed(const void *p, long long i, int type) {
+    if (type == B200Q_T_F32) return ((const float *)p)[i];
+    if (type == B200Q_T_F16) return __half2float(((const __half *)p)[i]);
+    return __bfloat162float(((const __nv_bfloat16 *)p)[i]);
+}
+
+__device__ __forceinline__ void store_typed(void *p, long long i, int type, float v) {
+    if (type == B200Q_T_F32) ((float *)p)[i] = v;
+    else if (type == B200Q_T_F16) ((__half *)p)[i] = __float2half_rn(v);
+    else ((__nv_bfloat16 *)p)[i] = __float2bfloat16_rn(v);
+}
+
+}  // namespace qwq

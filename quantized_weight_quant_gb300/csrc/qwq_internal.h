@@ -112,4 +112,38 @@ cudaError_t launch_silu_mul(const float *g, const float *u, float *h, long n, cu
 cudaError_t launch_rmsnorm(const float *x, const float *r, float *h, const float *w, float *y, int S, int D,
                            float eps, cudaStream_t st);
 
+// ---- 8-bit activations
+
+// RMSNorm (w != nullptr) or plain rows quantised to E4M3 with a scale per row.
+struct RowsQ8 {
+    const void *x, *r;
+    void *h;
+    int type;
+    long long ldx, ldr, ldh;   // values
+    const float *w;
+    uint8_t *y8;
+    long long ld8;             // bytes
+    float *ys;
+    int S, D;
+    float eps;
+};
+cudaError_t launch_rows_q8(const RowsQ8 &a, cudaStream_t st);
+
+// y = act(tg . x8) [+ res], or act(tg . x8) * (tu . x8) when tu is given.
+struct MatQ8 {
+    const Tensor *tg, *tu;
+    const uint8_t *x8;
+    long long ld8;
+    const float *xs;
+    const float *bias_g, *bias_u;
+    int act;
+    const void *res;
+    long long ldr;
+    void *y;
+    int type;
+    long long ldy;             // values
+    int S;
+};
+cudaError_t launch_mat_q8(const MatQ8 &a, cudaStream_t st);
+
 }  // namespace qwq
