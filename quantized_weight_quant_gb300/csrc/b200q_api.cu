@@ -27,6 +27,7 @@ cudaError_t launch_prefill_tc(const Tensor &t, const Tensor *tu, const float *x,
 cudaError_t decode_take_error(unsigned int *code);
 cudaError_t launch_tcs(const Tensor &t, const float *x, float *y, int S, cudaStream_t st, bool *handled);
 cudaError_t tcs_take_error(unsigned int *code);
+cudaError_t q8_take_error(unsigned int *code);
 size_t noalloc_capacity();
 cudaError_t launch_prefill_tc_noalloc(const Tensor &t, const float *x, float *y, int S, cudaStream_t st);
 cudaError_t prefill_take_error(unsigned int *code);
@@ -240,13 +241,14 @@ long long b200q_workspace_allocations(void) { return g_ws_allocs.load(std::memor
 int b200q_device_status(void) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "b200q_device_status");
-    unsigned int a = 0, b = 0, m = 0, c = 0;
+    unsigned int a = 0, b = 0, m = 0, c = 0, d = 0;
     e = decode_take_error(&a);
     if (e == cudaSuccess) e = prefill_take_error(&b);
     if (e == cudaSuccess) e = mla_take_error(&m);
     if (e == cudaSuccess) e = tcs_take_error(&c);
+    if (e == cudaSuccess) e = q8_take_error(&d);
     if (e != cudaSuccess) return cuda_fail(e, "b200q_device_status");
-    if (a || b || c || m == (unsigned)(-B200Q_ETIMEOUT))
+    if (a || b || c || d || m == (unsigned)(-B200Q_ETIMEOUT))
         return fail(B200Q_ETIMEOUT, "b200q_device_status: a kernel gave up on a bounded wait");
     if (m) return fail(B200Q_EINVAL, "b200q_device_status: an MLA call met a NULL or unaligned cache page");
     return B200Q_OK;
@@ -387,6 +389,7 @@ b200q_tensor *upload_impl(int fmt, int O, int I, int gs, const void *codes, cons
         e = cudaErrorNotSupported;
     if (e == cudaSuccess && !gemm_maps_encode(*t)) e = cudaErrorNotSupported;
     if (e == cudaSuccess && !tcs_map_encode(*t)) e = cudaErrorNotSupported;
+    if (e == cudaSuccess && !q8_map_encode(*t)) e = cudaErrorNotSupported;
     if (e != cudaSuccess) {
         cuda_fail(e, who);
         cudaGetLastError();

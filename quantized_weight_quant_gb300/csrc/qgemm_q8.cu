@@ -1,0 +1,630 @@
+// 8-bit rows on the fp8 tensor cores: matrix product and gated pair for more
+// rows than the few-row kernel takes.
+//     D[o, s] = sum_k A[o, k] B[s, k],  A = deq(W) as E4M3, B = the rows' bytes
+//     y[s, o] = act(scale[o] xs[s] D + bias[o]) + res[s, o],  or act(g) u
+//
+// Codes are exact in E4M3: int4 (-8..7) and int2 (-2..1) as one value, int8 as
+// the two values 16 * high (signed) and low (0..15), both times 2^-9 so that
+// the low field is its own E4M3 byte; B is read as it is.  Products are exact,
+// sums are the tensor cores' f32.
+//
+// Work is cut into (output tile, 128-column k-block) items, tile-major, and
+// every CTA takes one contiguous run of them (one CTA per SM), so that the
+// last wave is as full as the others.  A tile that one CTA holds whole goes
+// straight to y; a shared one is written as f32 planes (one per CTA), and the
+// CTA whose arrival completes the tile adds the planes in CTA order and runs
+// the epilogue.  No CTA waits for another, and the order of the additions does
+// not depend on the arrivals, so results repeat bit for bit.
+//
+// Warp roles:
+//   warp 0     TMA producer: per item the codes (two boxes of 64 rows) and N
+//              rows of x8 (128-byte swizzle), completion on an mbarrier;
+//   warp 1     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
+//              tensor memory, B from shared memory) into one of two
+//              accumulators;
+//   warps 2-9  dequantizers: codes -> E4M3 bytes by a 16-entry table lookup in
+//              registers (byte permutes), stored to a ring of A buffers in
+//              tensor memory, natural K order;
+//   warps 10-13 epilogue.
+// The gated pair takes 64 gate and 64 up rows per tile, interleaved by 16 in
+// the lanes, so that a gate and its up value sit in one warp, 16 lanes apart.
+// Every mbarrier wait is bounded; a wait that gives up records B200Q_ETIMEOUT,
+// raises the CTA's abort flag (which ends the other roles' waits), and the CTA
+// drains its copies and frees its tensor memory.
+#include <cuda.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "qmat_q8.h"
+
+namespace qwq {
+namespace {
+
+constexpr int BM = 128, BK = 128;
+constexpr int kMaxN = 192;                 // rows of x8 per tile
+constexpr int kDeqWarps = 8, kEpiWarps = 4;
+constexpr int kWEpi = 2 + kDeqWarps;
+constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
+constexpr int kTmemCols = 512, kAccBase = 128, kAccStride = kMaxN;   // A ring: columns 0..127
+constexpr int kSmemLimit = 232448;
+constexpr int kSmemFloor = 120 * 1024;      // one CTA per SM: it takes the whole tensor memory
+constexpr int kMiscBytes = 512;
+constexpr int kMaxStages = 12;
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+__device__ unsigned int g_q8_err = 0;
+
+// PIECES: E4M3 values per code.  CB: code bytes per row and k-block.
+template <int FMT> struct Fmt;
+template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128; };
+template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64; };
+template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32; };
+
+// ---------------------------------------------------------------- PTX helpers
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long global_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Waits for a phase; gives up after kWaitNs, or soon after another role has.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    unsigned long long t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if ((it & 63) == 63) {
+            if (*abort) return false;
+            if (t0 == 0) t0 = global_ns();
+            else if (global_ns() - t0 > kWaitNs) {
+                atomicExch(&g_q8_err, (unsigned)(-B200Q_ETIMEOUT));
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// Waits whether or not the CTA is winding down (copies and MMAs in flight must
+// finish before it leaves), for a quarter of kWaitNs at most.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_test(bar, parity) && global_ns() - t0 < kWaitNs / 4) {
+    }
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptor: K-major operand, 128-byte swizzle, rows of
+// 128 bytes, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// kind::f8f6f4: D f32, A and B E4M3 (format 0), both K-major, M = 128, N = n.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+__device__ __forceinline__ unsigned long long cas_acq_rel(unsigned long long *a, unsigned long long cmp,
+                                                          unsigned long long val) {
+    unsigned long long old;
+    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;" : "=l"(old) : "l"(a), "l"(cmp), "l"(val)
+                 : "memory");
+    return old;
+}
+
+// ---------------------------------------------------------------- codes -> E4M3
+// Four 4-bit fields (the low 16 bits of sel) through a 16-entry byte table:
+// entries 0-7 in (a0, a1), 8-15 in (b0, b1).  Two byte permutes on the fields'
+// low 3 bits; m, 0xFF where a field's top bit is set, picks between them.
+__device__ __forceinline__ uint32_t lut4(uint32_t sel7, uint32_t m, uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+    const uint32_t a = __byte_perm(a0, a1, sel7), b = __byte_perm(b0, b1, sel7);
+    return (a & ~m) | (b & m);
+}
+
+// prmt in its sign mode (selector bit 3): bytes of 0xFF or 0x00.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+// E4M3 bytes of 0..7 and of -8..-1.
+constexpr uint32_t kPos0 = 0x44403800u, kPos1 = 0x4E4C4A48u, kNeg0 = 0xCACCCED0u, kNeg1 = 0xB8C0C4C8u;
+
+// Eight nibbles of w -> the E4M3 bytes of code - 8, in nibble order.
+__device__ __forceinline__ void lut_i4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t s = w & 0x77777777u, w4 = w << 4;
+    lo = lut4(s, prmt(w4, w, 0xD9C8u), kNeg0, kNeg1, kPos0, kPos1);
+    hi = lut4(s >> 16, prmt(w4, w, 0xFBEAu), kNeg0, kNeg1, kPos0, kPos1);
+}
+
+// Sixteen 2-bit codes -> sixteen E4M3 bytes of code - 2.
+__device__ __forceinline__ void lut_i2(uint32_t w, uint32_t *o) {
+    constexpr uint32_t t = 0x3800B8C0u;      // -2, -1, 0, 1
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t x = h ? w >> 16 : w & 0xFFFFu;         // 8 codes, spread to one per nibble
+        x = (x | (x << 8)) & 0x00FF00FFu;
+        x = (x | (x << 4)) & 0x0F0F0F0Fu;
+        x = (x | (x << 2)) & 0x33333333u;
+        o[2 * h] = __byte_perm(t, 0u, x);
+        o[2 * h + 1] = __byte_perm(t, 0u, x >> 16);
+    }
+}
+
+// The 64 codes of half a row's k-block -> 16 registers per piece.
+template <int FMT>
+__device__ __forceinline__ void dequant(const uint8_t *c_s, int row, int half, uint32_t (&p0)[16], uint32_t (&p1)[16]) {
+    constexpr int CB = Fmt<FMT>::CB, kChunks = CB / 32;      // 16-byte chunks per half row
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        const int c = half * kChunks + j;
+        // the TMA swizzle of rows of CB bytes: chunk index xor bits of the row
+        const int pc = CB == 128 ? c ^ (row & 7) : CB == 64 ? c ^ ((row >> 1) & 3) : c ^ ((row >> 2) & 1);
+        const uint4 q = *reinterpret_cast<const uint4 *>(c_s + row * CB + pc * 16);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (FMT == B200Q_I4) {
+                lut_i4(w[k], p0[8 * j + 2 * k], p0[8 * j + 2 * k + 1]);
+            } else if constexpr (FMT == B200Q_I2) {
+                lut_i2(w[k], &p0[4 * k]);
+            } else {
+                // high nibbles: 16 h 2^-9 = h 2^-5 through the table; low nibbles: l 2^-9 is the byte l
+                const uint32_t h = (w[k] >> 4) & 0x0F0F0F0Fu, t = h | (h >> 4);
+                const uint32_t f = __byte_perm(t, 0u, 0x4420u);                    // four fields in 16 bits
+                const uint32_t f4 = f << 4;
+                const uint32_t m = prmt(f4, f, 0xD9C8u);
+                constexpr uint32_t d = 0x28282828u;
+                p0[4 * j + k] = lut4(f & 0x7777u, m, kPos0 - 0x28282800u, kPos1 - d, kNeg0 - d, kNeg1 - d);
+                p1[4 * j + k] = w[k] & 0x0F0F0F0Fu;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+struct Q8Params {
+    const float *scale_g, *scale_u, *bias_g, *bias_u, *xs;
+    const void *res;
+    void *y;
+    long long ldr, ldy;
+    float *planes;                 // [grid][2][N][128]
+    unsigned long long *cnt;       // [tiles] (token << 10) | arrivals
+    unsigned long long token;
+    int O, S, N, nk, n_tiles, act, type;
+    int stages;
+    long long items;               // tiles * nk
+};
+
+__device__ __forceinline__ long long run_start(const Q8Params &p, int c) { return (long long)c * p.items / gridDim.x; }
+__device__ __forceinline__ int owner_of(const Q8Params &p, long long i) {
+    return (int)(((i + 1) * gridDim.x - 1) / p.items);
+}
+
+template <int FMT, bool GLU>
+__global__ void __launch_bounds__(kThreads, 1)
+    qgemm_q8_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_u,
+                    const __grid_constant__ CUtensorMap map_x, const Q8Params p) {
+    constexpr int PIECES = Fmt<FMT>::PIECES, CB = Fmt<FMT>::CB, C_BYTES = BM * CB;
+    constexpr int kACols = 32 * PIECES, kNumA = kAccBase / kACols;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const int b_bytes = p.N * BK, kStages = p.stages;
+    uint8_t *b_s = smem;                                  // [stages][N][128], 128-byte swizzle
+    uint8_t *c_s = b_s + kStages * b_bytes;               // [stages][128][CB], CB-byte swizzle
+    uint64_t *bars = reinterpret_cast<uint64_t *>(c_s + kStages * C_BYTES);
+    uint64_t *full = bars, *empty = bars + kMaxStages;
+    uint64_t *a_full = empty + kMaxStages, *a_empty = a_full + 4;
+    uint64_t *acc_full = a_empty + 4, *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    volatile int *abort = reinterpret_cast<int *>(tmem_slot + 1);
+    volatile int *last_flag = abort + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long i0 = run_start(p, blockIdx.x), i1 = run_start(p, blockIdx.x + 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < kNumA; ++s) {
+            mbar_init(smem_u32(&a_full[s]), kDeqWarps);
+            mbar_init(smem_u32(&a_empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), kEpiWarps);
+        }
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------- TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            int tile = (int)(i0 / p.nk), kb = (int)(i0 % p.nk);
+            for (long long i = i0; i < i1; ++i) {
+                if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort)) break;
+                const uint32_t bar = smem_u32(&full[stage]);
+                const int mt = tile / p.n_tiles, n0 = (tile - mt * p.n_tiles) * p.N;
+                const uint32_t c_dst = smem_u32(c_s + stage * C_BYTES);
+                mbar_expect_tx(bar, (uint32_t)(C_BYTES + b_bytes));
+                const int r0 = GLU ? mt * 64 : mt * 128, r1 = GLU ? r0 : r0 + 64;
+                tma_load_2d(c_dst, &map_g, kb * CB, r0, bar);
+                tma_load_2d(c_dst + C_BYTES / 2, GLU ? &map_u : &map_g, kb * CB, r1, bar);
+                tma_load_2d(smem_u32(b_s + stage * b_bytes), &map_x, kb * BK, n0, bar);
+                ++issued;
+                if (++stage == kStages) stage = 0, phase ^= 1;
+                if (++kb == p.nk) kb = 0, ++tile;
+            }
+            // the last copies land before the CTA may leave (a completed phase returns at once)
+            for (long long k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
+                mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3(p.N);
+            int stage = 0, abuf = 0, t = 0;
+            uint32_t aphase = 0;
+            int kb = (int)(i0 % p.nk);
+            bool first = true, ok = true;
+            uint32_t d_tmem = 0;
+            for (long long i = i0; i < i1 && ok; ++i) {
+                if (first) {
+                    if (!mbar_wait(smem_u32(&acc_empty[t & 1]), ((t >> 1) & 1) ^ 1, abort)) break;
+                    tc_fence_after();
+                    d_tmem = tmem_base + kAccBase + (t & 1) * kAccStride;
+                }
+                // the dequantizers arrive only after the item's copies have landed
+                if (!mbar_wait(smem_u32(&a_full[abuf]), aphase, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a_tmem = tmem_base + abuf * kACols;
+                const uint32_t b_addr = smem_u32(b_s + stage * b_bytes);
+#pragma unroll
+                for (int k = 0; k < BK / 32; ++k)
+#pragma unroll
+                    for (int pc = 0; pc < PIECES; ++pc)
+                        mma_f8(d_tmem, a_tmem + 32 * pc + 8 * k, sw128_desc(b_addr + 32 * k), idesc,
+                               (first && k == 0 && pc == 0) ? 0u : 1u);
+                first = false;
+                mma_commit(smem_u32(&empty[stage]));
+                mma_commit(smem_u32(&a_empty[abuf]));
+                if (++stage == kStages) stage = 0;
+                if (++abuf == kNumA) abuf = 0, aphase ^= 1;
+                if (++kb == p.nk || i + 1 == i1) {
+                    mma_commit(smem_u32(&acc_full[t & 1]));
+                    kb = 0, ++t, first = true;
+                }
+            }
+            // MMAs issued before giving up must finish before tensor memory is freed
+            if (*abort) {
+                const int prev = abuf ? abuf - 1 : kNumA - 1;
+                mbar_drain(smem_u32(&a_empty[prev]), abuf ? aphase : aphase ^ 1);
+            }
+        }
+    } else if (warp < kWEpi) {
+        // ---------------- dequantizers: two warps per lane quarter, each half of the k-block
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        // shared-memory row of this thread's lane (the pair: 16 gate rows, then 16 up rows per quarter)
+        const int row = GLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 16;
+        int stage = 0, abuf = 0;
+        uint32_t phase = 0, aphase = 0;
+        for (long long i = i0; i < i1; ++i) {
+            if (!mbar_wait(smem_u32(&full[stage]), phase, abort)) break;
+            uint32_t v0[16], v1[16];
+            dequant<FMT>(c_s + stage * C_BYTES, row, half, v0, v1);
+            if (!mbar_wait(smem_u32(&a_empty[abuf]), aphase ^ 1, abort)) break;
+            tc_fence_after();
+            tmem_st16(tlane + abuf * kACols, v0);
+            if (PIECES == 2) tmem_st16(tlane + abuf * kACols + 32, v1);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&a_full[abuf]));
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (++abuf == kNumA) abuf = 0, aphase ^= 1;
+        }
+    } else {
+        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) ..
+        const int quarter = warp & 3;
+        const float unit = FMT == B200Q_I8 ? 512.f : 1.f;      // int8 values are times 2^-9
+        const bool up = GLU && lane >= 16;
+        int t = 0;
+        for (long long i = i0; i < i1; ++t) {
+            const int tile = (int)(i / p.nk);
+            const long long t0 = (long long)tile * p.nk, t1 = t0 + p.nk;
+            const long long end = t1 < i1 ? t1 : i1;
+            const bool whole = i == t0 && end == t1;
+            if (!mbar_wait(smem_u32(&acc_full[t & 1]), (t >> 1) & 1, abort)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase + (t & 1) * kAccStride;
+            const int mt = tile / p.n_tiles, n0 = (tile - mt * p.n_tiles) * p.N;
+            const int o = GLU ? mt * 64 + quarter * 16 + (lane & 15) : mt * 128 + quarter * 32 + lane;
+            bool emit = whole;
+            int first_c = 0, pieces = 0;
+            if (!whole) {
+                // this CTA's plane, then the tile's arrival count
+                float *pl = p.planes + ((long long)blockIdx.x * 2 + (i == i0 ? 0 : 1)) * p.N * BM + quarter * 32 + lane;
+                for (int c = 0; c < p.N; c += 16) {
+                    float v[16];
+                    tmem_ld16(taddr + c, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pl[(long long)(c + j) * BM] = v[j];
+                }
+                first_c = owner_of(p, t0);
+                pieces = owner_of(p, t1 - 1) - first_c + 1;
+                named_sync(1, kEpiWarps * 32);
+                if (threadIdx.x == kWEpi * 32) {
+                    const unsigned long long tag = p.token << 10;
+                    unsigned long long old = *(volatile unsigned long long *)&p.cnt[tile];
+                    int n;
+                    for (;;) {
+                        n = (old >> 10) == p.token ? (int)(old & 1023) + 1 : 1;
+                        const unsigned long long nv = n == pieces ? 0ull : tag | (unsigned)n;
+                        const unsigned long long prev = cas_acq_rel(&p.cnt[tile], old, nv);
+                        if (prev == old) break;
+                        old = prev;
+                    }
+                    *last_flag = n == pieces;
+                }
+                named_sync(1, kEpiWarps * 32);
+                emit = *last_flag != 0;
+                named_sync(1, kEpiWarps * 32);
+            }
+            if (emit) {
+                const bool live = o < p.O;
+                const float sc = live ? (up ? p.scale_u[o] : p.scale_g[o]) * unit : 0.f;
+                const float *bias = up ? p.bias_u : p.bias_g;
+                const float b = live && bias ? bias[o] : 0.f;
+                for (int c = 0; c < p.N; c += 16) {
+                    if (n0 + c >= p.S) break;
+                    float v[16];
+                    if (whole) {
+                        tmem_ld16(taddr + c, v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                        for (int z = 0; z < pieces; ++z) {
+                            const int cc = first_c + z;
+                            const int slot = run_start(p, cc) / p.nk == tile ? 0 : 1;
+                            const float *pl = p.planes + ((long long)cc * 2 + slot) * p.N * BM + quarter * 32 + lane;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] += __ldcg(pl + (long long)(c + j) * BM);
+                        }
+                    }
+                    const int s0 = n0 + c;
+                    if constexpr (GLU) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float xa = s0 + j < p.S ? p.xs[s0 + j] : 0.f, xb = s0 + j + 1 < p.S ? p.xs[s0 + j + 1] : 0.f;
+                            const float va = v[j] * xa * sc + b, vb = v[j + 1] * xb * sc + b;
+                            const float got = __shfl_xor_sync(0xffffffffu, up ? va : vb, 16);
+                            const float gt = up ? got : va, ut = up ? vb : got;
+                            const int s = s0 + j + (up ? 1 : 0);
+                            if (live && s < p.S) store_typed(p.y, s * p.ldy + o, p.type, act_q8(gt, p.act) * ut);
+                        }
+                    } else if (live) {
+                        float r[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            r[j] = p.res && s0 + j < p.S ? load_typed(p.res, (s0 + j) * p.ldr + o, p.type) : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (s0 + j < p.S) {
+                                const float a = act_q8(v[j] * p.xs[s0 + j] * sc + b, p.act);
+                                store_typed(p.y, (s0 + j) * p.ldy + o, p.type, p.res ? a + r[j] : a);
+                            }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[t & 1]));
+            i = end;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                     : "memory");
+}
+
+std::atomic<unsigned long long> g_token{0x51a9e8ull};
+
+template <int FMT, bool GLU>
+cudaError_t run(const MatQ8 &a, cudaStream_t st) {
+    constexpr int C_BYTES = BM * Fmt<FMT>::CB;
+    const Tensor &t = *a.tg;
+    // rows of x8 per tile: the fewest tiles of at most kMaxN rows, evenly filled
+    const int n_tiles = (a.S + kMaxN - 1) / kMaxN;
+    const int N = ((a.S + n_tiles - 1) / n_tiles + 15) / 16 * 16;
+    CUtensorMap map_x;
+    if (!tmap_encode_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x8, (uint64_t)t.I, (uint64_t)a.S, (uint64_t)a.ld8, BK,
+                        (uint32_t)N, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    Q8Params p{};
+    p.scale_g = t.scales;
+    p.scale_u = a.tu ? a.tu->scales : nullptr;
+    p.bias_g = a.bias_g;
+    p.bias_u = a.bias_u;
+    p.xs = a.xs;
+    p.res = a.res;
+    p.y = a.y;
+    p.ldr = a.ldr;
+    p.ldy = a.ldy;
+    p.O = t.O;
+    p.S = a.S;
+    p.N = N;
+    p.nk = (t.I + BK - 1) / BK;
+    p.n_tiles = (a.S + N - 1) / N;
+    p.act = a.act;
+    p.type = a.type;
+    const long long m_tiles = GLU ? (t.O + 63) / 64 : (t.O + 127) / 128;
+    const long long tiles = m_tiles * p.n_tiles;
+    if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
+    p.items = tiles * p.nk;
+    // at least four k-blocks per CTA
+    const int n_sms = sm_count(t.device);
+    long long grid = (p.items + 3) / 4;
+    if (grid > n_sms) grid = n_sms;
+    const int per = N * BK + C_BYTES;
+    int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
+    if (stages > kMaxStages) stages = kMaxStages;
+    p.stages = stages;
+    size_t smem = 1024 + (size_t)stages * per + kMiscBytes;
+    if (smem < kSmemFloor) smem = kSmemFloor;
+    cudaError_t e = allow_dynamic_smem((const void *)qgemm_q8_kernel<FMT, GLU>, kSmemLimit);
+    if (e != cudaSuccess) return e;
+    void *ws = nullptr;
+    const bool shared = p.items % grid != 0 || (p.items / grid) % p.nk != 0;   // some tile is cut
+    const size_t plane_bytes = (size_t)grid * 2 * N * BM * 4;
+    if (shared) {
+        e = workspace_alloc(&ws, plane_bytes + (size_t)tiles * 8, st);
+        if (e != cudaSuccess) return e;
+        p.planes = (float *)ws;
+        p.cnt = (unsigned long long *)((char *)ws + plane_bytes);
+        p.token = g_token.fetch_add(1, std::memory_order_relaxed) & ((1ull << 54) - 1);
+    }
+    qgemm_q8_kernel<FMT, GLU><<<(int)grid, kThreads, smem, st>>>(t.q8_map, a.tu ? a.tu->q8_map : t.q8_map, map_x, p);
+    count_launch();
+    e = cudaGetLastError();
+    if (ws) {
+        const cudaError_t ef = workspace_free(ws, st);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e;
+}
+
+}  // namespace
+
+// Codes as bytes [o_pad, ld], box 64 rows x one k-block, swizzled by the
+// box's width so that the dequantizers' 16-byte reads touch every bank once.
+bool q8_map_encode(Tensor &t) {
+    memset(&t.q8_map, 0, sizeof t.q8_map);
+    if (fmt_bits(t.fmt) == 0 || t.fmt == B200Q_F32) return true;
+    const uint32_t cb = t.fmt == B200Q_I8 ? 128 : t.fmt == B200Q_I4 ? 64 : 32;
+    return tmap_encode_2d(&t.q8_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.codes, (uint64_t)t.ld, (uint64_t)t.o_pad,
+                          (uint64_t)t.ld, cb, 64,
+                          cb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                          : cb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_32B);
+}
+
+cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st) {
+    switch (a.tg->fmt) {
+    case B200Q_I8: return a.tu ? run<B200Q_I8, true>(a, st) : run<B200Q_I8, false>(a, st);
+    case B200Q_I4: return a.tu ? run<B200Q_I4, true>(a, st) : run<B200Q_I4, false>(a, st);
+    case B200Q_I2: return a.tu ? run<B200Q_I2, true>(a, st) : run<B200Q_I2, false>(a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t q8_take_error(unsigned int *code) {
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_q8_err, sizeof(unsigned int));
+    if (e == cudaSuccess && *code) e = cudaMemcpyToSymbol(g_q8_err, &zero, sizeof(unsigned int));
+    return e;
+}
+
+}  // namespace qwq

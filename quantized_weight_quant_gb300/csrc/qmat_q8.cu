@@ -88,6 +88,7 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_mat_q8(const MatQ8 &a, cudaStream_t st) {
+    if (a.S > 8) return launch_gemm_q8(a, st);
     switch (a.tg->fmt) {
     case B200Q_I8: return run<B200Q_I8>(a, st);
     case B200Q_I4: return run<B200Q_I4>(a, st);

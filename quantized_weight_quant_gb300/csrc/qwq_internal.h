@@ -25,6 +25,8 @@ struct Tensor {
     CUtensorMap gemm_sc_map;  // group scales as f32 [o_pad, G_ld], box 128 rows x 4 (tensor-core GEMM)
     CUtensorMap tcs_map;      // int8 / int4 / int2 codes as bytes [o_pad, ld], box 128 rows x 128 bytes,
                               // 128-byte swizzle (f32-accurate tensor-core path for few tokens)
+    CUtensorMap q8_map;       // int8 / int4 / int2 codes as bytes [o_pad, ld], box 64 rows x 128 codes, swizzled by
+                              // the box's width (8-bit activation GEMM)
     int fmt;
     int O, I;
     int device;
@@ -102,6 +104,9 @@ bool gemm_maps_encode(Tensor &t);
 // Encodes Tensor::tcs_map (int8 / int4 / int2 tensors; others need none).
 bool tcs_map_encode(Tensor &t);
 
+// Encodes Tensor::q8_map (int8 / int4 / int2 tensors; others need none).
+bool q8_map_encode(Tensor &t);
+
 // f32-accurate SIMT path, any format, any S.  With tu != nullptr the launch
 // also computes yu = matmul(tu, x) (gate/up pair, same shape as t).
 cudaError_t launch_qmv_simt(const Tensor &t, const Tensor *tu, const float *x, float *y,
@@ -145,5 +150,8 @@ struct MatQ8 {
     int S;
 };
 cudaError_t launch_mat_q8(const MatQ8 &a, cudaStream_t st);
+
+// The tensor-core kernel behind it, any S.
+cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st);
 
 }  // namespace qwq
