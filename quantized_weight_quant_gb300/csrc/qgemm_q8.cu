@@ -17,15 +17,18 @@
 // not depend on the arrivals, so results repeat bit for bit.
 //
 // Warp roles:
-//   warp 0     TMA producer: per item the codes (two boxes of 64 rows) and N
-//              rows of x8 (128-byte swizzle), completion on an mbarrier;
-//   warp 1     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
+//   warps 0-2  TMA producers, one thread each: N rows of x8, and the two boxes
+//              of 64 code rows (128-byte swizzle for x8; a TMA takes its
+//              thread ~160 cycles and an mbarrier test ~290, so one thread
+//              for all three copies of an item would be slower than its MMAs);
+//   warp 3     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
 //              tensor memory, B from shared memory) into one of two
-//              accumulators;
-//   warps 2-9  dequantizers: codes -> E4M3 bytes by a 16-entry table lookup in
-//              registers (byte permutes), stored to a ring of A buffers in
-//              tensor memory, natural K order;
-//   warps 10-13 epilogue.
+//              accumulators; one commit per item frees both its stage and its
+//              A buffer;
+//   warps 4 .. dequantizers, in groups of four: codes -> E4M3 bytes by a
+//              16-entry table lookup in registers (byte permutes), stored to
+//              the group's A buffer in tensor memory, natural K order;
+//   last four  epilogue.
 // The gated pair takes 64 gate and 64 up rows per tile, interleaved by 16 in
 // the lanes, so that a gate and its up value sit in one warp, 16 lanes apart.
 // Every mbarrier wait is bounded; a wait that gives up records B200Q_ETIMEOUT,
@@ -43,23 +46,28 @@ namespace {
 
 constexpr int BM = 128, BK = 128;
 constexpr int kMaxN = 192;                 // rows of x8 per tile
-constexpr int kDeqWarps = 8, kEpiWarps = 4;
-constexpr int kWEpi = 2 + kDeqWarps;
-constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
+constexpr int kProducers = 3, kWMma = 3, kWDeq = 4;
+constexpr int kEpiWarps = 4;
 constexpr int kTmemCols = 512, kAccBase = 128, kAccStride = kMaxN;   // A ring: columns 0..127
 constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 120 * 1024;      // one CTA per SM: it takes the whole tensor memory
-constexpr int kMiscBytes = 512;
+constexpr int kMiscBytes = 512 + 2 * kMaxN * 4;   // barriers and counters, row scales of two tiles
 constexpr int kMaxStages = 12;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 __device__ unsigned int g_q8_err = 0;
 
 // PIECES: E4M3 values per code.  CB: code bytes per row and k-block.
+// GROUPS: A buffers, and groups of four dequantizing warps (one per tensor-
+// memory lane quarter); group g fills buffer g with every GROUPS-th item.
 template <int FMT> struct Fmt;
-template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128; };
-template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64; };
-template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32; };
+template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128, GROUPS = 2; };
+template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 4; };
+template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 4; };
+template <int FMT> struct Roles {
+    static constexpr int kWEpi = kWDeq + 4 * Fmt<FMT>::GROUPS;
+    static constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
+};
 
 // ---------------------------------------------------------------- PTX helpers
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -180,7 +188,47 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Counters in shared memory for the hand-offs that no copy and no commit is
+// part of: release on the add, acquire on the read, CTA scope.  (A test of an
+// mbarrier takes several hundred cycles here even when its phase is complete.)
+__device__ __forceinline__ void cnt_add(uint32_t addr) {
+    asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cnt_read(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ bool cnt_wait(uint32_t addr, uint32_t want, volatile int *abort) {
+    unsigned long long t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if ((int)(cnt_read(addr) - want) >= 0) return true;
+        if ((it & 255) == 255) {
+            if (*abort) return false;
+            if (t0 == 0) t0 = global_ns();
+            else if (global_ns() - t0 > kWaitNs) {
+                atomicExch(&g_q8_err, (unsigned)(-B200Q_ETIMEOUT));
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// A named barrier that also ORs a predicate over its threads.
+__device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
 
 __device__ __forceinline__ unsigned long long cas_acq_rel(unsigned long long *a, unsigned long long cmp,
                                                           unsigned long long val) {
@@ -280,22 +328,103 @@ __device__ __forceinline__ int owner_of(const Q8Params &p, long long i) {
     return (int)(((i + 1) * gridDim.x - 1) / p.items);
 }
 
+template <class T> __device__ __forceinline__ float widen(T v);
+template <> __device__ __forceinline__ float widen<float>(float v) { return v; }
+template <> __device__ __forceinline__ float widen<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T narrow(float v);
+template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Eight values from v[OFF] on: v += res, then y, for tokens s0, s0 + step, ...
+// below s0 + left; the loads before the stores.
+template <class T, int OFF>
+__device__ __forceinline__ void put8(const Q8Params &p, float (&v)[16], long long s0, int step, int left, int o) {
+    if (p.res) {
+        const T *r = (const T *)p.res + s0 * p.ldr + o;
+        const long long d = step * p.ldr;
+        T rv[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k, r += d)
+            if (step * k < left) rv[k] = *r;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (step * k < left) v[OFF + k] += widen<T>(rv[k]);
+    }
+    T *y = (T *)p.y + s0 * p.ldy + o;
+    const long long d = step * p.ldy;
+#pragma unroll
+    for (int k = 0; k < 8; ++k, y += d)
+        if (step * k < left) *y = narrow<T>(v[OFF + k]);
+}
+
+template <class T, bool GLU>
+__device__ __forceinline__ void put(const Q8Params &p, float (&v)[16], int s0, int left, int o) {
+    put8<T, 0>(p, v, s0, GLU ? 2 : 1, left, o);
+    if (!GLU) put8<T, 8>(p, v, s0 + 8, 1, left - 8, o);
+}
+
+// 16 accumulator columns (tokens s0 ..; left: how many exist) of this lane's
+// row -> y.  The pair: lanes 0-15 hold gate rows, lanes 16-31 the up rows of
+// the same outputs; of two neighbouring columns the lower lane finishes the
+// first and the upper lane the second, one shuffle for both.
+template <bool GLU>
+__device__ __forceinline__ void finish16(const Q8Params &p, float (&v)[16], const float *xs, float sc, float b, int s0,
+                                         int left, int o, bool live, bool up) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(xs + j);
+        v[j] = fmaf(v[j], x.x * sc, b);
+        v[j + 1] = fmaf(v[j + 1], x.y * sc, b);
+        v[j + 2] = fmaf(v[j + 2], x.z * sc, b);
+        v[j + 3] = fmaf(v[j + 3], x.w * sc, b);
+    }
+    constexpr int K = GLU ? 8 : 16;
+    float u[K];
+    if constexpr (GLU) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * j] : v[2 * j + 1], 16);
+            u[j] = up ? v[2 * j + 1] : got;
+            v[j] = up ? got : v[2 * j];
+        }
+        s0 += up, left -= up;
+    }
+    switch (p.act) {
+    case B200Q_ACT_RELU: act_n<B200Q_ACT_RELU, K>(v); break;
+    case B200Q_ACT_GELU: act_n<B200Q_ACT_GELU, K>(v); break;
+    case B200Q_ACT_GELU_TANH: act_n<B200Q_ACT_GELU_TANH, K>(v); break;
+    case B200Q_ACT_SILU: act_n<B200Q_ACT_SILU, K>(v); break;
+    }
+    if constexpr (GLU) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) v[j] *= u[j];
+    }
+    if (!live) return;
+    if (p.type == B200Q_T_F32) put<float, GLU>(p, v, s0, left, o);
+    else if (p.type == B200Q_T_F16) put<__half, GLU>(p, v, s0, left, o);
+    else put<__nv_bfloat16, GLU>(p, v, s0, left, o);
+}
+
 template <int FMT, bool GLU>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     qgemm_q8_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_u,
                     const __grid_constant__ CUtensorMap map_x, const Q8Params p) {
     constexpr int PIECES = Fmt<FMT>::PIECES, CB = Fmt<FMT>::CB, C_BYTES = BM * CB;
-    constexpr int kACols = 32 * PIECES, kNumA = kAccBase / kACols;
+    constexpr int kACols = 32 * PIECES, kNumA = Fmt<FMT>::GROUPS, kWEpi = Roles<FMT>::kWEpi;
+    static_assert(kACols * kNumA <= kAccBase, "A ring");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int b_bytes = p.N * BK, kStages = p.stages;
     uint8_t *b_s = smem;                                  // [stages][N][128], 128-byte swizzle
     uint8_t *c_s = b_s + kStages * b_bytes;               // [stages][128][CB], CB-byte swizzle
-    uint64_t *bars = reinterpret_cast<uint64_t *>(c_s + kStages * C_BYTES);
-    uint64_t *full = bars, *empty = bars + kMaxStages;
-    uint64_t *a_full = empty + kMaxStages, *a_empty = a_full + 4;
-    uint64_t *acc_full = a_empty + 4, *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    float *xs_s = reinterpret_cast<float *>(c_s + kStages * C_BYTES);      // [2][kMaxN] row scales of a tile
+    uint64_t *bars = reinterpret_cast<uint64_t *>(xs_s + 2 * kMaxN);
+    uint64_t *full = bars, *done = bars + kMaxStages;      // per stage: copies landed; MMAs finished
+    uint64_t *acc_full = done + kMaxStages, *acc_empty = acc_full + 2;
+    uint32_t *a_ready = reinterpret_cast<uint32_t *>(acc_empty + 2);       // [4] warps that have filled A buffer g, counted on
+    uint32_t *tmem_slot = a_ready + 4;
     volatile int *abort = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *last_flag = abort + 1;
 
@@ -304,13 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&full[s]), kProducers);
+            mbar_init(smem_u32(&done[s]), 1);
         }
-        for (int s = 0; s < kNumA; ++s) {
-            mbar_init(smem_u32(&a_full[s]), kDeqWarps);
-            mbar_init(smem_u32(&a_empty[s]), 1);
-        }
+        for (int s = 0; s < kNumA; ++s) a_ready[s] = 0;
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
             mbar_init(smem_u32(&acc_empty[b]), kEpiWarps);
@@ -318,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
+    if (warp == kWMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
@@ -329,23 +455,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    if (warp == 0) {
-        // ---------------- TMA producer
+    if (warp < kProducers) {
+        // ---------------- TMA producers: warp 0 the rows of x8, warps 1 and 2 a box of codes each
         if (lane == 0) {
+            const uint32_t bytes = warp == 0 ? (uint32_t)b_bytes : (uint32_t)(C_BYTES / 2);
+            const CUtensorMap *map = warp == 0 ? &map_x : GLU && warp == 2 ? &map_u : &map_g;
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
             int tile = (int)(i0 / p.nk), kb = (int)(i0 % p.nk);
             for (long long i = i0; i < i1; ++i) {
-                if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort)) break;
+                if (!mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort)) break;
                 const uint32_t bar = smem_u32(&full[stage]);
                 const int mt = tile / p.n_tiles, n0 = (tile - mt * p.n_tiles) * p.N;
-                const uint32_t c_dst = smem_u32(c_s + stage * C_BYTES);
-                mbar_expect_tx(bar, (uint32_t)(C_BYTES + b_bytes));
-                const int r0 = GLU ? mt * 64 : mt * 128, r1 = GLU ? r0 : r0 + 64;
-                tma_load_2d(c_dst, &map_g, kb * CB, r0, bar);
-                tma_load_2d(c_dst + C_BYTES / 2, GLU ? &map_u : &map_g, kb * CB, r1, bar);
-                tma_load_2d(smem_u32(b_s + stage * b_bytes), &map_x, kb * BK, n0, bar);
+                mbar_expect_tx(bar, bytes);
+                if (warp == 0)
+                    tma_load_2d(smem_u32(b_s + stage * b_bytes), map, kb * BK, n0, bar);
+                else
+                    tma_load_2d(smem_u32(c_s + stage * C_BYTES + (warp - 1) * (C_BYTES / 2)), map, kb * CB,
+                                GLU ? mt * 64 : mt * 128 + (warp - 1) * 64, bar);
                 ++issued;
                 if (++stage == kStages) stage = 0, phase ^= 1;
                 if (++kb == p.nk) kb = 0, ++tile;
@@ -354,29 +482,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (long long k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
                 mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
         }
-    } else if (warp == 1) {
+    } else if (warp == kWMma) {
         // ---------------- MMA issuer
         if (lane == 0) {
             const uint32_t idesc = idesc_e4m3(p.N);
             int stage = 0, abuf = 0, t = 0;
-            uint32_t aphase = 0;
+            uint32_t phase = 0, ready = 4;
             int kb = (int)(i0 % p.nk);
-            bool first = true, ok = true;
+            bool first = true;
             uint32_t d_tmem = 0;
-            for (long long i = i0; i < i1 && ok; ++i) {
+            uint32_t seen = cnt_read(smem_u32(&a_ready[0]));
+            for (long long i = i0; i < i1; ++i) {
                 if (first) {
                     if (!mbar_wait(smem_u32(&acc_empty[t & 1]), ((t >> 1) & 1) ^ 1, abort)) break;
-                    tc_fence_after();
                     d_tmem = tmem_base + kAccBase + (t & 1) * kAccStride;
                 }
                 // the dequantizers arrive only after the item's copies have landed
-                if (!mbar_wait(smem_u32(&a_full[abuf]), aphase, abort)) {
-                    ok = false;
-                    break;
-                }
+                if ((int)(seen - ready) < 0 && !cnt_wait(smem_u32(&a_ready[abuf]), ready, abort)) break;
                 tc_fence_after();
                 const uint32_t a_tmem = tmem_base + abuf * kACols;
                 const uint32_t b_addr = smem_u32(b_s + stage * b_bytes);
+                if (++abuf == kNumA) abuf = 0, ready += 4;
+                seen = cnt_read(smem_u32(&a_ready[abuf]));      // the next item's, its latency under these MMAs
 #pragma unroll
                 for (int k = 0; k < BK / 32; ++k)
 #pragma unroll
@@ -384,47 +511,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_f8(d_tmem, a_tmem + 32 * pc + 8 * k, sw128_desc(b_addr + 32 * k), idesc,
                                (first && k == 0 && pc == 0) ? 0u : 1u);
                 first = false;
-                mma_commit(smem_u32(&empty[stage]));
-                mma_commit(smem_u32(&a_empty[abuf]));
-                if (++stage == kStages) stage = 0;
-                if (++abuf == kNumA) abuf = 0, aphase ^= 1;
+                mma_commit(smem_u32(&done[stage]));
+                if (++stage == kStages) stage = 0, phase ^= 1;
                 if (++kb == p.nk || i + 1 == i1) {
                     mma_commit(smem_u32(&acc_full[t & 1]));
                     kb = 0, ++t, first = true;
                 }
             }
             // MMAs issued before giving up must finish before tensor memory is freed
-            if (*abort) {
-                const int prev = abuf ? abuf - 1 : kNumA - 1;
-                mbar_drain(smem_u32(&a_empty[prev]), abuf ? aphase : aphase ^ 1);
-            }
+            if (*abort) mbar_drain(smem_u32(&done[stage ? stage - 1 : kStages - 1]), stage ? phase : phase ^ 1);
         }
     } else if (warp < kWEpi) {
-        // ---------------- dequantizers: two warps per lane quarter, each half of the k-block
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        // ---------------- dequantizers: group g, items g, g + GROUPS, ..., one thread per row
+        const int quarter = warp & 3, g = (warp - kWDeq) >> 2;
         // shared-memory row of this thread's lane (the pair: 16 gate rows, then 16 up rows per quarter)
         const int row = GLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
-        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 16;
-        int stage = 0, abuf = 0;
-        uint32_t phase = 0, aphase = 0;
-        for (long long i = i0; i < i1; ++i) {
+        const uint32_t tdst = tmem_base + ((uint32_t)(quarter * 32) << 16) + g * kACols;
+        int stage = g, fstage = 0;                 // the item's stage; the stage of the buffer's previous item
+        uint32_t phase = 0, fphase = 0;
+        for (long long i = i0 + g; i < i1; i += kNumA) {
             if (!mbar_wait(smem_u32(&full[stage]), phase, abort)) break;
             uint32_t v0[16], v1[16];
-            dequant<FMT>(c_s + stage * C_BYTES, row, half, v0, v1);
-            if (!mbar_wait(smem_u32(&a_empty[abuf]), aphase ^ 1, abort)) break;
+            dequant<FMT>(c_s + stage * C_BYTES, row, 0, v0, v1);
+            // the buffer is free when the MMAs of its previous item have finished (the barrier cannot
+            // run a phase ahead: that takes this item, as kStages >= kNumA)
+            if (i >= i0 + kNumA && !mbar_wait(smem_u32(&done[fstage]), fphase, abort)) break;
             tc_fence_after();
-            tmem_st16(tlane + abuf * kACols, v0);
-            if (PIECES == 2) tmem_st16(tlane + abuf * kACols + 32, v1);
+            tmem_st16(tdst, v0);
+            if (PIECES == 2) tmem_st16(tdst + 32, v1);
+            dequant<FMT>(c_s + stage * C_BYTES, row, 1, v0, v1);
+            tmem_st16(tdst + 16, v0);
+            if (PIECES == 2) tmem_st16(tdst + 48, v1);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&a_full[abuf]));
-            if (++stage == kStages) stage = 0, phase ^= 1;
-            if (++abuf == kNumA) abuf = 0, aphase ^= 1;
+            if (lane == 0) cnt_add(smem_u32(&a_ready[g]));
+            fstage = stage, fphase = phase;
+            stage += kNumA;
+            if (stage >= kStages) stage -= kStages, phase ^= 1;
         }
     } else {
         // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) ..
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, et = threadIdx.x - kWEpi * 32;
         const float unit = FMT == B200Q_I8 ? 512.f : 1.f;      // int8 values are times 2^-9
         const bool up = GLU && lane >= 16;
         int t = 0;
@@ -433,11 +561,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long t0 = (long long)tile * p.nk, t1 = t0 + p.nk;
             const long long end = t1 < i1 ? t1 : i1;
             const bool whole = i == t0 && end == t1;
-            if (!mbar_wait(smem_u32(&acc_full[t & 1]), (t >> 1) & 1, abort)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase + (t & 1) * kAccStride;
             const int mt = tile / p.n_tiles, n0 = (tile - mt * p.n_tiles) * p.N;
             const int o = GLU ? mt * 64 + quarter * 16 + (lane & 15) : mt * 128 + quarter * 32 + lane;
+            const bool live = o < p.O;
+            // the tile's scales and bias, while its MMAs run
+            float *xs = xs_s + (t & 1) * kMaxN;
+            for (int c = et; c < p.N; c += kEpiWarps * 32) xs[c] = n0 + c < p.S ? p.xs[n0 + c] : 0.f;
+            const float sc = live ? (up ? p.scale_u[o] : p.scale_g[o]) * unit : 0.f;
+            const float *bias = up ? p.bias_u : p.bias_g;
+            const float b = live && bias ? bias[o] : 0.f;
+            // one decision for the four warps, and xs is written
+            if (named_sync_or(1, kEpiWarps * 32, !mbar_wait(smem_u32(&acc_full[t & 1]), (t >> 1) & 1, abort))) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase + (t & 1) * kAccStride;
             bool emit = whole;
             int first_c = 0, pieces = 0;
             if (!whole) {
@@ -447,12 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float v[16];
                     tmem_ld16(taddr + c, v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pl[(long long)(c + j) * BM] = v[j];
+                    for (int j = 0; j < 16; ++j) pl[(c + j) * BM] = v[j];
                 }
                 first_c = owner_of(p, t0);
                 pieces = owner_of(p, t1 - 1) - first_c + 1;
                 named_sync(1, kEpiWarps * 32);
-                if (threadIdx.x == kWEpi * 32) {
+                if (et == 0) {
                     const unsigned long long tag = p.token << 10;
                     unsigned long long old = *(volatile unsigned long long *)&p.cnt[tile];
                     int n;
@@ -467,15 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 named_sync(1, kEpiWarps * 32);
                 emit = *last_flag != 0;
-                named_sync(1, kEpiWarps * 32);
             }
             if (emit) {
-                const bool live = o < p.O;
-                const float sc = live ? (up ? p.scale_u[o] : p.scale_g[o]) * unit : 0.f;
-                const float *bias = up ? p.bias_u : p.bias_g;
-                const float b = live && bias ? bias[o] : 0.f;
-                for (int c = 0; c < p.N; c += 16) {
-                    if (n0 + c >= p.S) break;
+                const int ns = p.S - n0 < p.N ? p.S - n0 : p.N;      // rows of x8 in this tile
+                for (int c = 0; c < ns; c += 16) {
                     float v[16];
                     if (whole) {
                         tmem_ld16(taddr + c, v);
@@ -485,34 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int z = 0; z < pieces; ++z) {
                             const int cc = first_c + z;
                             const int slot = run_start(p, cc) / p.nk == tile ? 0 : 1;
-                            const float *pl = p.planes + ((long long)cc * 2 + slot) * p.N * BM + quarter * 32 + lane;
+                            const float *pl = p.planes + (((long long)cc * 2 + slot) * p.N + c) * BM + quarter * 32 + lane;
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] += __ldcg(pl + (long long)(c + j) * BM);
+                            for (int j = 0; j < 16; ++j) v[j] += __ldcg(pl + j * BM);
                         }
                     }
-                    const int s0 = n0 + c;
-                    if constexpr (GLU) {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float xa = s0 + j < p.S ? p.xs[s0 + j] : 0.f, xb = s0 + j + 1 < p.S ? p.xs[s0 + j + 1] : 0.f;
-                            const float va = v[j] * xa * sc + b, vb = v[j + 1] * xb * sc + b;
-                            const float got = __shfl_xor_sync(0xffffffffu, up ? va : vb, 16);
-                            const float gt = up ? got : va, ut = up ? vb : got;
-                            const int s = s0 + j + (up ? 1 : 0);
-                            if (live && s < p.S) store_typed(p.y, s * p.ldy + o, p.type, act_q8(gt, p.act) * ut);
-                        }
-                    } else if (live) {
-                        float r[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            r[j] = p.res && s0 + j < p.S ? load_typed(p.res, (s0 + j) * p.ldr + o, p.type) : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (s0 + j < p.S) {
-                                const float a = act_q8(v[j] * p.xs[s0 + j] * sc + b, p.act);
-                                store_typed(p.y, (s0 + j) * p.ldy + o, p.type, p.res ? a + r[j] : a);
-                            }
-                    }
+                    finish16<GLU>(p, v, xs + c, sc, b, n0 + c, ns - c, o, live, up);
                 }
             }
             tc_fence_before();
@@ -525,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1)
+    if (warp == kWMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
                      : "memory");
 }
@@ -586,7 +695,7 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
         p.cnt = (unsigned long long *)((char *)ws + plane_bytes);
         p.token = g_token.fetch_add(1, std::memory_order_relaxed) & ((1ull << 54) - 1);
     }
-    qgemm_q8_kernel<FMT, GLU><<<(int)grid, kThreads, smem, st>>>(t.q8_map, a.tu ? a.tu->q8_map : t.q8_map, map_x, p);
+    qgemm_q8_kernel<FMT, GLU><<<(int)grid, Roles<FMT>::kThreads, smem, st>>>(t.q8_map, a.tu ? a.tu->q8_map : t.q8_map, map_x, p);
     count_launch();
     e = cudaGetLastError();
     if (ws) {

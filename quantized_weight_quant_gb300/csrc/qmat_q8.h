@@ -9,15 +9,23 @@
 namespace qwq {
 
 // v, activated.  f32 expf / tanhf / erff; for large |v| the exponentials
-// overflow or vanish to the activation's limits (silu(-inf side) -> -0).
+// overflow or vanish to the activation's limits.  __fdividef (2 ulp) gives 0
+// where silu's denominator passes 2^126, v < -87, where silu is below 1e-36.
 template <int ACT>
 __device__ __forceinline__ float act_q8(float v) {
     if constexpr (ACT == B200Q_ACT_RELU) return v < 0.f ? 0.f : v;      // keeps a NaN
     if constexpr (ACT == B200Q_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
     if constexpr (ACT == B200Q_ACT_GELU_TANH)
         return 0.5f * v * (1.f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
-    if constexpr (ACT == B200Q_ACT_SILU) return v / (1.f + expf(-v));
+    if constexpr (ACT == B200Q_ACT_SILU) return __fdividef(v, 1.f + expf(-v));
     return v;
+}
+
+// The first K of v.
+template <int ACT, int K, int N>
+__device__ __forceinline__ void act_n(float (&v)[N]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = act_q8<ACT>(v[k]);
 }
 
 __device__ __forceinline__ float act_q8(float v, int act) {
