@@ -125,6 +125,13 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     }
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     volatile int *abort = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *last_flag = abort + 1;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: uniform
     const long long i0 = run_start(p, blockIdx.x), i1 = run_start(p, blockIdx.x + 1);
 
     if (threadIdx.x == 0) {
@@ -453,74 +460,83 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp < kProducers) {
-        // ---------------- TMA producers: warp 0 the rows of x8, warps 1 and 2 a box of codes each
-        if (lane == 0) {
-            const uint32_t bytes = warp == 0 ? (uint32_t)b_bytes : (uint32_t)(C_BYTES / 2);
-            const CUtensorMap *map = warp == 0 ? &map_x : GLU && warp == 2 ? &map_u : &map_g;
-            int stage = 0;
-            uint32_t phase = 0;
-            long long issued = 0;
-            int tile = (int)(i0 / p.nk), kb = (int)(i0 % p.nk);
-            for (long long i = i0; i < i1; ++i) {
-                if (!mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort)) break;
-                const uint32_t bar = smem_u32(&full[stage]);
-                const int mt = tile / p.n_tiles, n0 = (tile - mt * p.n_tiles) * p.N;
+        // ---------------- TMA producers: warp 0 the rows of x8, warps 1 and 2 a box of codes each.
+        // The whole warp walks the items (so that addresses stay in uniform registers), one lane issues.
+        const bool leader = elect_one();
+        const uint32_t bytes = warp == 0 ? (uint32_t)b_bytes : (uint32_t)(C_BYTES / 2);
+        const CUtensorMap *map = warp == 0 ? &map_x : GLU && warp == 2 ? &map_u : &map_g;
+        const uint32_t dst0 = warp == 0 ? smem_u32(b_s) : smem_u32(c_s + (warp - 1) * (C_BYTES / 2));
+        const uint32_t step = warp == 0 ? (uint32_t)b_bytes : (uint32_t)C_BYTES;
+        const int kcols = warp == 0 ? BK : CB;
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        int tile = (int)(i0 / p.nk), kb = (int)(i0 % p.nk);
+        int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+        const int n = (int)(i1 - i0);
+        for (int i = 0; i < n; ++i) {
+            if (!mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort)) break;
+            const uint32_t bar = smem_u32(&full[stage]);
+            const int row = warp == 0 ? nt * p.N : GLU ? mt * 64 : mt * 128 + (warp - 1) * 64;
+            if (leader) {
                 mbar_expect_tx(bar, bytes);
-                if (warp == 0)
-                    tma_load_2d(smem_u32(b_s + stage * b_bytes), map, kb * BK, n0, bar);
-                else
-                    tma_load_2d(smem_u32(c_s + stage * C_BYTES + (warp - 1) * (C_BYTES / 2)), map, kb * CB,
-                                GLU ? mt * 64 : mt * 128 + (warp - 1) * 64, bar);
-                ++issued;
-                if (++stage == kStages) stage = 0, phase ^= 1;
-                if (++kb == p.nk) kb = 0, ++tile;
+                tma_load_2d(dst0 + stage * step, map, kb * kcols, row, bar);
             }
-            // the last copies land before the CTA may leave (a completed phase returns at once)
-            for (long long k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
-                mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
+            ++issued;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (++kb == p.nk) {
+                kb = 0;
+                if (++nt == p.n_tiles) nt = 0, ++mt;
+            }
         }
+        __syncwarp();
+        // the last copies land before the CTA may leave (a completed phase returns at once)
+        for (int k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
+            mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
     } else if (warp == kWMma) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3(p.N);
-            int stage = 0, abuf = 0, t = 0;
-            uint32_t phase = 0, ready = 4;
-            int kb = (int)(i0 % p.nk);
-            bool first = true;
-            uint32_t d_tmem = 0;
-            uint32_t seen = cnt_read(smem_u32(&a_ready[0]));
-            for (long long i = i0; i < i1; ++i) {
-                if (first) {
-                    if (!mbar_wait(smem_u32(&acc_empty[t & 1]), ((t >> 1) & 1) ^ 1, abort)) break;
-                    d_tmem = tmem_base + kAccBase + (t & 1) * kAccStride;
-                }
-                // the dequantizers arrive only after the item's copies have landed
-                if ((int)(seen - ready) < 0 && !cnt_wait(smem_u32(&a_ready[abuf]), ready, abort)) break;
-                tc_fence_after();
-                const uint32_t a_tmem = tmem_base + abuf * kACols;
-                const uint32_t b_addr = smem_u32(b_s + stage * b_bytes);
-                if (++abuf == kNumA) abuf = 0, ready += 4;
-                seen = cnt_read(smem_u32(&a_ready[abuf]));      // the next item's, its latency under these MMAs
+        // ---------------- MMA issuer: the whole warp walks the items, one lane issues
+        const bool leader = elect_one();
+        const uint32_t idesc = idesc_e4m3(p.N);
+        const uint64_t desc0 = sw128_desc(smem_u32(b_s));
+        int stage = 0, abuf = 0, t = 0;
+        uint32_t phase = 0, ready = 4;
+        int kb = (int)(i0 % p.nk);
+        bool first = true;
+        uint32_t d_tmem = 0;
+        uint32_t seen = cnt_read(smem_u32(&a_ready[0]));
+        const int n = (int)(i1 - i0);
+        for (int i = 0; i < n; ++i) {
+            if (first) {
+                if (!mbar_wait(smem_u32(&acc_empty[t & 1]), ((t >> 1) & 1) ^ 1, abort)) break;
+                d_tmem = tmem_base + kAccBase + (t & 1) * kAccStride;
+            }
+            // the dequantizers arrive only after the item's copies have landed
+            if ((int)(seen - ready) < 0 && !cnt_wait(smem_u32(&a_ready[abuf]), ready, abort)) break;
+            tc_fence_after();
+            const uint32_t a_tmem = tmem_base + abuf * kACols;
+            const uint64_t desc = desc0 + (uint64_t)((stage * b_bytes) >> 4);
+            if (++abuf == kNumA) abuf = 0, ready += 4;
+            seen = cnt_read(smem_u32(&a_ready[abuf]));      // the next item's, its latency under these MMAs
+            const bool last = ++kb == p.nk || i + 1 == n;
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < BK / 32; ++k)
 #pragma unroll
                     for (int pc = 0; pc < PIECES; ++pc)
-                        mma_f8(d_tmem, a_tmem + 32 * pc + 8 * k, sw128_desc(b_addr + 32 * k), idesc,
+                        mma_f8(d_tmem, a_tmem + 32 * pc + 8 * k, desc + 2 * k, idesc,
                                (first && k == 0 && pc == 0) ? 0u : 1u);
-                first = false;
                 mma_commit(smem_u32(&done[stage]));
-                if (++stage == kStages) stage = 0, phase ^= 1;
-                if (++kb == p.nk || i + 1 == i1) {
-                    mma_commit(smem_u32(&acc_full[t & 1]));
-                    kb = 0, ++t, first = true;
-                }
+                if (last) mma_commit(smem_u32(&acc_full[t & 1]));
             }
-            // MMAs issued before giving up must finish before tensor memory is freed
-            if (*abort) mbar_drain(smem_u32(&done[stage ? stage - 1 : kStages - 1]), stage ? phase : phase ^ 1);
+            first = last;
+            if (last) kb = 0, ++t;
+            if (++stage == kStages) stage = 0, phase ^= 1;
         }
+        __syncwarp();
+        // MMAs issued before giving up must finish before tensor memory is freed
+        if (*abort) mbar_drain(smem_u32(&done[stage ? stage - 1 : kStages - 1]), stage ? phase : phase ^ 1);
     } else if (warp < kWEpi) {
         // ---------------- dequantizers: group g, items g, g + GROUPS, ..., one thread per row
         const int quarter = warp & 3, g = (warp - kWDeq) >> 2;
