@@ -308,7 +308,8 @@ def rmsnorm(x, w, y, S: int, D: int, eps: float, r=None, h=None, stream=None) ->
 class Q8Rows:
     """S activation rows of D values in 8 bits, on the device: `codes`, uint8
     [S, ld] E4M3 bytes (ld: D rounded up to 16; bytes past D are unused), and
-    `scales`, f32 [S].  A row stands for codes * scale."""
+    `scales`, f32 [S].  A row stands for codes * scale.  Both may be replaced
+    by tensors of the caller's (views of larger buffers, say)."""
 
     def __init__(self, S: int, D: int, device="cuda"):
         import torch
@@ -316,47 +317,85 @@ class Q8Rows:
         self.codes = torch.empty((S, -(-D // 16) * 16), dtype=torch.uint8, device=device)
         self.scales = torch.empty((S,), dtype=torch.float32, device=device)
 
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, c):
+        import torch
+        if c.dtype != torch.uint8 or c.dim() != 2 or c.shape[1] < self.D or (c.shape[1] > 1 and c.stride(1) != 1):
+            raise ValueError("8-bit rows: expected uint8 codes [rows, %d or more] with contiguous columns" % self.D)
+        self._codes, self._values = c, c[:, :self.D].view(torch.float8_e4m3fn)
+        self._rows, self._cp = (c.shape[0] if c.is_cuda else -1), c.data_ptr()
+        self._ld = c.stride(0) if c.shape[0] > 1 else max(c.stride(0), c.shape[1])
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @scales.setter
+    def scales(self, s):
+        import torch
+        if s.dtype != torch.float32 or s.dim() != 1 or not s.is_contiguous():
+            raise ValueError("8-bit rows: expected contiguous float32 scales [rows]")
+        self._scales, self._sp, self._srows = s, s.data_ptr(), (s.shape[0] if s.is_cuda else -1)
+
     def values(self):
         """The codes as E4M3 numbers, float8_e4m3fn [S, D] (a view)."""
-        import torch
-        return self.codes[:, :self.D].view(torch.float8_e4m3fn)
+        return self._values
+
+
+_WIDE = None
 
 
 def _wide(a, S: int, D: int, name: str, type_=None):
     """(pointer, element type, row stride) of a wide operand: a CUDA tensor
     [S or more, D] of float32 / float16 / bfloat16 with unit column stride."""
-    import torch
-    if not isinstance(a, torch.Tensor):
+    global _WIDE
+    if _WIDE is None:
+        import torch
+        _WIDE = (torch.Tensor, {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16})
+    if not isinstance(a, _WIDE[0]):
         raise TypeError("%s: expected a torch CUDA tensor" % name)
     if not a.is_cuda:
         raise ValueError("%s: expected a CUDA tensor, got a %s tensor" % (name, a.device))
-    t = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}.get(a.dtype)
+    t = _WIDE[1].get(a.dtype)
     if t is None or (type_ is not None and t != type_):
         raise ValueError("%s: element type %s not taken here" % (name, a.dtype))
-    if a.dim() != 2 or a.shape[0] < S or a.shape[1] != D:
-        raise ValueError("%s: expected [%d, %d], got %s" % (name, S, D, list(a.shape)))
-    if D > 1 and a.stride(1) != 1:
+    shape, stride = a.shape, a.stride()
+    if len(shape) != 2 or shape[0] < S or shape[1] != D:
+        raise ValueError("%s: expected [%d, %d], got %s" % (name, S, D, list(shape)))
+    if D > 1 and stride[1] != 1:
         raise ValueError("%s: columns must be contiguous" % name)
-    return a.data_ptr(), t, (a.stride(0) if a.shape[0] > 1 else max(a.stride(0), D))
+    return a.data_ptr(), t, (stride[0] if shape[0] > 1 else max(stride[0], D))
 
 
 def _q8(a, S: int, D: int):
     """(codes pointer, row stride, scales pointer) of a Q8Rows."""
-    import torch
-    c, s = a.codes, a.scales
-    if not (c.is_cuda and s.is_cuda) or c.dtype != torch.uint8 or s.dtype != torch.float32:
-        raise ValueError("8-bit rows: expected CUDA uint8 codes and float32 scales")
-    if c.dim() != 2 or c.shape[0] < S or c.shape[1] < D or c.stride(1) != 1 or a.D != D:
-        raise ValueError("8-bit rows: expected %d rows of %d columns" % (S, D))
-    if s.dim() != 1 or s.shape[0] < S or not s.is_contiguous():
-        raise ValueError("8-bit rows: expected %d contiguous scales" % S)
-    return c.data_ptr(), (c.stride(0) if c.shape[0] > 1 else max(c.stride(0), c.shape[1])), s.data_ptr()
+    if not isinstance(a, Q8Rows):
+        raise TypeError("8-bit rows: expected a Q8Rows")
+    if a.D != D or a._rows < S or a._srows < S:
+        raise ValueError("8-bit rows: expected %d CUDA rows of %d columns" % (S, D))
+    return a._cp, a._ld, a._sp
 
 
 def _vec(a, n: int, name: str) -> int:
-    if a is not None and getattr(a, "numel", lambda: n)() < n:
+    if a is None:
+        return 0
+    if not isinstance(a, int) and a.numel() < n:
         raise ValueError("%s: expected %d floats" % (name, n))
     return _dptr(a)
+
+
+def _raw_stream(stream) -> int:
+    """_stream, without building a torch stream object for the default."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
+    return _stream(stream)
 
 
 def quantize_q8(x, out, S: int, D: int, stream=None) -> None:
@@ -364,7 +403,7 @@ def quantize_q8(x, out, S: int, D: int, stream=None) -> None:
     (b200q_quantize_q8)."""
     xp, t, ldx = _wide(x, S, D, "x")
     cp, ld8, sp = _q8(out, S, D)
-    _check(lib.b200q_quantize_q8(xp, t, ldx, cp, ld8, sp, S, D, _stream(stream)))
+    _check(lib.b200q_quantize_q8(xp, t, ldx, cp, ld8, sp, S, D, _raw_stream(stream)))
 
 
 def rmsnorm_q8(x, w, out, S: int, D: int, eps: float, r=None, h=None, stream=None) -> None:
@@ -375,7 +414,7 @@ def rmsnorm_q8(x, w, out, S: int, D: int, eps: float, r=None, h=None, stream=Non
     hp, _, ldh = _wide(h, S, D, "h", t) if h is not None else (0, t, 0)
     cp, ld8, sp = _q8(out, S, D)
     _check(lib.b200q_rmsnorm_q8(xp, rp, hp, t, ldx, ldr, ldh, _vec(w, D, "w"), cp, ld8, sp, S, D, eps,
-                                _stream(stream)))
+                                _raw_stream(stream)))
 
 
 def matmul_q8(t, xq, y, S: int, bias=None, act: int = ACT_NONE, res=None, stream=None) -> None:
@@ -385,7 +424,7 @@ def matmul_q8(t, xq, y, S: int, bias=None, act: int = ACT_NONE, res=None, stream
     yp, ty, ldy = _wide(y, S, t.O, "y")
     rp, _, ldr = _wide(res, S, t.O, "res", ty) if res is not None else (0, ty, 0)
     _check(lib.b200q_matmul_q8(_h(t), cp, ld8, sp, _vec(bias, t.O, "bias"), act, rp, ldr, yp, ty, ldy, S,
-                               _stream(stream)))
+                               _raw_stream(stream)))
 
 
 def glu_q8(tg, tu, xq, y, S: int, act: int = ACT_SILU, bias_g=None, bias_u=None, stream=None) -> None:
@@ -393,7 +432,7 @@ def glu_q8(tg, tu, xq, y, S: int, act: int = ACT_SILU, bias_g=None, bias_u=None,
     cp, ld8, sp = _q8(xq, S, tg.I)
     yp, ty, ldy = _wide(y, S, tg.O, "y")
     _check(lib.b200q_glu_q8(_h(tg), _h(tu), cp, ld8, sp, _vec(bias_g, tg.O, "bias_g"), _vec(bias_u, tg.O, "bias_u"),
-                            act, yp, ty, ldy, S, _stream(stream)))
+                            act, yp, ty, ldy, S, _raw_stream(stream)))
 
 
 def selftest_timeout(wait_us: int, stream=None) -> None:
