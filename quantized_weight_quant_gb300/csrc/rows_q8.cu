@@ -33,24 +33,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// A 16-byte vector of T as floats, and back.
+// 16 bytes of T, and as floats.
 template <class T> constexpr int kVec = 16 / (int)sizeof(T);
+template <class T> union Vec {
+    uint4 q;
+    T e[kVec<T>];
+    __device__ __forceinline__ float at(int j) const { return to_f<T>(e[j]); }
+};
 
-template <class T>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[kVec<T>]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const T *e = reinterpret_cast<const T *>(&a);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) v[j] = to_f<T>(e[j]);
-}
-
-template <class T>
-__device__ __forceinline__ void store_vec(T *p, const float (&v)[kVec<T>]) {
-    uint4 a;
-    T *e = reinterpret_cast<T *>(&a);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) e[j] = from_f<T>(v[j]);
-    *reinterpret_cast<uint4 *>(p) = a;
+// v / d, correctly rounded, for a divisor that many values share: with
+// rd = 1 / d rounded, q = v rd and one correction by the exact remainder
+// (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  v / d itself, with its own reciprocal for
+// every value, made these kernels arithmetic-bound.
+__device__ __forceinline__ float div_by(float v, float d, float rd) {
+    const float q = v * rd;
+    return fmaf(fmaf(-q, d, v), rd, q);
 }
 
 // Sum and maximum over the block.
@@ -76,108 +74,177 @@ __device__ __forceinline__ void block_reduce(float &ss, unsigned &m) {
     }
 }
 
-// The row's root (1 for plain rows) and scale from the two reductions.
-__device__ __forceinline__ void row_scale(const RowsQ8 &a, float ss, unsigned m, float &root, float &s) {
-    root = a.w ? sqrtf(ss / (float)a.D + a.eps) : 1.f;
-    const float top = __uint_as_float(m) / root / kMax8;
-    s = top < kMinScale ? kMinScale : top;                     // a NaN stays
+// A plain row's scale from its largest magnitude.
+__device__ __forceinline__ float plain_scale(unsigned m) {
+    const float top = __uint_as_float(m) / kMax8;
+    return top < kMinScale ? kMinScale : top;                  // a NaN stays
+}
+
+// A norm's scale from sum h^2 and max |h w|, and the factors f.x, f.y of h w
+// that give the codes: (h w / root) / s = h w * 448 / max |h w|, one rounding
+// instead of two divisions; where that factor could overflow, or the scale is
+// the least one, 1 / root and 1 / s.  A sum that is not finite (a NaN or an
+// infinity in the row, or h^2 beyond f32) makes the scale NaN.
+__device__ __forceinline__ void norm_scale(const RowsQ8 &a, float ss, float m, float &s, float2 &f) {
+    const float root = sqrtf(ss / (float)a.D + a.eps);
+    const float top = ss <= 3.402823466e38f ? m / root / kMax8 : __int_as_float(0x7FC00000);
+    s = top < kMinScale ? kMinScale : top;
+    f = top < kMinScale || m < 1e-30f ? make_float2(1.f / root, 1.f / s) : make_float2(kMax8 / m, 1.f);
 }
 
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }   // orders as |v|, NaN last
 
-// One block per row, the row in registers: NV vectors of 16 bytes per thread
-// (VEC: every operand's rows start on 16 bytes), or as many single values
-// with the block's threads on neighbouring columns.
-template <class T, int NV, bool VEC, bool NORM>
-__global__ void __launch_bounds__(1024) rows_q8_kernel(const RowsQ8 a) {
-    constexpr int E = kVec<T>;
-    const long long row = blockIdx.x;
-    const int tid = threadIdx.x, n = blockDim.x;
-    const T *x = (const T *)a.x + row * a.ldx;
-    const T *r = NORM && a.r ? (const T *)a.r + row * a.ldr : nullptr;
-    T *h = NORM && a.h ? (T *)a.h + row * a.ldh : nullptr;
-    uint8_t *y = a.y8 + row * a.ld8;
-    float v[NV][E], g[NORM ? NV : 1][E];
-    auto col = [&](int k, int j) { return VEC ? (k * n + tid) * E + j : (k * E + j) * n + tid; };
+// The 16 bytes from offset sh (0..15) on of two neighbouring vectors.  sh is
+// the same for all vectors of a row.
+__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint32_t sh) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const bool s8 = sh & 8, s4 = sh & 4;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        if (VEC && col(k, E - 1) < a.D) {
-            load_vec<T>(x + col(k, 0), v[k]);
+    for (int i = 0; i < 6; ++i) w[i] = s8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = s4 ? w[i + 1] : w[i];
+    const uint32_t bits = 8 * (sh & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// A thread's values: vector k is kVec neighbouring columns from at(k) on, so
+// that its bytes of y8 are aligned; a row's last vector may be short.
+// ALIGNED: every wide operand's rows start on 16 bytes.  Otherwise a vector is
+// the two aligned ones around it, shifted into place; next to the ends of a
+// row, where those would reach past it, values are read one by one, and h is
+// written value by value.
+template <class T, bool ALIGNED> struct Cols {
+    int n, tid, D;
+    __device__ __forceinline__ int at(int k) const { return (k * n + tid) * kVec<T>; }
+    __device__ __forceinline__ bool full(int k) const { return at(k) + kVec<T> <= D; }
+    template <class U>
+    __device__ __forceinline__ Vec<U> load(const U *p, int c) const {
+        constexpr int m = kVec<U>;
+        Vec<U> v;
+        if (ALIGNED ? c + m <= D : c >= m && c + 2 * m <= D) {
+            const char *a = (const char *)(p + c);
+            const uint32_t sh = ALIGNED ? 0u : (uint32_t)((uintptr_t)a & 15u);
+            const uint4 *b = reinterpret_cast<const uint4 *>(a - sh);
+            v.q = ALIGNED ? b[0] : shifted(b[0], b[1], sh);
         } else {
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[k][j] = col(k, j) < a.D ? to_f<T>(x[col(k, j)]) : 0.f;
+            for (int j = 0; j < m; ++j) v.e[j] = c + j < D ? p[c + j] : from_f<U>(0.f);
+        }
+        return v;
+    }
+    __device__ __forceinline__ void store(T *p, int k, const Vec<T> &v) const {
+        if (ALIGNED && full(k)) {
+            *reinterpret_cast<uint4 *>(p + at(k)) = v.q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec<T>; ++j)
+                if (at(k) + j < D) p[at(k) + j] = v.e[j];
         }
     }
-    if (NORM && r) {
+    // E4M3 bytes, in pairs
+    __device__ __forceinline__ void store8(uint8_t *y, int k, const uint32_t (&c)[kVec<T> / 2]) const {
+        if (full(k)) {
+            const uint32_t lo = __byte_perm(c[0], c[1], 0x5410);
+            if constexpr (kVec<T> == 4) *reinterpret_cast<uint32_t *>(y + at(k)) = lo;
+            else *reinterpret_cast<uint2 *>(y + at(k)) = make_uint2(lo, __byte_perm(c[2], c[3], 0x5410));
+        } else {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float q[E];
-            if (VEC && col(k, E - 1) < a.D) {
-                load_vec<T>(r + col(k, 0), q);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) q[j] = col(k, j) < a.D ? to_f<T>(r[col(k, j)]) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[k][j] += q[j];
+            for (int j = 0; j < kVec<T>; ++j)
+                if (at(k) + j < D) y[at(k) + j] = (uint8_t)(c[j / 2] >> (8 * (j & 1)));
         }
     }
-    float ss = 0.f;
+};
+
+// Threads of a block at most, by vectors per thread: registers for two blocks
+// per SM at least, so that one row's loads run under another's arithmetic.
+constexpr int most_threads(int nv) { return nv == 1 ? 1024 : 512; }
+constexpr int least_blocks(int nv) { return nv == 1 ? 1 : 2; }
+
+// The row in registers, NV vectors per thread; blockDim.y rows per block (more
+// than one only where blockDim.x is one warp).
+template <class T, int NV, bool ALIGNED>
+__global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) quantize_q8_kernel(const RowsQ8 a) {
+    constexpr int E = kVec<T>;
+    const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    if (row >= a.S) return;                      // whole warps: blockDim.y > 1 has no barrier
+    const Cols<T, ALIGNED> cols{(int)blockDim.x, (int)threadIdx.x, a.D};
+    const T *x = (const T *)a.x + row * a.ldx;
+    uint8_t *y = a.y8 + row * a.ld8;
+    Vec<T> v[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = cols.load(x, cols.at(k));
     unsigned m = 0;
 #pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) m = max(m, magnitude(v[k].at(j)));
+    float none = 0.f;
+    block_reduce(none, m);
+    const float s = plain_scale(m), rs = 1.f / s;
+    if (threadIdx.x == 0) a.ys[row] = s;
+#pragma unroll
     for (int k = 0; k < NV; ++k) {
-        if constexpr (NORM) {
-            if (VEC && col(k, E - 1) < a.D) {
+        uint32_t c[E / 2];
 #pragma unroll
-                for (int j = 0; j < E; j += 4) {
-                    const float4 w = *reinterpret_cast<const float4 *>(a.w + col(k, j));
-                    g[k][j] = w.x, g[k][j + 1] = w.y, g[k][j + 2] = w.z, g[k][j + 3] = w.w;
-                }
-            } else {
+        for (int j = 0; j < E; j += 2) c[j / 2] = e4m3x2(div_by(v[k].at(j), s, rs), div_by(v[k].at(j + 1), s, rs));
+        cols.store8(y, k, c);
+    }
+}
+
+template <class T, int NV, bool ALIGNED>
+__global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) rmsnorm_q8_kernel(const RowsQ8 a) {
+    constexpr int E = kVec<T>;
+    const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    if (row >= a.S) return;
+    const Cols<T, ALIGNED> cols{(int)blockDim.x, (int)threadIdx.x, a.D};
+    const T *x = (const T *)a.x + row * a.ldx;
+    const T *r = a.r ? (const T *)a.r + row * a.ldr : nullptr;
+    T *h = a.h ? (T *)a.h + row * a.ldh : nullptr;
+    uint8_t *y = a.y8 + row * a.ld8;
+    Vec<T> xv[NV], rv[NV];
 #pragma unroll
-                for (int j = 0; j < E; ++j) g[k][j] = col(k, j) < a.D ? a.w[col(k, j)] : 0.f;
-            }
+    for (int k = 0; k < NV; ++k) xv[k] = cols.load(x, cols.at(k));
+    if (r) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) rv[k] = cols.load(r, cols.at(k));
+    }
+    float v[NV][E], ss = 0.f, m = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        Vec<T> hv;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            v[k][j] = r ? xv[k].at(j) + rv[k].at(j) : xv[k].at(j);
+            hv.e[j] = from_f<T>(v[k][j]);
         }
-        if (h) {
-            if (VEC && col(k, E - 1) < a.D) {
-                store_vec<T>(h + col(k, 0), v[k]);
-            } else {
+        if (h) cols.store(h, k, hv);
+        float g[E];
 #pragma unroll
-                for (int j = 0; j < E; ++j)
-                    if (col(k, j) < a.D) h[col(k, j)] = from_f<T>(v[k][j]);
-            }
+        for (int j = 0; j < E; j += 4) {
+            const Vec<float> wv = cols.load(a.w, cols.at(k) + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[j + i] = wv.e[i];
         }
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            if constexpr (NORM) {
-                ss = fmaf(v[k][j], v[k][j], ss);
-                v[k][j] *= g[k][j];
-            }
-            m = max(m, magnitude(v[k][j]));
+            ss = fmaf(v[k][j], v[k][j], ss);
+            v[k][j] *= g[j];
+            m = fmaxf(m, fabsf(v[k][j]));
         }
     }
-    block_reduce(ss, m);
-    float root, s;
-    row_scale(a, ss, m, root, s);
-    if (tid == 0) a.ys[row] = s;
+    unsigned mb = __float_as_uint(m);
+    block_reduce(ss, mb);
+    float s;
+    float2 f;
+    norm_scale(a, ss, __uint_as_float(mb), s, f);
+    if (threadIdx.x == 0) a.ys[row] = s;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        uint32_t c[E];
+        uint32_t c[E / 2];
 #pragma unroll
-        for (int j = 0; j < E; j += 2) {
-            const float u0 = NORM ? v[k][j] / root : v[k][j], u1 = NORM ? v[k][j + 1] / root : v[k][j + 1];
-            const uint32_t p = e4m3x2(u0 / s, u1 / s);
-            c[j] = p & 255u, c[j + 1] = p >> 8;
-        }
-        if (VEC && col(k, E - 1) < a.D) {
-            const uint32_t lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-            if constexpr (E == 4) *reinterpret_cast<uint32_t *>(y + col(k, 0)) = lo;
-            else *reinterpret_cast<uint2 *>(y + col(k, 0)) = make_uint2(lo, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
-        } else {
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (col(k, j) < a.D) y[col(k, j)] = (uint8_t)c[j];
-        }
+        for (int j = 0; j < E; j += 2) c[j / 2] = e4m3x2(v[k][j] * f.x * f.y, v[k][j + 1] * f.x * f.y);
+        cols.store8(y, k, c);
     }
 }
 
@@ -199,30 +266,31 @@ __global__ void __launch_bounds__(kLongThreads) rows_q8_long_kernel(const RowsQ8
         m = max(m, magnitude(a.w ? v * a.w[d] : v));
     }
     block_reduce(ss, m);
-    float root, s;
-    row_scale(a, ss, m, root, s);
+    float s = plain_scale(m);
+    float2 f = make_float2(0.f, 0.f);
+    if (a.w) norm_scale(a, ss, __uint_as_float(m), s, f);
     if (threadIdx.x == 0) a.ys[row] = s;
+    const float rs = 1.f / s;
     for (int d = threadIdx.x; d < a.D; d += kLongThreads) {
         const float v = r ? to_f<T>(x[d]) + to_f<T>(r[d]) : to_f<T>(x[d]);
         if (h) h[d] = from_f<T>(v);                             // after this thread's last read of x[d], r[d]
-        const float u = a.w ? v * a.w[d] / root : v;
-        y[d] = (uint8_t)e4m3x2(u / s, 0.f);
+        y[d] = (uint8_t)e4m3x2(a.w ? v * a.w[d] * f.x * f.y : div_by(v, s, rs), 0.f);
     }
 }
 
-template <class T, int NV, bool VEC>
-void start(const RowsQ8 &a, int threads, cudaStream_t st) {
-    if (a.w) rows_q8_kernel<T, NV, VEC, true><<<a.S, threads, 0, st>>>(a);
-    else rows_q8_kernel<T, NV, VEC, false><<<a.S, threads, 0, st>>>(a);
+template <class T, int NV, bool ALIGNED>
+void start(const RowsQ8 &a, dim3 block, cudaStream_t st) {
+    const unsigned grid = (unsigned)((a.S + (long long)block.y - 1) / block.y);
+    if (a.w) rmsnorm_q8_kernel<T, NV, ALIGNED><<<grid, block, 0, st>>>(a);
+    else quantize_q8_kernel<T, NV, ALIGNED><<<grid, block, 0, st>>>(a);
 }
 
-template <class T, bool VEC>
-void start_nv(const RowsQ8 &a, int nv, int threads, cudaStream_t st) {
-    switch (nv) {
-    case 1: return start<T, 1, VEC>(a, threads, st);
-    case 2: return start<T, 2, VEC>(a, threads, st);
-    default: return start<T, 4, VEC>(a, threads, st);
-    }
+template <class T, bool ALIGNED>
+void start_nv(const RowsQ8 &a, int nv, dim3 block, cudaStream_t st) {
+    if (nv == 1) start<T, 1, ALIGNED>(a, block, st);
+    else if (nv == 2) start<T, 2, ALIGNED>(a, block, st);
+    else if (nv == 4 || kVec<T> == 8) start<T, 4, ALIGNED>(a, block, st);
+    else start<T, 32 / kVec<T>, ALIGNED>(a, block, st);
 }
 
 template <class T>
@@ -231,20 +299,26 @@ cudaError_t run(const RowsQ8 &a, cudaStream_t st) {
     auto ok = [](const void *p, long long ld) {
         return !p || ((uintptr_t)p % 16 == 0 && ld * (long long)sizeof(T) % 16 == 0);
     };
-    const bool vec = ok(a.x, a.ldx) && ok(a.r, a.ldr) && ok(a.h, a.ldh) && (uintptr_t)a.w % 16 == 0;
-    // few rows: one vector per thread, the shortest chain; many: several, so
-    // that a block has more bytes in flight behind its one barrier
-    const int units = (a.D + E - 1) / E;
+    const bool aligned = ok(a.x, a.ldx) && ok(a.r, a.ldr) && ok(a.h, a.ldh) && (uintptr_t)a.w % 16 == 0;
+    const int units = (a.D + E - 1) / E;             // 16-byte vectors of a row
     int dev = 0;
     cudaGetDevice(&dev);
-    int nv = a.S <= 2 * sm_count(dev) ? 1 : 4;
-    while (nv < 4 && units > nv * 1024) nv *= 2;
-    if (units > nv * 1024) {
+    // few rows: as many threads as there are vectors, the shortest chain;
+    // many: up to 32 values per thread, several blocks per SM
+    int nv = 1;
+    const int most = a.S <= 2 * sm_count(dev) ? 1024 : 256;
+    while (nv < 32 / E && units > nv * (most < most_threads(nv) ? most : most_threads(nv))) nv *= 2;         // 32 values per thread at most
+    dim3 block(((units + nv - 1) / nv + 31) / 32 * 32);
+    if (a.S > 2 * sm_count(dev) && units <= 128) {   // short rows: a warp each, four to a block, no barrier
+        nv = units <= 32 ? 1 : units <= 64 ? 2 : 4;
+        block = dim3(32, 4);
+    }
+    if ((int)block.x > most_threads(nv)) {
         rows_q8_long_kernel<T><<<a.S, kLongThreads, 0, st>>>(a);
+    } else if (aligned) {
+        start_nv<T, true>(a, nv, block, st);
     } else {
-        const int threads = ((units + nv - 1) / nv + 31) / 32 * 32;
-        if (vec) start_nv<T, true>(a, nv, threads, st);
-        else start_nv<T, false>(a, nv, threads, st);
+        start_nv<T, false>(a, nv, block, st);
     }
     count_launch();
     return cudaGetLastError();
