@@ -151,7 +151,8 @@ struct MatQ8 {
 };
 cudaError_t launch_mat_q8(const MatQ8 &a, cudaStream_t st);
 
-// The tensor-core kernel behind it, any S.
+// The kernels behind it: few rows (sets *handled if it took the call), any S.
+cudaError_t launch_mv_q8(const MatQ8 &a, cudaStream_t st, bool *handled);
 cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st);
 
 }  // namespace qwq
