@@ -7,19 +7,27 @@
 // instruction m16n8k16 (f16 in, f32 sums): 16 weight rows against 8 tokens.
 // The tcgen05 kernel needs 128 weight rows per tile, which leaves too few
 // tiles to fill the GPU at one token without splitting K between CTAs.
-//   * Codes and E4M3 values are exact in f16, so every product is exact.  An
-//     int4 field ORed into the mantissa of 1024 is 1024 + c (or 1024 + 16 c,
-//     one position up): one LOP3 and one packed f16 FMA per two weights.
+//   * Codes (signed) and E4M3 values are exact in f16, so every product is
+//     exact; sums are f32.  An int4 field ORed into the mantissa of 1024 is
+//     1024 + c (or 1024 + 16 c, one position up): one LOP3 and one packed f16
+//     FMA per two weights.  (Unsigned fields as f16 subnormals, with the zero
+//     point times sum_i x8 taken off at the end, need no FMA, but lose the
+//     bound where a large x meets codes that stand for zero.  The E4M3 form of
+//     the instruction costs more: its operands are widened first.)
 //   * The order of K inside an instruction is free as long as both operands
 //     agree: a thread keeps the order in which the fields of its own 16 bytes
 //     of codes come apart, and x is stored in shared memory in that order.
-//   * Weights go from global memory straight to registers, 16 bytes per thread
-//     and row, several steps ahead; a warp's step is 64 bytes of 16 rows, and
-//     the warps of a CTA take neighbouring steps of one tile, so K is split
-//     over them and their sums are added in warp order at the end of the tile.
-//   * The first steps' loads are issued before the dependency wait (the
-//     weights are never written after their upload), and so run under the
-//     previous kernel's end and the staging of x.
+//   * x is staged in f16 where that leaves room for the ring, otherwise as its
+//     bytes, which become f16 in registers.
+//   * Each thread copies its own 16 bytes of codes per row and step to its own
+//     slot of a ring in shared memory (cp.async), several steps ahead and
+//     across tile boundaries; nothing but its own wait orders them.  A warp's
+//     step is 64 bytes of 16 rows; the warps of a CTA take neighbouring steps
+//     of one tile, so K is split over them and their sums are added in warp
+//     order at the end of the tile.
+//   * The ring is filled before the dependency wait (the weights are never
+//     written after their upload): memory works under the previous kernel's
+//     end and the staging of x.
 #include <cuda_fp16.h>
 
 #include "qmat_q8.h"
@@ -30,7 +38,8 @@ namespace {
 constexpr int kTokens = 8;
 constexpr int kTileRows = 16;
 
-// KC: codes in 16 bytes.  WORDS: mma instructions per 32-bit word of codes.
+// KC: codes in 16 bytes.  MMAS: instructions per 32-bit word of codes (each
+// takes four codes per thread and row).
 template <int FMT> struct Fmt;
 template <> struct Fmt<B200Q_I8> { static constexpr int KC = 16, MMAS = 1; };
 template <> struct Fmt<B200Q_I4> { static constexpr int KC = 32, MMAS = 2; };
@@ -48,43 +57,84 @@ struct MvParams {
     int pitch;                              // bytes of a token's x in shared memory
 };
 
-__device__ __forceinline__ uint32_t lop_or(uint32_t w, uint32_t mask, uint32_t magic) {
+__device__ __forceinline__ uint32_t lop_or(uint32_t w, uint32_t mask) {     // (w & mask) | 1024 in f16, twice
     uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
     return r;
 }
 
-__device__ __forceinline__ uint32_t h2(uint32_t a, uint32_t mul, uint32_t add) {
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t mul, uint32_t add) {
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(mul), "r"(add));
     return r;
 }
 
-// A word of codes -> pairs of exact f16 values, pair 2 m and 2 m + 1 for
-// instruction m.  f16 constants: 0x6400 = 1024; products and sums are exact.
+// Instruction t of a word of codes: two pairs of exact f16 values.
+//   int8  (0,1) (2,3);  int4  t = 0: (0,4) (2,6), t = 1: (1,5) (3,7);
+//   int2  (t,8+t) (4+t,12+t)
+// A field at bit b of 1024's mantissa is 1024 + c 2^b; times 2^-b, minus the
+// rest and the zero point, is the code's value.
 template <int FMT>
-__device__ __forceinline__ void pairs(uint32_t w, uint32_t (&p)[2 * Fmt<FMT>::MMAS]) {
-    constexpr uint32_t k1024 = 0x64006400u, one = 0x3C003C00u;
-    if constexpr (FMT == B200Q_I8) {                      // natural order: 1024 + (c + 128) - 1152
+__device__ __forceinline__ void fields(uint32_t w, int t, uint32_t &a, uint32_t &b) {
+    constexpr uint32_t one = 0x3C003C00u;
+    if constexpr (FMT == B200Q_I8) {                      // 1024 + (c + 128) - 1152
         const uint32_t u = w ^ 0x80808080u;
-        p[0] = h2(__byte_perm(u, k1024, 0x5150), one, 0xE480E480u);
-        p[1] = h2(__byte_perm(u, k1024, 0x5352), one, 0xE480E480u);
-    } else if constexpr (FMT == B200Q_I4) {               // (0,4) (1,5) (2,6) (3,7)
-        const uint32_t v = w >> 8;
-        p[0] = h2(lop_or(w, 0x000F000Fu, k1024), one, 0xE408E408u);            // - 1032
-        p[1] = h2(lop_or(w, 0x00F000F0u, k1024), 0x2C002C00u, 0xD480D480u);    // / 16 - 72
-        p[2] = h2(lop_or(v, 0x000F000Fu, k1024), one, 0xE408E408u);
-        p[3] = h2(lop_or(v, 0x00F000F0u, k1024), 0x2C002C00u, 0xD480D480u);
-    } else {                                              // (0,8) (1,9) .. (7,15)
-        const uint32_t v = w >> 8;
+        a = fma_h2(__byte_perm(u, 0x64006400u, 0x5150), one, 0xE480E480u);
+        b = fma_h2(__byte_perm(u, 0x64006400u, 0x5352), one, 0xE480E480u);
+    } else if constexpr (FMT == B200Q_I4) {               // - 1032, / 16 - 72
+        const uint32_t mask = t ? 0x00F000F0u : 0x000F000Fu;
+        const uint32_t mul = t ? 0x2C002C00u : one, add = t ? 0xD480D480u : 0xE408E408u;
+        a = fma_h2(lop_or(w, mask), mul, add);
+        b = fma_h2(lop_or(w >> 8, mask), mul, add);
+    } else {                                              // - 1026, / 4 - 258, / 16 - 66, / 64 - 18
+        const uint32_t mask = 0x00030003u << (2 * t);
+        const uint32_t mul = t == 0 ? one : t == 1 ? 0x34003400u : t == 2 ? 0x2C002C00u : 0x24002400u;
+        const uint32_t add = t == 0 ? 0xE402E402u : t == 1 ? 0xDC08DC08u : t == 2 ? 0xD420D420u : 0xCC80CC80u;
+        a = fma_h2(lop_or(w, mask), mul, add);
+        b = fma_h2(lop_or(w >> 8, mask), mul, add);
+    }
+}
+
+// 16 bytes of x8 in the order of fields(): word h holds the two pairs of
+// instruction h % MMAS.
+template <int FMT>
+__device__ __forceinline__ uint4 permuted(uint4 q) {
+    if constexpr (FMT == B200Q_I8) return q;
+    if constexpr (FMT == B200Q_I4)
+        return make_uint4(__byte_perm(q.x, q.y, 0x6240), __byte_perm(q.x, q.y, 0x7351), __byte_perm(q.z, q.w, 0x6240),
+                          __byte_perm(q.z, q.w, 0x7351));
+    const uint32_t a = __byte_perm(q.x, q.z, 0x5140), b = __byte_perm(q.y, q.w, 0x5140);
+    const uint32_t c = __byte_perm(q.x, q.z, 0x7362), d = __byte_perm(q.y, q.w, 0x7362);
+    return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x5410),
+                      __byte_perm(c, d, 0x7632));
+}
+
+// Two E4M3 bytes -> two f16 (exact).
+__device__ __forceinline__ uint32_t x_pair(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+    return r;
+}
+
+// 16 bytes of x8 (columns k0 ..) into a token's staged row: per 64-byte group
+// of codes, the 16-byte pieces of its four chunks side by side.
+template <int FMT, bool XH>
+__device__ __forceinline__ void stage16(uint8_t *row, int k0, uint4 q) {
+    constexpr int KC = Fmt<FMT>::KC;
+    const int c = k0 / KC, tig = c & 3, grp = c >> 2, in = (k0 % KC) / 16;
+    if constexpr (!XH) {
+        *reinterpret_cast<uint4 *>(row + grp * (4 * KC) + in * 64 + tig * 16) = q;
+    } else {
+        uint8_t *dst = row + grp * (8 * KC) + in * 128 + tig * 16;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t f[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t q = h ? v : w;
-            p[4 * h] = h2(lop_or(q, 0x00030003u, k1024), one, 0xE402E402u);                // - 1026
-            p[4 * h + 1] = h2(lop_or(q, 0x000C000Cu, k1024), 0x34003400u, 0xDC08DC08u);    // / 4 - 258
-            p[4 * h + 2] = h2(lop_or(q, 0x00300030u, k1024), 0x2C002C00u, 0xD420D420u);    // / 16 - 66
-            p[4 * h + 3] = h2(lop_or(q, 0x00C000C0u, k1024), 0x24002400u, 0xCC80CC80u);    // / 64 - 18
+        for (int h = 0; h < 4; ++h) {
+            f[2 * h] = x_pair(w[h] & 0xFFFFu);
+            f[2 * h + 1] = x_pair(w[h] >> 16);
         }
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4 *>(dst + 64) = make_uint4(f[4], f[5], f[6], f[7]);
     }
 }
 
@@ -96,172 +146,168 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Two E4M3 bytes -> two f16 (exact).
-__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
-    return r;
-}
-
-// 16 bytes of x8 (columns k0 ..) into a token's staged row.
-template <int FMT>
-__device__ __forceinline__ void stage16(uint8_t *row, int k0, uint4 q) {
-    constexpr int KC = Fmt<FMT>::KC;
-    const uint32_t b[4] = {q.x, q.y, q.z, q.w};
-    uint32_t n[8];                                     // natural pairs (0,1) (2,3) ..
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n[2 * i] = e4m3_h2(b[i] & 0xFFFFu), n[2 * i + 1] = e4m3_h2(b[i] >> 16);
-    const int c = k0 / KC, tig = c & 3, grp = c >> 2;
-    uint8_t *dst = row + (size_t)grp * (8 * KC) + tig * 16 + (k0 % KC) / 8 * 64;
-    uint4 lo, hi;
-    if constexpr (FMT == B200Q_I8) {
-        lo = make_uint4(n[0], n[1], n[2], n[3]);
-        hi = make_uint4(n[4], n[5], n[6], n[7]);
-    } else if constexpr (FMT == B200Q_I4) {            // each eight as (0,4) (1,5) (2,6) (3,7)
-        lo = make_uint4(__byte_perm(n[0], n[2], 0x5410), __byte_perm(n[0], n[2], 0x7632),
-                        __byte_perm(n[1], n[3], 0x5410), __byte_perm(n[1], n[3], 0x7632));
-        hi = make_uint4(__byte_perm(n[4], n[6], 0x5410), __byte_perm(n[4], n[6], 0x7632),
-                        __byte_perm(n[5], n[7], 0x5410), __byte_perm(n[5], n[7], 0x7632));
-    } else {                                           // sixteen as (0,8) (1,9) .. (7,15)
-        lo = make_uint4(__byte_perm(n[0], n[4], 0x5410), __byte_perm(n[0], n[4], 0x7632),
-                        __byte_perm(n[1], n[5], 0x5410), __byte_perm(n[1], n[5], 0x7632));
-        hi = make_uint4(__byte_perm(n[2], n[6], 0x5410), __byte_perm(n[2], n[6], 0x7632),
-                        __byte_perm(n[3], n[7], 0x5410), __byte_perm(n[3], n[7], 0x7632));
-    }
-    *reinterpret_cast<uint4 *>(dst) = lo;
-    *reinterpret_cast<uint4 *>(dst + 64) = hi;
-}
-
-template <int FMT, bool GLU>
+// AHEAD: steps in the ring.  XH: x staged in f16.
+template <int FMT, bool GLU, bool XH, int AHEAD>
 __global__ void __launch_bounds__(1024, 1) qmv_q8_kernel(const MvParams p) {
     constexpr int KC = Fmt<FMT>::KC, MMAS = Fmt<FMT>::MMAS, M = GLU ? 2 : 1;
-    constexpr int kAhead = GLU ? 2 : 4;                // steps in flight per warp
+    constexpr int kGroup = (XH ? 8 : 4) * KC;          // bytes of a token's x per 64-byte group of codes
+    constexpr int kSlot = M * 1024;                    // bytes of a warp's step: [M][2 row halves][32 lanes] x 16
     extern __shared__ __align__(128) uint8_t smem[];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tig = lane & 3;
-    float *red = reinterpret_cast<float *>(smem + (size_t)p.S * p.pitch);      // [warps][M][128]
-    const int steps = p.ng > warp ? (p.ng - warp + warps - 1) / warps : 0;     // of this warp per tile
+    uint8_t *ring = smem + warp * (AHEAD * kSlot) + lane * 16;
+    float *red = reinterpret_cast<float *>(smem + warps * (AHEAD * kSlot));     // [2][warps][M][128]
+    uint8_t *xsm = reinterpret_cast<uint8_t *>(red + 2 * warps * M * 128);
+    const int steps = p.ng > warp ? (p.ng - warp + warps - 1) / warps : 0;      // of this warp per tile
 
-    uint4 q[kAhead][M][2];
-    const uint8_t *src[M];
-    auto aim = [&](int tile) {
+    // the copy cursor runs AHEAD steps before the arithmetic
+    int ftile = steps ? (int)blockIdx.x : p.tiles, fst = 0, fslot = 0;
+    const uint32_t ring32 = (uint32_t)__cvta_generic_to_shared(ring);
+    const long long tile_step = (long long)gridDim.x * kTileRows * p.ld - (long long)steps * warps * 64;
+    const long long row8 = 8 * p.ld;
+    long long off = ((long long)blockIdx.x * kTileRows + g) * p.ld + warp * 64 + tig * 16;
+    auto copy_step = [&]() {
+        if (ftile < p.tiles) {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-            src[m] = p.codes[m] + ((long long)tile * kTileRows + g) * p.ld + warp * 64 + tig * 16;
-    };
-    auto fetch = [&](int slot, int st) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            q[slot][m][0] = load_codes(src[m] + (long long)st * warps * 64);
-            q[slot][m][1] = load_codes(src[m] + (long long)st * warps * 64 + 8 * p.ld);
+            for (int m = 0; m < M; ++m) {
+                copy16(ring32 + fslot * kSlot + m * 1024, p.codes[m] + off);
+                copy16(ring32 + fslot * kSlot + m * 1024 + 512, p.codes[m] + off + row8);
+            }
+            off += warps * 64;
+            if (++fst == steps) fst = 0, ftile += gridDim.x, off += tile_step;
+            if (++fslot == AHEAD) fslot = 0;
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");       // empty at the end: the waits count groups
     };
-    aim(blockIdx.x);
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s)
-        if (s < steps) fetch(s, s);
+#pragma unroll 1
+    for (int s = 0; s < AHEAD; ++s) copy_step();
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // x, in f16 and the codes' order, zero past I
-    const int kpad = p.ng * 4 * KC;
+    // x, zero past I
+    const int cols = p.ng * 4 * KC;
     for (int s = 0; s < p.S; ++s) {
         const uint8_t *xr = p.x8 + s * p.ld8;
-        uint8_t *row = smem + (size_t)s * p.pitch;
-        for (int k = threadIdx.x * 16; k < kpad; k += blockDim.x * 16) {
+        uint8_t *row = xsm + s * p.pitch;
+#pragma unroll 2
+        for (int k = threadIdx.x * 16; k < cols; k += blockDim.x * 16) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (k + 16 <= p.I) {
                 v = *reinterpret_cast<const uint4 *>(xr + k);
             } else if (k < p.I) {
                 uint32_t w[4] = {0u, 0u, 0u, 0u};
-                for (int j = 0; k + j < p.I; ++j) w[j >> 2] |= (uint32_t)xr[k + j] << (8 * (j & 3));
+#pragma unroll
+                for (int j = 0; j < 15; ++j)
+                    if (k + j < p.I) w[j >> 2] |= (uint32_t)xr[k + j] << (8 * (j & 3));
                 v = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            stage16<FMT>(row, k, v);
+            stage16<FMT, XH>(row, k, permuted<FMT>(v));
         }
     }
     __syncthreads();
 
     const bool have = g < p.S;
-    const uint8_t *xb = smem + (size_t)(have ? g : 0) * p.pitch + tig * 16 + (size_t)warp * (8 * KC);
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const uint8_t *xb = xsm + (have ? g : 0) * p.pitch + tig * 16 + warp * kGroup;
+    int slot = 0, buf = 0;
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, buf ^= 1) {
         float acc[M][4] = {};
-        for (int s0 = 0; s0 < steps; s0 += kAhead) {
+        const uint8_t *xp = xb;
+        for (int st = 0; st < steps; ++st, xp += warps * kGroup) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+            uint4 q[M][2];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int st = s0 + a;
-                if (st >= steps) break;
-                const uint8_t *xp = xb + (size_t)st * warps * (8 * KC);
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {           // words of the 16 bytes
-                    uint32_t b[2 * MMAS];
-                    if constexpr (MMAS == 1) {
-                        uint2 v = make_uint2(0u, 0u);
-                        if (have) v = *reinterpret_cast<const uint2 *>(xp + (i >> 1) * 64 + (i & 1) * 8);
-                        b[0] = v.x, b[1] = v.y;
-                    } else {
+                for (int h = 0; h < 2; ++h)
+                    q[m][h] = *reinterpret_cast<const uint4 *>(ring + slot * kSlot + m * 1024 + h * 512);
+            if (++slot == AHEAD) slot = 0;
+            constexpr int L = kGroup / 64;              // 16-byte pieces of x per chunk
+            uint4 xv[L];
 #pragma unroll
-                        for (int h = 0; h < MMAS / 2; ++h) {
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (have) v = *reinterpret_cast<const uint4 *>(xp + (i * (MMAS / 2) + h) * 64);
-                            b[4 * h] = v.x, b[4 * h + 1] = v.y, b[4 * h + 2] = v.z, b[4 * h + 3] = v.w;
-                        }
-                    }
+            for (int l = 0; l < L; ++l)
+                xv[l] = have ? *reinterpret_cast<const uint4 *>(xp + l * 64) : make_uint4(0u, 0u, 0u, 0u);
+            copy_step();       // into the slot just read: this thread's own, so no barrier
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        uint32_t lo[2 * MMAS], hi[2 * MMAS];
-                        const uint4 &c0 = q[a][m][0], &c1 = q[a][m][1];
-                        pairs<FMT>(i == 0 ? c0.x : i == 1 ? c0.y : i == 2 ? c0.z : c0.w, lo);
-                        pairs<FMT>(i == 0 ? c1.x : i == 1 ? c1.y : i == 2 ? c1.z : c1.w, hi);
-#pragma unroll
-                        for (int t = 0; t < MMAS; ++t)
-                            mma_f16(acc[m], lo[2 * t], hi[2 * t], lo[2 * t + 1], hi[2 * t + 1], b[2 * t], b[2 * t + 1]);
-                    }
+            for (int n = 0; n < 4 * MMAS; ++n) {
+                const int i = n / MMAS, t = n % MMAS;   // word of the 16 bytes, instruction of the word
+                uint32_t b0, b1;
+                if constexpr (XH) {
+                    const uint4 &v = xv[n / 2];
+                    b0 = n & 1 ? v.z : v.x, b1 = n & 1 ? v.w : v.y;
+                } else {
+                    const uint4 &v = xv[n / 4];
+                    const uint32_t e = n % 4 == 0 ? v.x : n % 4 == 1 ? v.y : n % 4 == 2 ? v.z : v.w;
+                    b0 = x_pair(e & 0xFFFFu), b1 = x_pair(e >> 16);
                 }
-                if (st + kAhead < steps) fetch(a, st + kAhead);
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const uint4 &c0 = q[m][0], &c1 = q[m][1];
+                    uint32_t a0, a1, a2, a3;
+                    fields<FMT>(i == 0 ? c0.x : i == 1 ? c0.y : i == 2 ? c0.z : c0.w, t, a0, a2);
+                    fields<FMT>(i == 0 ? c1.x : i == 1 ? c1.y : i == 2 ? c1.z : c1.w, t, a1, a3);
+                    mma_f16(acc[m], a0, a1, a2, a3, b0, b1);
+                }
             }
         }
-        const int next = tile + gridDim.x;
-        if (next < p.tiles) {
-            aim(next);
-#pragma unroll
-            for (int s = 0; s < kAhead; ++s)
-                if (s < steps) fetch(s, s);
-        }
-        // [row][token] of the tile, added over the warps in order
+        // [row][token] of the tile, added over the warps in order; the two
+        // buffers take turns, so that one barrier per tile is enough
+        float *rb = red + buf * warps * M * 128;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            float *r = red + (warp * M + m) * 128;
+            float *r = rb + (warp * M + m) * 128;
             *reinterpret_cast<float2 *>(r + g * 8 + 2 * tig) = make_float2(acc[m][0], acc[m][1]);
             *reinterpret_cast<float2 *>(r + (g + 8) * 8 + 2 * tig) = make_float2(acc[m][2], acc[m][3]);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < 128; e += blockDim.x) {
-            const int s = e >> 4, r = e & 15, o = tile * kTileRows + r;
-            if (s >= p.S || o >= p.O) continue;
-            float v[M];
+        if (threadIdx.x < 128) {
+            const int s = threadIdx.x >> 4, r = threadIdx.x & 15, o = tile * kTileRows + r;
+            if (s < p.S && o < p.O) {
+                float v[M];
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                float sum = 0.f;
-                for (int w = 0; w < warps; ++w) sum += red[(w * M + m) * 128 + r * 8 + s];
-                v[m] = fmaf(sum, p.xs[s] * p.scale[m][o], p.bias[m] ? p.bias[m][o] : 0.f);
+                for (int m = 0; m < M; ++m) {
+                    float sum = 0.f;
+#pragma unroll 8
+                    for (int w = 0; w < warps; ++w) sum += rb[(w * M + m) * 128 + r * 8 + s];
+                    v[m] = fmaf(sum, p.xs[s] * p.scale[m][o], p.bias[m] ? p.bias[m][o] : 0.f);
+                }
+                float out = act_q8(v[0], p.act);
+                if constexpr (GLU) out *= v[1];
+                if (p.res) out += load_typed(p.res, s * p.ldr + o, p.type);
+                store_typed(p.y, s * p.ldy + o, p.type, out);
             }
-            float out = act_q8(v[0], p.act);
-            if constexpr (GLU) out *= v[1];
-            if (p.res) out += load_typed(p.res, s * p.ldr + o, p.type);
-            store_typed(p.y, s * p.ldy + o, p.type, out);
         }
-        __syncthreads();
     }
+}
+
+// Shared memory beside x and the ring: two sets of the warps' sums.
+constexpr long long sums_bytes(int warps, int M) { return (long long)warps * 2 * M * 512; }
+
+template <int FMT, bool GLU, bool XH, int AHEAD>
+cudaError_t start(const MvParams &p, int device, int c, int warps, cudaStream_t st, bool *handled) {
+    constexpr int M = GLU ? 2 : 1;
+    const size_t smem = (size_t)(p.S * p.pitch + sums_bytes(warps, M)) + (size_t)warps * M * AHEAD * 1024;
+    cudaError_t e = allow_dynamic_smem((const void *)qmv_q8_kernel<FMT, GLU, XH, AHEAD>, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    const int slots = sm_count(device) * c;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.tiles < slots ? p.tiles : slots);
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, qmv_q8_kernel<FMT, GLU, XH, AHEAD>, p);
+    count_launch();
+    *handled = true;
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int FMT, bool GLU>
@@ -290,30 +336,27 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st, bool *handled) {
     p.ng = (int)(t.ld / 64);
     p.act = a.act;
     p.type = a.type;
-    p.pitch = p.ng * 8 * KC + 64;                       // 64 bytes off a 128-byte multiple: two tokens' reads differ in bank
-    // 32 warps per SM: four CTAs of 8, two of 16 or one of 32, as x fits
-    const long long xbytes = (long long)a.S * p.pitch;
-    int warps = 8;
-    while (warps <= 32 && (xbytes + (long long)warps * M * 512 + 1024) * (32 / warps) > 228 * 1024) warps *= 2;
-    if (warps > 32) return cudaSuccess;                 // x does not fit: not handled here
-    const size_t smem = (size_t)xbytes + (size_t)warps * M * 512;
-    cudaError_t e = allow_dynamic_smem((const void *)qmv_q8_kernel<FMT, GLU>, 227 * 1024);
-    if (e != cudaSuccess) return e;
-    const int slots = sm_count(t.device) * (32 / warps);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.tiles < slots ? p.tiles : slots);
-    cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, qmv_q8_kernel<FMT, GLU>, p);
-    count_launch();
-    *handled = true;
-    return e != cudaSuccess ? e : cudaGetLastError();
+    // 32 warps per SM in c CTAs: several, so that one's end of a tile runs under
+    // another's copies; 16 where x leaves no room for more.  x in f16 if it
+    // fits beside a ring of four steps (two of the pair) with two CTAs per SM
+    // or more, as bytes otherwise (12288 x 6144 int4, 8 tokens: f16 with one
+    // CTA 16.1 us, bytes with two 14.9 us; one token, f16: 12.0 us).
+    // Rows are 64 bytes off a 128-byte multiple: two tokens' reads differ in bank.
+    constexpr int kShape[4][2] = {{4, 8}, {2, 16}, {1, 32}, {1, 16}};      // CTAs per SM, warps per CTA
+    for (int xh = 1; xh >= 0; --xh)
+        for (const auto &sh : kShape) {
+            const int c = sh[0], warps = sh[1];
+            p.pitch = p.ng * (xh ? 8 : 4) * KC + 64;
+            const long long room = 228 * 1024 / c - 1024 - (long long)p.S * p.pitch - sums_bytes(warps, M);
+            const long long ahead = room / (warps * M * 1024);
+            if (ahead >= (GLU || !xh ? 2 : 4) && !(xh && c == 1)) {
+                if (xh) return ahead >= 4 ? start<FMT, GLU, true, 4>(p, t.device, c, warps, st, handled)
+                                          : start<FMT, GLU, true, 2>(p, t.device, c, warps, st, handled);
+                return ahead >= 4 ? start<FMT, GLU, false, 4>(p, t.device, c, warps, st, handled)
+                                  : start<FMT, GLU, false, 2>(p, t.device, c, warps, st, handled);
+            }
+        }
+    return cudaSuccess;                                 // x does not fit: not handled here
 }
 
 }  // namespace
