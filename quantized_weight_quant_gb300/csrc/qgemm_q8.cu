@@ -22,13 +22,16 @@
 //              thread ~160 cycles and an mbarrier test ~290, so one thread
 //              for all three copies of an item would be slower than its MMAs);
 //   warp 3     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
-//              tensor memory, B from shared memory) into one of two
-//              accumulators; one commit per item frees both its stage and its
-//              A buffer;
+//              tensor memory, B from shared memory); one commit per item frees
+//              both its stage and its A buffer;
 //   warps 4 .. dequantizers, in groups of four: codes -> E4M3 bytes by a
 //              16-entry table lookup in registers (byte permutes), stored to
 //              the group's A buffer in tensor memory, natural K order;
-//   last four  epilogue.
+//   last eight epilogue, two warps per lane quarter.
+// A tile of more than 128 rows of x8 takes two accumulators, so that one
+// dequantized A serves up to 256 rows (at 192, dequantizing and shared memory,
+// not the MMAs, set the time of an item).  Three accumulators take turns: the
+// next tile's MMAs start when the first of its two is drained.
 // The gated pair takes 64 gate and 64 up rows per tile, interleaved by 16 in
 // the lanes, so that a gate and its up value sit in one warp, 16 lanes apart.
 // Every mbarrier wait is bounded; a wait that gives up records B200Q_ETIMEOUT,
@@ -45,10 +48,10 @@ namespace qwq {
 namespace {
 
 constexpr int BM = 128, BK = 128;
-constexpr int kMaxN = 192;                 // rows of x8 per tile
+constexpr int kSlotN = 128, kMaxN = 2 * kSlotN;   // rows of x8 per accumulator, per tile
 constexpr int kProducers = 3, kWMma = 3, kWDeq = 4;
-constexpr int kEpiWarps = 4;
-constexpr int kTmemCols = 512, kAccBase = 128, kAccStride = kMaxN;   // A ring: columns 0..127
+constexpr int kEpiWarps = 8;
+constexpr int kTmemCols = 512, kAccBase = 128, kSlots = 3;   // A ring: columns 0..127, then three accumulators
 constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 120 * 1024;      // one CTA per SM: it takes the whole tensor memory
 constexpr int kMiscBytes = 512 + 2 * kMaxN * 4;   // barriers and counters, row scales of two tiles
@@ -67,6 +70,13 @@ template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GRO
 template <int FMT> struct Roles {
     static constexpr int kWEpi = kWDeq + 4 * Fmt<FMT>::GROUPS;
     static constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
+    // Registers per thread: what a launch of kThreads gets (a multiple of 8),
+    // and its split between the producers' and MMA issuer's warpgroup, the
+    // dequantizers' and the epilogue's two.
+    static constexpr int kWarpgroups = kThreads / 128;
+    static constexpr int kRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kRegsLow = 40, kRegsDeq = Fmt<FMT>::GROUPS == 4 ? 56 : 88, kRegsEpi = Fmt<FMT>::GROUPS == 4 ? 120 : 128;
+    static_assert(kRegsLow + Fmt<FMT>::GROUPS * kRegsDeq + 2 * kRegsEpi <= kWarpgroups * kRegs, "register split");
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -132,6 +142,9 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+// One decision for the warp after a wait, and its lanes meet again.
+__device__ __forceinline__ bool together(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -174,7 +187,10 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                  : "memory");
 }
 
+// tcgen05.ld / st are warp instructions (.sync.aligned): the lanes meet before
+// each, since waits and branches of the activations may have parted them.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    __syncwarp();
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
             taddr),
@@ -185,6 +201,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -224,11 +241,16 @@ __device__ __forceinline__ bool cnt_wait(uint32_t addr, uint32_t want, volatile 
     }
 }
 
-__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// bar.sync / bar.red are aligned too.
+__device__ __forceinline__ void named_sync(int id, int n) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
 
 // A named barrier that also ORs a predicate over its threads.
 __device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
         : "=r"(r)
@@ -429,8 +451,8 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     float *xs_s = reinterpret_cast<float *>(c_s + kStages * C_BYTES);      // [2][kMaxN] row scales of a tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(xs_s + 2 * kMaxN);
     uint64_t *full = bars, *done = bars + kMaxStages;      // per stage: copies landed; MMAs finished
-    uint64_t *acc_full = done + kMaxStages, *acc_empty = acc_full + 2;
-    uint32_t *a_ready = reinterpret_cast<uint32_t *>(acc_empty + 2);       // [4] warps that have filled A buffer g, counted on
+    uint64_t *acc_full = done + kMaxStages, *acc_empty = acc_full + kSlots;
+    uint32_t *a_ready = reinterpret_cast<uint32_t *>(acc_empty + kSlots);       // [4] warps that have filled A buffer g, counted on
     uint32_t *tmem_slot = a_ready + 4;
     volatile int *abort = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *last_flag = abort + 1;
@@ -444,7 +466,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             mbar_init(smem_u32(&done[s]), 1);
         }
         for (int s = 0; s < kNumA; ++s) a_ready[s] = 0;
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kSlots; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
             mbar_init(smem_u32(&acc_empty[b]), kEpiWarps);
         }
@@ -462,6 +484,10 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+    if (warp < kWDeq) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<FMT>::kRegsLow));
+    else if (warp < kWEpi) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<FMT>::kRegsDeq));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<FMT>::kRegsEpi));
+
     if (warp < kProducers) {
         // ---------------- TMA producers: warp 0 the rows of x8, warps 1 and 2 a box of codes each.
         // The whole warp walks the items (so that addresses stay in uniform registers), one lane issues.
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
         const int n = (int)(i1 - i0);
         for (int i = 0; i < n; ++i) {
-            if (!mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort)) break;
+            if (!together(mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort))) break;
             const uint32_t bar = smem_u32(&full[stage]);
             const int row = warp == 0 ? nt * p.N : GLU ? mt * 64 : mt * 128 + (warp - 1) * 64;
             if (leader) {
@@ -498,22 +524,34 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     } else if (warp == kWMma) {
         // ---------------- MMA issuer: the whole warp walks the items, one lane issues
         const bool leader = elect_one();
-        const uint32_t idesc = idesc_e4m3(p.N);
+        const int n0 = p.N <= kSlotN ? p.N : (p.N + 31) / 32 * 16, n1 = p.N - n0;     // rows of the one or two accumulators
+        const uint32_t idesc0 = idesc_e4m3(n0), idesc1 = idesc_e4m3(n1);
         const uint64_t desc0 = sw128_desc(smem_u32(b_s));
-        int stage = 0, abuf = 0, t = 0;
-        uint32_t phase = 0, ready = 4;
+        const uint32_t half = (uint32_t)(n0 * BK) >> 4;
+        int stage = 0, abuf = 0, slot = 0;
+        uint32_t phase = 0, ready = 4, sphase = 0;         // sphase: bit per accumulator
         int kb = (int)(i0 % p.nk);
         bool first = true;
-        uint32_t d_tmem = 0;
+        uint32_t d0 = 0, d1 = 0, s0 = 0, s1 = 0;
         uint32_t seen = cnt_read(smem_u32(&a_ready[0]));
         const int n = (int)(i1 - i0);
         for (int i = 0; i < n; ++i) {
             if (first) {
-                if (!mbar_wait(smem_u32(&acc_empty[t & 1]), ((t >> 1) & 1) ^ 1, abort)) break;
-                d_tmem = tmem_base + kAccBase + (t & 1) * kAccStride;
+                s0 = slot;
+                if (!together(mbar_wait(smem_u32(&acc_empty[s0]), ((sphase >> s0) & 1) ^ 1, abort))) break;
+                sphase ^= 1u << s0;
+                d0 = tmem_base + kAccBase + s0 * kSlotN;
+                if (++slot == kSlots) slot = 0;
+                if (n1) {
+                    s1 = slot;
+                    if (!together(mbar_wait(smem_u32(&acc_empty[s1]), ((sphase >> s1) & 1) ^ 1, abort))) break;
+                    sphase ^= 1u << s1;
+                    d1 = tmem_base + kAccBase + s1 * kSlotN;
+                    if (++slot == kSlots) slot = 0;
+                }
             }
             // the dequantizers arrive only after the item's copies have landed
-            if ((int)(seen - ready) < 0 && !cnt_wait(smem_u32(&a_ready[abuf]), ready, abort)) break;
+            if (!together((int)(seen - ready) >= 0 || cnt_wait(smem_u32(&a_ready[abuf]), ready, abort))) break;
             tc_fence_after();
             const uint32_t a_tmem = tmem_base + abuf * kACols;
             const uint64_t desc = desc0 + (uint64_t)((stage * b_bytes) >> 4);
@@ -524,14 +562,19 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < BK / 32; ++k)
 #pragma unroll
-                    for (int pc = 0; pc < PIECES; ++pc)
-                        mma_f8(d_tmem, a_tmem + 32 * pc + 8 * k, desc + 2 * k, idesc,
-                               (first && k == 0 && pc == 0) ? 0u : 1u);
+                    for (int pc = 0; pc < PIECES; ++pc) {
+                        const uint32_t keep = (first && k == 0 && pc == 0) ? 0u : 1u, at = a_tmem + 32 * pc + 8 * k;
+                        mma_f8(d0, at, desc + 2 * k, idesc0, keep);
+                        if (n1) mma_f8(d1, at, desc + half + 2 * k, idesc1, keep);
+                    }
                 mma_commit(smem_u32(&done[stage]));
-                if (last) mma_commit(smem_u32(&acc_full[t & 1]));
+                if (last) {
+                    mma_commit(smem_u32(&acc_full[s0]));
+                    if (n1) mma_commit(smem_u32(&acc_full[s1]));
+                }
             }
             first = last;
-            if (last) kb = 0, ++t;
+            if (last) kb = 0;
             if (++stage == kStages) stage = 0, phase ^= 1;
         }
         __syncwarp();
@@ -546,18 +589,19 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         int stage = g, fstage = 0;                 // the item's stage; the stage of the buffer's previous item
         uint32_t phase = 0, fphase = 0;
         for (long long i = i0 + g; i < i1; i += kNumA) {
-            if (!mbar_wait(smem_u32(&full[stage]), phase, abort)) break;
+            if (!together(mbar_wait(smem_u32(&full[stage]), phase, abort))) break;
             uint32_t v0[16], v1[16];
             dequant<FMT>(c_s + stage * C_BYTES, row, 0, v0, v1);
             // the buffer is free when the MMAs of its previous item have finished (the barrier cannot
             // run a phase ahead: that takes this item, as kStages >= kNumA)
-            if (i >= i0 + kNumA && !mbar_wait(smem_u32(&done[fstage]), fphase, abort)) break;
+            if (i >= i0 + kNumA && !together(mbar_wait(smem_u32(&done[fstage]), fphase, abort))) break;
             tc_fence_after();
             tmem_st16(tdst, v0);
             if (PIECES == 2) tmem_st16(tdst + 32, v1);
             dequant<FMT>(c_s + stage * C_BYTES, row, 1, v0, v1);
             tmem_st16(tdst + 16, v0);
             if (PIECES == 2) tmem_st16(tdst + 48, v1);
+            __syncwarp();
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             __syncwarp();
@@ -567,43 +611,71 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             if (stage >= kStages) stage -= kStages, phase ^= 1;
         }
     } else {
-        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) ..
-        const int quarter = warp & 3, et = threadIdx.x - kWEpi * 32;
+        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) .., 16 columns at a time, alternately
+        constexpr int kEpi = kEpiWarps * 32;
+        const int quarter = warp & 3, odd = (warp - kWEpi) >> 2, et = threadIdx.x - kWEpi * 32;
         const float unit = FMT == B200Q_I8 ? 512.f : 1.f;      // int8 values are times 2^-9
         const bool up = GLU && lane >= 16;
-        int t = 0;
-        for (long long i = i0; i < i1; ++t) {
+        const int n0 = p.N <= kSlotN ? p.N : (p.N + 31) / 32 * 16;
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase;
+        const int arow = quarter * 32 + lane;
+        int t = 0, slot = 0;
+        uint32_t sphase = 0;
+        bool ok = true;
+        for (long long i = i0; i < i1 && ok; ++t) {
             const int tile = (int)(i / p.nk);
             const long long t0 = (long long)tile * p.nk, t1 = t0 + p.nk;
             const long long end = t1 < i1 ? t1 : i1;
             const bool whole = i == t0 && end == t1;
-            const int mt = tile / p.n_tiles, n0 = (tile - mt * p.n_tiles) * p.N;
-            const int o = GLU ? mt * 64 + quarter * 16 + (lane & 15) : mt * 128 + quarter * 32 + lane;
+            const int mt = tile / p.n_tiles, tok0 = (tile - mt * p.n_tiles) * p.N;
+            const int ns = p.S - tok0 < p.N ? p.S - tok0 : p.N;          // rows of x8 in this tile
+            const int o = GLU ? mt * 64 + quarter * 16 + (lane & 15) : mt * 128 + arow;
             const bool live = o < p.O;
             // the tile's scales and bias, while its MMAs run
             float *xs = xs_s + (t & 1) * kMaxN;
-            for (int c = et; c < p.N; c += kEpiWarps * 32) xs[c] = n0 + c < p.S ? p.xs[n0 + c] : 0.f;
+            for (int c = et; c < p.N; c += kEpi) xs[c] = c < ns ? p.xs[tok0 + c] : 0.f;
             const float sc = live ? (up ? p.scale_u[o] : p.scale_g[o]) * unit : 0.f;
             const float *bias = up ? p.bias_u : p.bias_g;
             const float b = live && bias ? bias[o] : 0.f;
-            // one decision for the four warps, and xs is written
-            if (named_sync_or(1, kEpiWarps * 32, !mbar_wait(smem_u32(&acc_full[t & 1]), (t >> 1) & 1, abort))) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase + (t & 1) * kAccStride;
-            bool emit = whole;
-            int first_c = 0, pieces = 0;
+            // the next accumulator; one decision for all epilogue warps, and xs is written
+            auto take = [&]() {
+                const bool got = mbar_wait(smem_u32(&acc_full[slot]), (sphase >> slot) & 1, abort);
+                if (named_sync_or(1, kEpi, !got)) return false;
+                sphase ^= 1u << slot;
+                tc_fence_after();
+                return true;
+            };
+            auto give = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[slot]));
+                if (++slot == kSlots) slot = 0;
+            };
+            const float4 *planes = nullptr;
+            int pieces = 0;
+            long long pl0 = 0;
             if (!whole) {
-                // this CTA's plane, then the tile's arrival count
-                float *pl = p.planes + ((long long)blockIdx.x * 2 + (i == i0 ? 0 : 1)) * p.N * BM + quarter * 32 + lane;
-                for (int c = 0; c < p.N; c += 16) {
-                    float v[16];
-                    tmem_ld16(taddr + c, v);
+                // this CTA's plane, [N / 4][128 rows] of four columns, then the tile's arrival count; the CTA
+                // that completes it adds the planes in CTA order
+                float4 *plane = reinterpret_cast<float4 *>(p.planes) +
+                                ((long long)blockIdx.x * 2 + (i == i0 ? 0 : 1)) * (p.N / 4) * BM + arow;
+                for (int c0 = 0; c0 < p.N && ok; c0 += n0) {
+                    ok = take();
+                    if (!ok) break;
+                    const int cn = p.N - c0 < n0 ? p.N - c0 : n0;
+                    for (int c = odd * 16; c < cn; c += 32) {
+                        float v[16];
+                        tmem_ld16(tlane + slot * kSlotN + c, v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pl[(c + j) * BM] = v[j];
+                        for (int j = 0; j < 4; ++j)
+                            plane[((c0 + c) / 4 + j) * BM] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                    give();
                 }
-                first_c = owner_of(p, t0);
+                if (!ok) break;
+                const int first_c = owner_of(p, t0);
                 pieces = owner_of(p, t1 - 1) - first_c + 1;
-                named_sync(1, kEpiWarps * 32);
+                named_sync(1, kEpi);
                 if (et == 0) {
                     const unsigned long long tag = p.token << 10;
                     unsigned long long old = *(volatile unsigned long long *)&p.cnt[tile];
@@ -617,36 +689,49 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     }
                     *last_flag = n == pieces;
                 }
-                named_sync(1, kEpiWarps * 32);
-                emit = *last_flag != 0;
+                named_sync(1, kEpi);
+                i = end;
+                if (!*last_flag) continue;
+                planes = reinterpret_cast<const float4 *>(p.planes) + arow + (long long)first_c * 2 * (p.N / 4) * BM;
+                // only a tile's first CTA can hold it in its second plane
+                pl0 = run_start(p, first_c) / p.nk == tile ? 0 : (long long)(p.N / 4) * BM;
             }
-            if (emit) {
-                const int ns = p.S - n0 < p.N ? p.S - n0 : p.N;      // rows of x8 in this tile
-                for (int c = 0; c < ns; c += 16) {
+            const int step = whole ? n0 : p.N;            // an accumulator at a time, or all planes
+            for (int c0 = 0; c0 < p.N; c0 += step) {
+                if (whole) {
+                    ok = take();
+                    if (!ok) break;
+                }
+                const int cn = min(p.N - c0, step), cl = min(cn, ns - c0);
+                for (int c = odd * 16; c < cl; c += 32) {
                     float v[16];
                     if (whole) {
-                        tmem_ld16(taddr + c, v);
+                        tmem_ld16(tlane + slot * kSlotN + c, v);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                        const float4 *pl = planes + (c / 4) * BM;
+#pragma unroll 1
                         for (int z = 0; z < pieces; ++z) {
-                            const int cc = first_c + z;
-                            const int slot = run_start(p, cc) / p.nk == tile ? 0 : 1;
-                            const float *pl = p.planes + (((long long)cc * 2 + slot) * p.N + c) * BM + quarter * 32 + lane;
+                            const float4 *pz = pl + (z ? (long long)z * 2 * (p.N / 4) * BM : pl0);
+                            float4 q[4];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] += __ldcg(pl + j * BM);
+                            for (int j = 0; j < 4; ++j) q[j] = __ldcg(pz + j * BM);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[4 * j] += q[j].x, v[4 * j + 1] += q[j].y, v[4 * j + 2] += q[j].z, v[4 * j + 3] += q[j].w;
                         }
                     }
-                    finish16<GLU>(p, v, xs + c, sc, b, n0 + c, ns - c, o, live, up);
+                    finish16<GLU>(p, v, xs + c0 + c, sc, b, tok0 + c0 + c, ns - c0 - c, o, live, up);
                 }
+                if (whole) give();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[t & 1]));
+            if (!ok) break;
             i = end;
         }
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -8,7 +8,7 @@
 
 namespace qwq {
 
-// v, activated.  f32 expf / tanhf / erff; for large |v| the exponentials
+// v, activated.  f32 expf / erff; for large |v| the exponentials
 // overflow or vanish to the activation's limits.  __fdividef (2 ulp) gives 0
 // where silu's denominator passes 2^126, v < -87, where silu is below 1e-36.
 template <int ACT>
@@ -16,7 +16,7 @@ __device__ __forceinline__ float act_q8(float v) {
     if constexpr (ACT == B200Q_ACT_RELU) return v < 0.f ? 0.f : v;      // keeps a NaN
     if constexpr (ACT == B200Q_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
     if constexpr (ACT == B200Q_ACT_GELU_TANH)
-        return 0.5f * v * (1.f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
+        return __fdividef(v, 1.f + expf(-1.59576912f * (v + 0.044715f * v * v * v)));    // (1 + tanh a) / 2 = 1 / (1 + e^-2a)
     if constexpr (ACT == B200Q_ACT_SILU) return __fdividef(v, 1.f + expf(-v));
     return v;
 }
