@@ -20,7 +20,9 @@
 //   warps 0-2  TMA producers, one thread each: N rows of x8, and the two boxes
 //              of 64 code rows (128-byte swizzle for x8; a TMA takes its
 //              thread ~160 cycles and an mbarrier test ~290, so one thread
-//              for all three copies of an item would be slower than its MMAs);
+//              for all three copies of an item would be slower than its MMAs).
+//              Codes and x8 have rings of their own: codes are done with when
+//              they are dequantized, x8 when the MMAs have read it;
 //   warp 3     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
 //              tensor memory, B from shared memory); one commit per item frees
 //              both its stage and its A buffer;
@@ -63,20 +65,14 @@ __device__ unsigned int g_q8_err = 0;
 // PIECES: E4M3 values per code.  CB: code bytes per row and k-block.
 // GROUPS: A buffers, and groups of four dequantizing warps (one per tensor-
 // memory lane quarter); group g fills buffer g with every GROUPS-th item.
+// CODES: stages of the ring of code tiles.
 template <int FMT> struct Fmt;
-template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128, GROUPS = 2; };
-template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 4; };
-template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 4; };
+template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128, GROUPS = 2, CODES = 5; };
+template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 4, CODES = 7; };
+template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 4, CODES = 8; };
 template <int FMT> struct Roles {
     static constexpr int kWEpi = kWDeq + 4 * Fmt<FMT>::GROUPS;
     static constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
-    // Registers per thread: what a launch of kThreads gets (a multiple of 8),
-    // and its split between the producers' and MMA issuer's warpgroup, the
-    // dequantizers' and the epilogue's two.
-    static constexpr int kWarpgroups = kThreads / 128;
-    static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kRegsLow = 40, kRegsDeq = Fmt<FMT>::GROUPS == 4 ? 56 : 88, kRegsEpi = Fmt<FMT>::GROUPS == 4 ? 120 : 128;
-    static_assert(kRegsLow + Fmt<FMT>::GROUPS * kRegsDeq + 2 * kRegsEpi <= kWarpgroups * kRegs, "register split");
 };
 
 // ---------------------------------------------------------------- PTX helpers
@@ -104,6 +100,17 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Whether a phase is complete, without waiting at all.
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
@@ -199,7 +206,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    __syncwarp();
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
     __syncwarp();
     asm volatile(
@@ -349,12 +367,14 @@ struct Q8Params {
     unsigned long long token;
     int O, S, N, nk, n_tiles, act, type;
     int stages;
-    long long items;               // tiles * nk
+    int items;                     // tiles * nk
 };
 
-__device__ __forceinline__ long long run_start(const Q8Params &p, int c) { return (long long)c * p.items / gridDim.x; }
-__device__ __forceinline__ int owner_of(const Q8Params &p, long long i) {
-    return (int)(((i + 1) * gridDim.x - 1) / p.items);
+__device__ __forceinline__ int run_start(const Q8Params &p, int c) {
+    return (int)((long long)c * p.items / (long long)gridDim.x);
+}
+__device__ __forceinline__ int owner_of(const Q8Params &p, int i) {
+    return (int)(((i + 1ll) * (long long)gridDim.x - 1) / p.items);
 }
 
 template <class T> __device__ __forceinline__ float widen(T v);
@@ -366,10 +386,10 @@ template <> __device__ __forceinline__ float narrow<float>(float v) { return v; 
 template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Eight values from v[OFF] on: v += res, then y, for tokens s0, s0 + step, ...
-// below s0 + left; the loads before the stores.
-template <class T, int OFF>
-__device__ __forceinline__ void put8(const Q8Params &p, float (&v)[16], long long s0, int step, int left, int o) {
+// Eight values: v += res, then y, for tokens s0, s0 + step, ... below s0 + left;
+// the loads before the stores.
+template <class T, int W>
+__device__ __forceinline__ void put8(const Q8Params &p, float (&v)[W], int s0, int step, int left, int o) {
     if (p.res) {
         const T *r = (const T *)p.res + s0 * p.ldr + o;
         const long long d = step * p.ldr;
@@ -379,38 +399,33 @@ __device__ __forceinline__ void put8(const Q8Params &p, float (&v)[16], long lon
             if (step * k < left) rv[k] = *r;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (step * k < left) v[OFF + k] += widen<T>(rv[k]);
+            if (step * k < left) v[k] += widen<T>(rv[k]);
     }
     T *y = (T *)p.y + s0 * p.ldy + o;
     const long long d = step * p.ldy;
 #pragma unroll
     for (int k = 0; k < 8; ++k, y += d)
-        if (step * k < left) *y = narrow<T>(v[OFF + k]);
+        if (step * k < left) *y = narrow<T>(v[k]);
 }
 
-template <class T, bool GLU>
-__device__ __forceinline__ void put(const Q8Params &p, float (&v)[16], int s0, int left, int o) {
-    put8<T, 0>(p, v, s0, GLU ? 2 : 1, left, o);
-    if (!GLU) put8<T, 8>(p, v, s0 + 8, 1, left - 8, o);
-}
-
-// 16 accumulator columns (tokens s0 ..; left: how many exist) of this lane's
-// row -> y.  The pair: lanes 0-15 hold gate rows, lanes 16-31 the up rows of
-// the same outputs; of two neighbouring columns the lower lane finishes the
-// first and the upper lane the second, one shuffle for both.
-template <bool GLU>
-__device__ __forceinline__ void finish16(const Q8Params &p, float (&v)[16], const float *xs, float sc, float b, int s0,
-                                         int left, int o, bool live, bool up) {
+// W accumulator columns (tokens s0 ..; left: how many exist) of this lane's row
+// -> eight values of y.  The product takes 8 columns.  The pair takes 16: lanes
+// 0-15 hold gate rows, lanes 16-31 the up rows of the same outputs; of two
+// neighbouring columns the lower lane finishes the first and the upper lane the
+// second, one shuffle for both.
+template <bool GLU, int W>
+__device__ __forceinline__ void finish(const Q8Params &p, float (&v)[W], const float *xs, float sc, float b, int s0,
+                                       int left, int o, bool live, bool up) {
+    static_assert(W == (GLU ? 16 : 8), "columns");
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
+    for (int j = 0; j < W; j += 4) {
         const float4 x = *reinterpret_cast<const float4 *>(xs + j);
         v[j] = fmaf(v[j], x.x * sc, b);
         v[j + 1] = fmaf(v[j + 1], x.y * sc, b);
         v[j + 2] = fmaf(v[j + 2], x.z * sc, b);
         v[j + 3] = fmaf(v[j + 3], x.w * sc, b);
     }
-    constexpr int K = GLU ? 8 : 16;
-    float u[K];
+    float u[8];
     if constexpr (GLU) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -421,19 +436,19 @@ __device__ __forceinline__ void finish16(const Q8Params &p, float (&v)[16], cons
         s0 += up, left -= up;
     }
     switch (p.act) {
-    case B200Q_ACT_RELU: act_n<B200Q_ACT_RELU, K>(v); break;
-    case B200Q_ACT_GELU: act_n<B200Q_ACT_GELU, K>(v); break;
-    case B200Q_ACT_GELU_TANH: act_n<B200Q_ACT_GELU_TANH, K>(v); break;
-    case B200Q_ACT_SILU: act_n<B200Q_ACT_SILU, K>(v); break;
+    case B200Q_ACT_RELU: act_n<B200Q_ACT_RELU, 8>(v); break;
+    case B200Q_ACT_GELU: act_n<B200Q_ACT_GELU, 8>(v); break;
+    case B200Q_ACT_GELU_TANH: act_n<B200Q_ACT_GELU_TANH, 8>(v); break;
+    case B200Q_ACT_SILU: act_n<B200Q_ACT_SILU, 8>(v); break;
     }
     if constexpr (GLU) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) v[j] *= u[j];
+        for (int j = 0; j < 8; ++j) v[j] *= u[j];
     }
     if (!live) return;
-    if (p.type == B200Q_T_F32) put<float, GLU>(p, v, s0, left, o);
-    else if (p.type == B200Q_T_F16) put<__half, GLU>(p, v, s0, left, o);
-    else put<__nv_bfloat16, GLU>(p, v, s0, left, o);
+    if (p.type == B200Q_T_F32) put8<float>(p, v, s0, GLU ? 2 : 1, left, o);
+    else if (p.type == B200Q_T_F16) put8<__half>(p, v, s0, GLU ? 2 : 1, left, o);
+    else put8<__nv_bfloat16>(p, v, s0, GLU ? 2 : 1, left, o);
 }
 
 template <int FMT, bool GLU>
@@ -441,29 +456,34 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     qgemm_q8_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_u,
                     const __grid_constant__ CUtensorMap map_x, const Q8Params p) {
     constexpr int PIECES = Fmt<FMT>::PIECES, CB = Fmt<FMT>::CB, C_BYTES = BM * CB;
-    constexpr int kACols = 32 * PIECES, kNumA = Fmt<FMT>::GROUPS, kWEpi = Roles<FMT>::kWEpi;
+    constexpr int kCodes = Fmt<FMT>::CODES, kACols = 32 * PIECES, kNumA = Fmt<FMT>::GROUPS, kWEpi = Roles<FMT>::kWEpi;
     static_assert(kACols * kNumA <= kAccBase, "A ring");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int b_bytes = p.N * BK, kStages = p.stages;
     uint8_t *b_s = smem;                                  // [stages][N][128], 128-byte swizzle
-    uint8_t *c_s = b_s + kStages * b_bytes;               // [stages][128][CB], CB-byte swizzle
-    float *xs_s = reinterpret_cast<float *>(c_s + kStages * C_BYTES);      // [2][kMaxN] row scales of a tile
+    uint8_t *c_s = b_s + kStages * b_bytes;               // [kCodes][128][CB], CB-byte swizzle
+    float *xs_s = reinterpret_cast<float *>(c_s + kCodes * C_BYTES);       // [2][kMaxN] row scales of a tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(xs_s + 2 * kMaxN);
-    uint64_t *full = bars, *done = bars + kMaxStages;      // per stage: copies landed; MMAs finished
-    uint64_t *acc_full = done + kMaxStages, *acc_empty = acc_full + kSlots;
+    uint64_t *full = bars, *done = bars + kMaxStages;      // per stage of x8: copy landed; MMAs finished
+    uint64_t *c_full = done + kMaxStages, *c_free = c_full + kCodes;       // per stage of codes: copies landed; read
+    uint64_t *acc_full = c_free + kCodes, *acc_empty = acc_full + kSlots;
     uint32_t *a_ready = reinterpret_cast<uint32_t *>(acc_empty + kSlots);       // [4] warps that have filled A buffer g, counted on
     uint32_t *tmem_slot = a_ready + 4;
     volatile int *abort = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *last_flag = abort + 1;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: uniform
-    const long long i0 = run_start(p, blockIdx.x), i1 = run_start(p, blockIdx.x + 1);
+    const int i0 = run_start(p, blockIdx.x), i1 = run_start(p, blockIdx.x + 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&full[s]), kProducers);
+            mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&done[s]), 1);
+        }
+        for (int s = 0; s < kCodes; ++s) {
+            mbar_init(smem_u32(&c_full[s]), 2);
+            mbar_init(smem_u32(&c_free[s]), 4);
         }
         for (int s = 0; s < kNumA; ++s) a_ready[s] = 0;
         for (int b = 0; b < kSlots; ++b) {
@@ -484,10 +504,6 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-    if (warp < kWDeq) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<FMT>::kRegsLow));
-    else if (warp < kWEpi) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<FMT>::kRegsDeq));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<FMT>::kRegsEpi));
-
     if (warp < kProducers) {
         // ---------------- TMA producers: warp 0 the rows of x8, warps 1 and 2 a box of codes each.
         // The whole warp walks the items (so that addresses stay in uniform registers), one lane issues.
@@ -496,22 +512,24 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         const CUtensorMap *map = warp == 0 ? &map_x : GLU && warp == 2 ? &map_u : &map_g;
         const uint32_t dst0 = warp == 0 ? smem_u32(b_s) : smem_u32(c_s + (warp - 1) * (C_BYTES / 2));
         const uint32_t step = warp == 0 ? (uint32_t)b_bytes : (uint32_t)C_BYTES;
+        const int stages = warp == 0 ? kStages : kCodes;
+        uint64_t *landed = warp == 0 ? full : c_full, *free = warp == 0 ? done : c_free;
         const int kcols = warp == 0 ? BK : CB;
         int stage = 0, issued = 0;
         uint32_t phase = 0;
-        int tile = (int)(i0 / p.nk), kb = (int)(i0 % p.nk);
+        int tile = i0 / p.nk, kb = i0 % p.nk;
         int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
-        const int n = (int)(i1 - i0);
+        const int n = i1 - i0;
         for (int i = 0; i < n; ++i) {
-            if (!together(mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort))) break;
-            const uint32_t bar = smem_u32(&full[stage]);
+            if (!together(mbar_wait(smem_u32(&free[stage]), phase ^ 1, abort))) break;
+            const uint32_t bar = smem_u32(&landed[stage]);
             const int row = warp == 0 ? nt * p.N : GLU ? mt * 64 : mt * 128 + (warp - 1) * 64;
             if (leader) {
                 mbar_expect_tx(bar, bytes);
                 tma_load_2d(dst0 + stage * step, map, kb * kcols, row, bar);
             }
             ++issued;
-            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (++stage == stages) stage = 0, phase ^= 1;
             if (++kb == p.nk) {
                 kb = 0;
                 if (++nt == p.n_tiles) nt = 0, ++mt;
@@ -519,8 +537,8 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         }
         __syncwarp();
         // the last copies land before the CTA may leave (a completed phase returns at once)
-        for (int k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
-            mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
+        for (int k = issued < stages ? 0 : issued - stages; k < issued; ++k)
+            mbar_drain(smem_u32(&landed[k % stages]), (uint32_t)((k / stages) & 1));
     } else if (warp == kWMma) {
         // ---------------- MMA issuer: the whole warp walks the items, one lane issues
         const bool leader = elect_one();
@@ -530,11 +548,12 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         const uint32_t half = (uint32_t)(n0 * BK) >> 4;
         int stage = 0, abuf = 0, slot = 0;
         uint32_t phase = 0, ready = 4, sphase = 0;         // sphase: bit per accumulator
-        int kb = (int)(i0 % p.nk);
+        int kb = i0 % p.nk;
         bool first = true;
         uint32_t d0 = 0, d1 = 0, s0 = 0, s1 = 0;
         uint32_t seen = cnt_read(smem_u32(&a_ready[0]));
-        const int n = (int)(i1 - i0);
+        bool seen_b = mbar_peek(smem_u32(&full[0]), 0);
+        const int n = i1 - i0;
         for (int i = 0; i < n; ++i) {
             if (first) {
                 s0 = slot;
@@ -550,13 +569,18 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     if (++slot == kSlots) slot = 0;
                 }
             }
-            // the dequantizers arrive only after the item's copies have landed
-            if (!together((int)(seen - ready) >= 0 || cnt_wait(smem_u32(&a_ready[abuf]), ready, abort))) break;
+            if (!together(((int)(seen - ready) >= 0 || cnt_wait(smem_u32(&a_ready[abuf]), ready, abort)) &&
+                          (seen_b || mbar_wait(smem_u32(&full[stage]), phase, abort))))
+                break;
             tc_fence_after();
             const uint32_t a_tmem = tmem_base + abuf * kACols;
             const uint64_t desc = desc0 + (uint64_t)((stage * b_bytes) >> 4);
             if (++abuf == kNumA) abuf = 0, ready += 4;
-            seen = cnt_read(smem_u32(&a_ready[abuf]));      // the next item's, its latency under these MMAs
+            const int cur = stage;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            // the next item's, their latency under these MMAs
+            seen = cnt_read(smem_u32(&a_ready[abuf]));
+            seen_b = mbar_peek(smem_u32(&full[stage]), phase);
             const bool last = ++kb == p.nk || i + 1 == n;
             if (leader) {
 #pragma unroll
@@ -567,7 +591,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                         mma_f8(d0, at, desc + 2 * k, idesc0, keep);
                         if (n1) mma_f8(d1, at, desc + half + 2 * k, idesc1, keep);
                     }
-                mma_commit(smem_u32(&done[stage]));
+                mma_commit(smem_u32(&done[cur]));
                 if (last) {
                     mma_commit(smem_u32(&acc_full[s0]));
                     if (n1) mma_commit(smem_u32(&acc_full[s1]));
@@ -575,30 +599,35 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             }
             first = last;
             if (last) kb = 0;
-            if (++stage == kStages) stage = 0, phase ^= 1;
         }
         __syncwarp();
-        // MMAs issued before giving up must finish before tensor memory is freed
-        if (*abort) mbar_drain(smem_u32(&done[stage ? stage - 1 : kStages - 1]), stage ? phase : phase ^ 1);
+        // the MMAs issued and their arrivals in shared memory, also those before giving up, land before the CTA may leave
+        mbar_drain(smem_u32(&done[stage ? stage - 1 : kStages - 1]), stage ? phase : phase ^ 1);
     } else if (warp < kWEpi) {
         // ---------------- dequantizers: group g, items g, g + GROUPS, ..., one thread per row
         const int quarter = warp & 3, g = (warp - kWDeq) >> 2;
         // shared-memory row of this thread's lane (the pair: 16 gate rows, then 16 up rows per quarter)
         const int row = GLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
         const uint32_t tdst = tmem_base + ((uint32_t)(quarter * 32) << 16) + g * kACols;
-        int stage = g, fstage = 0;                 // the item's stage; the stage of the buffer's previous item
+        int stage = g, fstage = g;                 // the item's code stage; the x8 stage of the buffer's previous item
         uint32_t phase = 0, fphase = 0;
-        for (long long i = i0 + g; i < i1; i += kNumA) {
-            if (!together(mbar_wait(smem_u32(&full[stage]), phase, abort))) break;
+        for (int i = i0 + g; i < i1; i += kNumA) {
+            if (!together(mbar_wait(smem_u32(&c_full[stage]), phase, abort))) break;
             uint32_t v0[16], v1[16];
             dequant<FMT>(c_s + stage * C_BYTES, row, 0, v0, v1);
             // the buffer is free when the MMAs of its previous item have finished (the barrier cannot
             // run a phase ahead: that takes this item, as kStages >= kNumA)
-            if (i >= i0 + kNumA && !together(mbar_wait(smem_u32(&done[fstage]), fphase, abort))) break;
+            if (i >= i0 + kNumA) {
+                if (!together(mbar_wait(smem_u32(&done[fstage]), fphase, abort))) break;
+                fstage += kNumA;
+                if (fstage >= kStages) fstage -= kStages, fphase ^= 1;
+            }
             tc_fence_after();
             tmem_st16(tdst, v0);
             if (PIECES == 2) tmem_st16(tdst + 32, v1);
             dequant<FMT>(c_s + stage * C_BYTES, row, 1, v0, v1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c_free[stage]));
             tmem_st16(tdst + 16, v0);
             if (PIECES == 2) tmem_st16(tdst + 48, v1);
             __syncwarp();
@@ -606,13 +635,12 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) cnt_add(smem_u32(&a_ready[g]));
-            fstage = stage, fphase = phase;
             stage += kNumA;
-            if (stage >= kStages) stage -= kStages, phase ^= 1;
+            if (stage >= kCodes) stage -= kCodes, phase ^= 1;
         }
     } else {
-        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) .., 16 columns at a time, alternately
-        constexpr int kEpi = kEpiWarps * 32;
+        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) .., W columns at a time, the two warps alternately
+        constexpr int kEpi = kEpiWarps * 32, W = GLU ? 16 : 8, kStep = W * kEpiWarps / 4;
         const int quarter = warp & 3, odd = (warp - kWEpi) >> 2, et = threadIdx.x - kWEpi * 32;
         const float unit = FMT == B200Q_I8 ? 512.f : 1.f;      // int8 values are times 2^-9
         const bool up = GLU && lane >= 16;
@@ -622,10 +650,9 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         int t = 0, slot = 0;
         uint32_t sphase = 0;
         bool ok = true;
-        for (long long i = i0; i < i1 && ok; ++t) {
-            const int tile = (int)(i / p.nk);
-            const long long t0 = (long long)tile * p.nk, t1 = t0 + p.nk;
-            const long long end = t1 < i1 ? t1 : i1;
+        for (int i = i0; i < i1 && ok; ++t) {
+            const int tile = i / p.nk, t0 = tile * p.nk, t1 = t0 + p.nk;
+            const int end = min(t1, i1);
             const bool whole = i == t0 && end == t1;
             const int mt = tile / p.n_tiles, tok0 = (tile - mt * p.n_tiles) * p.N;
             const int ns = p.S - tok0 < p.N ? p.S - tok0 : p.N;          // rows of x8 in this tile
@@ -663,11 +690,11 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     ok = take();
                     if (!ok) break;
                     const int cn = p.N - c0 < n0 ? p.N - c0 : n0;
-                    for (int c = odd * 16; c < cn; c += 32) {
-                        float v[16];
-                        tmem_ld16(tlane + slot * kSlotN + c, v);
+                    for (int c = odd * W; c < cn; c += kStep) {
+                        float v[W];
+                        tmem_ld(tlane + slot * kSlotN + c, v);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < W / 4; ++j)
                             plane[((c0 + c) / 4 + j) * BM] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     }
                     give();
@@ -703,26 +730,26 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     if (!ok) break;
                 }
                 const int cn = min(p.N - c0, step), cl = min(cn, ns - c0);
-                for (int c = odd * 16; c < cl; c += 32) {
-                    float v[16];
+                for (int c = odd * W; c < cl; c += kStep) {
+                    float v[W];
                     if (whole) {
-                        tmem_ld16(tlane + slot * kSlotN + c, v);
+                        tmem_ld(tlane + slot * kSlotN + c, v);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                        for (int j = 0; j < W; ++j) v[j] = 0.f;
                         const float4 *pl = planes + (c / 4) * BM;
 #pragma unroll 1
                         for (int z = 0; z < pieces; ++z) {
                             const float4 *pz = pl + (z ? (long long)z * 2 * (p.N / 4) * BM : pl0);
-                            float4 q[4];
+                            float4 q[W / 4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) q[j] = __ldcg(pz + j * BM);
+                            for (int j = 0; j < W / 4; ++j) q[j] = __ldcg(pz + j * BM);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                            for (int j = 0; j < W / 4; ++j)
                                 v[4 * j] += q[j].x, v[4 * j + 1] += q[j].y, v[4 * j + 2] += q[j].z, v[4 * j + 3] += q[j].w;
                         }
                     }
-                    finish16<GLU>(p, v, xs + c0 + c, sc, b, tok0 + c0 + c, ns - c0 - c, o, live, up);
+                    finish<GLU>(p, v, xs + c0 + c, sc, b, tok0 + c0 + c, ns - c0 - c, o, live, up);
                 }
                 if (whole) give();
             }
@@ -772,17 +799,18 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     p.type = a.type;
     const long long m_tiles = GLU ? (t.O + 63) / 64 : (t.O + 127) / 128;
     const long long tiles = m_tiles * p.n_tiles;
-    if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
-    p.items = tiles * p.nk;
+    if (tiles * p.nk > 0x7ffffff0ll) return cudaErrorInvalidValue;
+    p.items = (int)(tiles * p.nk);
     // at least four k-blocks per CTA
     const int n_sms = sm_count(t.device);
-    long long grid = (p.items + 3) / 4;
+    long long grid = (p.items + 3ll) / 4;
     if (grid > n_sms) grid = n_sms;
-    const int per = N * BK + C_BYTES;
-    int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
+    constexpr int kFixed = 1024 + Fmt<FMT>::CODES * C_BYTES + kMiscBytes;
+    static_assert((kSmemLimit - kFixed) / (kMaxN * BK) >= Fmt<FMT>::GROUPS && Fmt<FMT>::CODES >= Fmt<FMT>::GROUPS, "rings");
+    int stages = (kSmemLimit - kFixed) / (N * BK);
     if (stages > kMaxStages) stages = kMaxStages;
     p.stages = stages;
-    size_t smem = 1024 + (size_t)stages * per + kMiscBytes;
+    size_t smem = kFixed + (size_t)stages * N * BK;
     if (smem < kSmemFloor) smem = kSmemFloor;
     cudaError_t e = allow_dynamic_smem((const void *)qgemm_q8_kernel<FMT, GLU>, kSmemLimit);
     if (e != cudaSuccess) return e;
@@ -822,12 +850,25 @@ bool q8_map_encode(Tensor &t) {
 }
 
 cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st) {
-    switch (a.tg->fmt) {
-    case B200Q_I8: return a.tu ? run<B200Q_I8, true>(a, st) : run<B200Q_I8, false>(a, st);
-    case B200Q_I4: return a.tu ? run<B200Q_I4, true>(a, st) : run<B200Q_I4, false>(a, st);
-    case B200Q_I2: return a.tu ? run<B200Q_I2, true>(a, st) : run<B200Q_I2, false>(a, st);
+    // item numbers are 32-bit: longer batches in parts
+    constexpr int kRows = 1 << 16;
+    const long long b = a.type == B200Q_T_F32 ? 4 : 2;
+    for (int s0 = 0; s0 < a.S; s0 += kRows) {
+        MatQ8 c = a;
+        c.S = a.S - s0 < kRows ? a.S - s0 : kRows;
+        c.x8 += s0 * a.ld8;
+        c.xs += s0;
+        c.y = (char *)a.y + s0 * a.ldy * b;
+        if (a.res) c.res = (const char *)a.res + s0 * a.ldr * b;
+        cudaError_t e = cudaErrorInvalidValue;
+        switch (a.tg->fmt) {
+        case B200Q_I8: e = a.tu ? run<B200Q_I8, true>(c, st) : run<B200Q_I8, false>(c, st); break;
+        case B200Q_I4: e = a.tu ? run<B200Q_I4, true>(c, st) : run<B200Q_I4, false>(c, st); break;
+        case B200Q_I2: e = a.tu ? run<B200Q_I2, true>(c, st) : run<B200Q_I2, false>(c, st); break;
+        }
+        if (e != cudaSuccess) return e;
     }
-    return cudaErrorInvalidValue;
+    return cudaSuccess;
 }
 
 cudaError_t q8_take_error(unsigned int *code) {
