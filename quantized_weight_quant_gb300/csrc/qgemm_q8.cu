@@ -20,20 +20,15 @@
 //   warps 0-2  TMA producers, one thread each: N rows of x8, and the two boxes
 //              of 64 code rows (128-byte swizzle for x8; a TMA takes its
 //              thread ~160 cycles and an mbarrier test ~290, so one thread
-//              for all three copies of an item would be slower than its MMAs).
-//              Codes and x8 have rings of their own: codes are done with when
-//              they are dequantized, x8 when the MMAs have read it;
+//              for all three copies of an item would be slower than its MMAs);
 //   warp 3     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
-//              tensor memory, B from shared memory); one commit per item frees
-//              both its stage and its A buffer;
+//              tensor memory, B from shared memory) into one of two
+//              accumulators; one commit per item frees both its stage and its
+//              A buffer;
 //   warps 4 .. dequantizers, in groups of four: codes -> E4M3 bytes by a
 //              16-entry table lookup in registers (byte permutes), stored to
 //              the group's A buffer in tensor memory, natural K order;
-//   last eight epilogue, two warps per lane quarter.
-// A tile of more than 128 rows of x8 takes two accumulators, so that one
-// dequantized A serves up to 256 rows (at 192, dequantizing and shared memory,
-// not the MMAs, set the time of an item).  Three accumulators take turns: the
-// next tile's MMAs start when the first of its two is drained.
+//   last four  epilogue.
 // The gated pair takes 64 gate and 64 up rows per tile, interleaved by 16 in
 // the lanes, so that a gate and its up value sit in one warp, 16 lanes apart.
 // Every mbarrier wait is bounded; a wait that gives up records B200Q_ETIMEOUT,
@@ -50,10 +45,10 @@ namespace qwq {
 namespace {
 
 constexpr int BM = 128, BK = 128;
-constexpr int kSlotN = 128, kMaxN = 2 * kSlotN;   // rows of x8 per accumulator, per tile
+constexpr int kMaxN = 192;                 // rows of x8 per tile
 constexpr int kProducers = 3, kWMma = 3, kWDeq = 4;
-constexpr int kEpiWarps = 8;
-constexpr int kTmemCols = 512, kAccBase = 128, kSlots = 3;   // A ring: columns 0..127, then three accumulators
+constexpr int kEpiWarps = 4;
+constexpr int kTmemCols = 512, kAccBase = 128, kAccStride = kMaxN;   // A ring: columns 0..127
 constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 120 * 1024;      // one CTA per SM: it takes the whole tensor memory
 constexpr int kMiscBytes = 512 + 2 * kMaxN * 4;   // barriers and counters, row scales of two tiles
@@ -65,11 +60,10 @@ __device__ unsigned int g_q8_err = 0;
 // PIECES: E4M3 values per code.  CB: code bytes per row and k-block.
 // GROUPS: A buffers, and groups of four dequantizing warps (one per tensor-
 // memory lane quarter); group g fills buffer g with every GROUPS-th item.
-// CODES: stages of the ring of code tiles.
 template <int FMT> struct Fmt;
-template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128, GROUPS = 2, CODES = 5; };
-template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 4, CODES = 7; };
-template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 4, CODES = 8; };
+template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128, GROUPS = 2; };
+template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 4; };
+template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 4; };
 template <int FMT> struct Roles {
     static constexpr int kWEpi = kWDeq + 4 * Fmt<FMT>::GROUPS;
     static constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
@@ -106,17 +100,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Whether a phase is complete, without waiting at all.
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // Waits for a phase; gives up after kWaitNs, or soon after another role has.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     unsigned long long t0 = 0;
@@ -125,7 +108,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         if ((it & 63) == 63) {
             if (*abort) return false;
             if (t0 == 0) t0 = global_ns();
-            else if (global_ns() - t0 > kWaitNs) {
+            else if ((long long)(global_ns() - t0) > (long long)kWaitNs) {
                 atomicExch(&g_q8_err, (unsigned)(-B200Q_ETIMEOUT));
                 *abort = 1;
                 return false;
@@ -138,7 +121,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // finish before it leaves), for a quarter of kWaitNs at most.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     const unsigned long long t0 = global_ns();
-    while (!mbar_test(bar, parity) && global_ns() - t0 < kWaitNs / 4) {
+    while (!mbar_test(bar, parity) && (long long)(global_ns() - t0) < (long long)(kWaitNs / 4)) {
     }
 }
 
@@ -250,7 +233,7 @@ __device__ __forceinline__ bool cnt_wait(uint32_t addr, uint32_t want, volatile 
         if ((it & 255) == 255) {
             if (*abort) return false;
             if (t0 == 0) t0 = global_ns();
-            else if (global_ns() - t0 > kWaitNs) {
+            else if ((long long)(global_ns() - t0) > (long long)kWaitNs) {
                 atomicExch(&g_q8_err, (unsigned)(-B200Q_ETIMEOUT));
                 *abort = 1;
                 return false;
@@ -327,14 +310,18 @@ __device__ __forceinline__ void lut_i2(uint32_t w, uint32_t *o) {
 
 // The 64 codes of half a row's k-block -> 16 registers per piece.
 template <int FMT>
-__device__ __forceinline__ void dequant(const uint8_t *c_s, int row, int half, uint32_t (&p0)[16], uint32_t (&p1)[16]) {
+__device__ __forceinline__ void dequant(uint32_t c_s, int row, int half, uint32_t (&p0)[16], uint32_t (&p1)[16]) {
     constexpr int CB = Fmt<FMT>::CB, kChunks = CB / 32;      // 16-byte chunks per half row
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
         const int c = half * kChunks + j;
         // the TMA swizzle of rows of CB bytes: chunk index xor bits of the row
         const int pc = CB == 128 ? c ^ (row & 7) : CB == 64 ? c ^ ((row >> 1) & 3) : c ^ ((row >> 2) & 1);
-        const uint4 q = *reinterpret_cast<const uint4 *>(c_s + row * CB + pc * 16);
+        uint4 q;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "r"(c_s + row * CB + pc * 16)
+                     : "memory");
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -456,20 +443,20 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     qgemm_q8_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_u,
                     const __grid_constant__ CUtensorMap map_x, const Q8Params p) {
     constexpr int PIECES = Fmt<FMT>::PIECES, CB = Fmt<FMT>::CB, C_BYTES = BM * CB;
-    constexpr int kCodes = Fmt<FMT>::CODES, kACols = 32 * PIECES, kNumA = Fmt<FMT>::GROUPS, kWEpi = Roles<FMT>::kWEpi;
+    constexpr int kACols = 32 * PIECES, kNumA = Fmt<FMT>::GROUPS, kWEpi = Roles<FMT>::kWEpi;
     static_assert(kACols * kNumA <= kAccBase, "A ring");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int b_bytes = p.N * BK, kStages = p.stages;
     uint8_t *b_s = smem;                                  // [stages][N][128], 128-byte swizzle
-    uint8_t *c_s = b_s + kStages * b_bytes;               // [kCodes][128][CB], CB-byte swizzle
-    float *xs_s = reinterpret_cast<float *>(c_s + kCodes * C_BYTES);       // [2][kMaxN] row scales of a tile
+    uint8_t *c_s = b_s + kStages * b_bytes;               // [stages][128][CB], CB-byte swizzle
+    float *xs_s = reinterpret_cast<float *>(c_s + kStages * C_BYTES);      // [2][kMaxN] row scales of a tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(xs_s + 2 * kMaxN);
-    uint64_t *full = bars, *done = bars + kMaxStages;      // per stage of x8: copy landed; MMAs finished
-    uint64_t *c_full = done + kMaxStages, *c_free = c_full + kCodes;       // per stage of codes: copies landed; read
-    uint64_t *acc_full = c_free + kCodes, *acc_empty = acc_full + kSlots;
-    uint32_t *a_ready = reinterpret_cast<uint32_t *>(acc_empty + kSlots);       // [4] warps that have filled A buffer g, counted on
-    uint32_t *tmem_slot = a_ready + 4;
+    uint64_t *full = bars, *done = bars + kMaxStages;      // per stage: copies landed; MMAs finished
+    uint64_t *acc_full = done + kMaxStages, *acc_empty = acc_full + 2;
+    uint32_t *a_ready = reinterpret_cast<uint32_t *>(acc_empty + 2);       // [4] warps that have filled A buffer g, counted on
+    uint64_t *fin = reinterpret_cast<uint64_t *>(a_ready + 4);             // after the last MMA
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
     volatile int *abort = reinterpret_cast<int *>(tmem_slot + 1);
     volatile int *last_flag = abort + 1;
 
@@ -478,18 +465,15 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&full[s]), kProducers);
             mbar_init(smem_u32(&done[s]), 1);
         }
-        for (int s = 0; s < kCodes; ++s) {
-            mbar_init(smem_u32(&c_full[s]), 2);
-            mbar_init(smem_u32(&c_free[s]), 4);
-        }
         for (int s = 0; s < kNumA; ++s) a_ready[s] = 0;
-        for (int b = 0; b < kSlots; ++b) {
+        for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
             mbar_init(smem_u32(&acc_empty[b]), kEpiWarps);
         }
+        mbar_init(smem_u32(fin), 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -502,7 +486,16 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // all columns are this CTA's, so they start at 0; anything else would be addressed wrongly below
+    constexpr uint32_t tmem_base = 0;
+    if (*tmem_slot != tmem_base) {
+        if (threadIdx.x == 0) atomicExch(&g_q8_err, (unsigned)(-B200Q_ECUDA));
+        __syncthreads();
+        if (warp == kWMma)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols)
+                         : "memory");
+        return;
+    }
 
     if (warp < kProducers) {
         // ---------------- TMA producers: warp 0 the rows of x8, warps 1 and 2 a box of codes each.
@@ -512,8 +505,6 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         const CUtensorMap *map = warp == 0 ? &map_x : GLU && warp == 2 ? &map_u : &map_g;
         const uint32_t dst0 = warp == 0 ? smem_u32(b_s) : smem_u32(c_s + (warp - 1) * (C_BYTES / 2));
         const uint32_t step = warp == 0 ? (uint32_t)b_bytes : (uint32_t)C_BYTES;
-        const int stages = warp == 0 ? kStages : kCodes;
-        uint64_t *landed = warp == 0 ? full : c_full, *free = warp == 0 ? done : c_free;
         const int kcols = warp == 0 ? BK : CB;
         int stage = 0, issued = 0;
         uint32_t phase = 0;
@@ -521,15 +512,15 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
         const int n = i1 - i0;
         for (int i = 0; i < n; ++i) {
-            if (!together(mbar_wait(smem_u32(&free[stage]), phase ^ 1, abort))) break;
-            const uint32_t bar = smem_u32(&landed[stage]);
+            if (!together(mbar_wait(smem_u32(&done[stage]), phase ^ 1, abort))) break;
+            const uint32_t bar = smem_u32(&full[stage]);
             const int row = warp == 0 ? nt * p.N : GLU ? mt * 64 : mt * 128 + (warp - 1) * 64;
             if (leader) {
                 mbar_expect_tx(bar, bytes);
                 tma_load_2d(dst0 + stage * step, map, kb * kcols, row, bar);
             }
             ++issued;
-            if (++stage == stages) stage = 0, phase ^= 1;
+            if (++stage == kStages) stage = 0, phase ^= 1;
             if (++kb == p.nk) {
                 kb = 0;
                 if (++nt == p.n_tiles) nt = 0, ++mt;
@@ -537,97 +528,70 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         }
         __syncwarp();
         // the last copies land before the CTA may leave (a completed phase returns at once)
-        for (int k = issued < stages ? 0 : issued - stages; k < issued; ++k)
-            mbar_drain(smem_u32(&landed[k % stages]), (uint32_t)((k / stages) & 1));
+        for (int k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
+            mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
     } else if (warp == kWMma) {
         // ---------------- MMA issuer: the whole warp walks the items, one lane issues
         const bool leader = elect_one();
-        const int n0 = p.N <= kSlotN ? p.N : (p.N + 31) / 32 * 16, n1 = p.N - n0;     // rows of the one or two accumulators
-        const uint32_t idesc0 = idesc_e4m3(n0), idesc1 = idesc_e4m3(n1);
+        const uint32_t idesc = idesc_e4m3(p.N);
         const uint64_t desc0 = sw128_desc(smem_u32(b_s));
-        const uint32_t half = (uint32_t)(n0 * BK) >> 4;
-        int stage = 0, abuf = 0, slot = 0;
-        uint32_t phase = 0, ready = 4, sphase = 0;         // sphase: bit per accumulator
+        int stage = 0, abuf = 0, t = 0;
+        uint32_t phase = 0, ready = 4;
         int kb = i0 % p.nk;
         bool first = true;
-        uint32_t d0 = 0, d1 = 0, s0 = 0, s1 = 0;
+        uint32_t d_tmem = 0;
         uint32_t seen = cnt_read(smem_u32(&a_ready[0]));
-        bool seen_b = mbar_peek(smem_u32(&full[0]), 0);
         const int n = i1 - i0;
         for (int i = 0; i < n; ++i) {
             if (first) {
-                s0 = slot;
-                if (!together(mbar_wait(smem_u32(&acc_empty[s0]), ((sphase >> s0) & 1) ^ 1, abort))) break;
-                sphase ^= 1u << s0;
-                d0 = tmem_base + kAccBase + s0 * kSlotN;
-                if (++slot == kSlots) slot = 0;
-                if (n1) {
-                    s1 = slot;
-                    if (!together(mbar_wait(smem_u32(&acc_empty[s1]), ((sphase >> s1) & 1) ^ 1, abort))) break;
-                    sphase ^= 1u << s1;
-                    d1 = tmem_base + kAccBase + s1 * kSlotN;
-                    if (++slot == kSlots) slot = 0;
-                }
+                if (!together(mbar_wait(smem_u32(&acc_empty[t & 1]), ((t >> 1) & 1) ^ 1, abort))) break;
+                d_tmem = tmem_base + kAccBase + (t & 1) * kAccStride;
             }
-            if (!together(((int)(seen - ready) >= 0 || cnt_wait(smem_u32(&a_ready[abuf]), ready, abort)) &&
-                          (seen_b || mbar_wait(smem_u32(&full[stage]), phase, abort))))
-                break;
+            // the dequantizers arrive only after the item's copies have landed
+            if (!together((int)(seen - ready) >= 0 || cnt_wait(smem_u32(&a_ready[abuf]), ready, abort))) break;
             tc_fence_after();
             const uint32_t a_tmem = tmem_base + abuf * kACols;
             const uint64_t desc = desc0 + (uint64_t)((stage * b_bytes) >> 4);
             if (++abuf == kNumA) abuf = 0, ready += 4;
-            const int cur = stage;
-            if (++stage == kStages) stage = 0, phase ^= 1;
-            // the next item's, their latency under these MMAs
-            seen = cnt_read(smem_u32(&a_ready[abuf]));
-            seen_b = mbar_peek(smem_u32(&full[stage]), phase);
+            seen = cnt_read(smem_u32(&a_ready[abuf]));      // the next item's, its latency under these MMAs
             const bool last = ++kb == p.nk || i + 1 == n;
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < BK / 32; ++k)
 #pragma unroll
-                    for (int pc = 0; pc < PIECES; ++pc) {
-                        const uint32_t keep = (first && k == 0 && pc == 0) ? 0u : 1u, at = a_tmem + 32 * pc + 8 * k;
-                        mma_f8(d0, at, desc + 2 * k, idesc0, keep);
-                        if (n1) mma_f8(d1, at, desc + half + 2 * k, idesc1, keep);
-                    }
-                mma_commit(smem_u32(&done[cur]));
-                if (last) {
-                    mma_commit(smem_u32(&acc_full[s0]));
-                    if (n1) mma_commit(smem_u32(&acc_full[s1]));
-                }
+                    for (int pc = 0; pc < PIECES; ++pc)
+                        mma_f8(d_tmem, a_tmem + 32 * pc + 8 * k, desc + 2 * k, idesc,
+                               (first && k == 0 && pc == 0) ? 0u : 1u);
+                mma_commit(smem_u32(&done[stage]));
+                if (last) mma_commit(smem_u32(&acc_full[t & 1]));
             }
             first = last;
-            if (last) kb = 0;
+            if (last) kb = 0, ++t;
+            if (++stage == kStages) stage = 0, phase ^= 1;
         }
+        // everything issued, also before giving up, and its arrivals in shared memory land before the CTA may leave
         __syncwarp();
-        // the MMAs issued and their arrivals in shared memory, also those before giving up, land before the CTA may leave
-        mbar_drain(smem_u32(&done[stage ? stage - 1 : kStages - 1]), stage ? phase : phase ^ 1);
+        if (leader) mma_commit(smem_u32(fin));
+        mbar_drain(smem_u32(fin), 0);
     } else if (warp < kWEpi) {
         // ---------------- dequantizers: group g, items g, g + GROUPS, ..., one thread per row
         const int quarter = warp & 3, g = (warp - kWDeq) >> 2;
         // shared-memory row of this thread's lane (the pair: 16 gate rows, then 16 up rows per quarter)
         const int row = GLU ? (lane >> 4) * 64 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
         const uint32_t tdst = tmem_base + ((uint32_t)(quarter * 32) << 16) + g * kACols;
-        int stage = g, fstage = g;                 // the item's code stage; the x8 stage of the buffer's previous item
+        int stage = g, fstage = 0;                 // the item's stage; the stage of the buffer's previous item
         uint32_t phase = 0, fphase = 0;
         for (int i = i0 + g; i < i1; i += kNumA) {
-            if (!together(mbar_wait(smem_u32(&c_full[stage]), phase, abort))) break;
+            if (!together(mbar_wait(smem_u32(&full[stage]), phase, abort))) break;
             uint32_t v0[16], v1[16];
-            dequant<FMT>(c_s + stage * C_BYTES, row, 0, v0, v1);
+            dequant<FMT>(smem_u32(c_s) + stage * C_BYTES, row, 0, v0, v1);
             // the buffer is free when the MMAs of its previous item have finished (the barrier cannot
             // run a phase ahead: that takes this item, as kStages >= kNumA)
-            if (i >= i0 + kNumA) {
-                if (!together(mbar_wait(smem_u32(&done[fstage]), fphase, abort))) break;
-                fstage += kNumA;
-                if (fstage >= kStages) fstage -= kStages, fphase ^= 1;
-            }
+            if (i >= i0 + kNumA && !together(mbar_wait(smem_u32(&done[fstage]), fphase, abort))) break;
             tc_fence_after();
             tmem_st16(tdst, v0);
             if (PIECES == 2) tmem_st16(tdst + 32, v1);
-            dequant<FMT>(c_s + stage * C_BYTES, row, 1, v0, v1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c_free[stage]));
+            dequant<FMT>(smem_u32(c_s) + stage * C_BYTES, row, 1, v0, v1);
             tmem_st16(tdst + 16, v0);
             if (PIECES == 2) tmem_st16(tdst + 48, v1);
             __syncwarp();
@@ -635,22 +599,19 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) cnt_add(smem_u32(&a_ready[g]));
+            fstage = stage, fphase = phase;
             stage += kNumA;
-            if (stage >= kCodes) stage -= kCodes, phase ^= 1;
+            if (stage >= kStages) stage -= kStages, phase ^= 1;
         }
     } else {
-        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) .., W columns at a time, the two warps alternately
-        constexpr int kEpi = kEpiWarps * 32, W = GLU ? 16 : 8, kStep = W * kEpiWarps / 4;
-        const int quarter = warp & 3, odd = (warp - kWEpi) >> 2, et = threadIdx.x - kWEpi * 32;
+        // ---------------- epilogue: tensor-memory lanes 32 * (warp % 4) .., W columns at a time
+        constexpr int kEpi = kEpiWarps * 32, W = GLU ? 16 : 8;
+        const int quarter = warp & 3, et = threadIdx.x - kWEpi * 32;
         const float unit = FMT == B200Q_I8 ? 512.f : 1.f;      // int8 values are times 2^-9
         const bool up = GLU && lane >= 16;
-        const int n0 = p.N <= kSlotN ? p.N : (p.N + 31) / 32 * 16;
-        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase;
         const int arow = quarter * 32 + lane;
-        int t = 0, slot = 0;
-        uint32_t sphase = 0;
-        bool ok = true;
-        for (int i = i0; i < i1 && ok; ++t) {
+        int t = 0;
+        for (int i = i0; i < i1; ++t) {
             const int tile = i / p.nk, t0 = tile * p.nk, t1 = t0 + p.nk;
             const int end = min(t1, i1);
             const bool whole = i == t0 && end == t1;
@@ -664,42 +625,24 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             const float sc = live ? (up ? p.scale_u[o] : p.scale_g[o]) * unit : 0.f;
             const float *bias = up ? p.bias_u : p.bias_g;
             const float b = live && bias ? bias[o] : 0.f;
-            // the next accumulator; one decision for all epilogue warps, and xs is written
-            auto take = [&]() {
-                const bool got = mbar_wait(smem_u32(&acc_full[slot]), (sphase >> slot) & 1, abort);
-                if (named_sync_or(1, kEpi, !got)) return false;
-                sphase ^= 1u << slot;
-                tc_fence_after();
-                return true;
-            };
-            auto give = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[slot]));
-                if (++slot == kSlots) slot = 0;
-            };
-            const float4 *planes = nullptr;
+            // one decision for the four warps, and xs is written
+            if (named_sync_or(1, kEpi, !mbar_wait(smem_u32(&acc_full[t & 1]), (t >> 1) & 1, abort))) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + kAccBase + (t & 1) * kAccStride;
+            const float *planes = nullptr;
             int pieces = 0;
             long long pl0 = 0;
+            bool emit = whole;
             if (!whole) {
-                // this CTA's plane, [N / 4][128 rows] of four columns, then the tile's arrival count; the CTA
-                // that completes it adds the planes in CTA order
-                float4 *plane = reinterpret_cast<float4 *>(p.planes) +
-                                ((long long)blockIdx.x * 2 + (i == i0 ? 0 : 1)) * (p.N / 4) * BM + arow;
-                for (int c0 = 0; c0 < p.N && ok; c0 += n0) {
-                    ok = take();
-                    if (!ok) break;
-                    const int cn = p.N - c0 < n0 ? p.N - c0 : n0;
-                    for (int c = odd * W; c < cn; c += kStep) {
-                        float v[W];
-                        tmem_ld(tlane + slot * kSlotN + c, v);
+                // this CTA's plane, [N][128 rows], then the tile's arrival count; the CTA that completes it adds
+                // the planes in CTA order
+                float *pl = p.planes + ((long long)blockIdx.x * 2 + (i == i0 ? 0 : 1)) * p.N * BM + arow;
+                for (int c = 0; c < p.N; c += W) {
+                    float v[W];
+                    tmem_ld(taddr + c, v);
 #pragma unroll
-                        for (int j = 0; j < W / 4; ++j)
-                            plane[((c0 + c) / 4 + j) * BM] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    }
-                    give();
+                    for (int j = 0; j < W; ++j) pl[(c + j) * BM] = v[j];
                 }
-                if (!ok) break;
                 const int first_c = owner_of(p, t0);
                 pieces = owner_of(p, t1 - 1) - first_c + 1;
                 named_sync(1, kEpi);
@@ -717,43 +660,35 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     *last_flag = n == pieces;
                 }
                 named_sync(1, kEpi);
-                i = end;
-                if (!*last_flag) continue;
-                planes = reinterpret_cast<const float4 *>(p.planes) + arow + (long long)first_c * 2 * (p.N / 4) * BM;
+                emit = *last_flag != 0;
+                planes = p.planes + arow + (long long)first_c * 2 * p.N * BM;
                 // only a tile's first CTA can hold it in its second plane
-                pl0 = run_start(p, first_c) / p.nk == tile ? 0 : (long long)(p.N / 4) * BM;
+                pl0 = run_start(p, first_c) / p.nk == tile ? 0 : (long long)p.N * BM;
             }
-            const int step = whole ? n0 : p.N;            // an accumulator at a time, or all planes
-            for (int c0 = 0; c0 < p.N; c0 += step) {
-                if (whole) {
-                    ok = take();
-                    if (!ok) break;
-                }
-                const int cn = min(p.N - c0, step), cl = min(cn, ns - c0);
-                for (int c = odd * W; c < cl; c += kStep) {
+            if (emit) {
+                for (int c = 0; c < ns; c += W) {
                     float v[W];
                     if (whole) {
-                        tmem_ld(tlane + slot * kSlotN + c, v);
+                        tmem_ld(taddr + c, v);
                     } else {
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] = 0.f;
-                        const float4 *pl = planes + (c / 4) * BM;
-#pragma unroll 1
+#pragma unroll 2
                         for (int z = 0; z < pieces; ++z) {
-                            const float4 *pz = pl + (z ? (long long)z * 2 * (p.N / 4) * BM : pl0);
-                            float4 q[W / 4];
+                            const float *pz = planes + (z ? (long long)z * 2 * p.N * BM : pl0) + c * BM;
+                            float q[W];
 #pragma unroll
-                            for (int j = 0; j < W / 4; ++j) q[j] = __ldcg(pz + j * BM);
+                            for (int j = 0; j < W; ++j) q[j] = __ldcg(pz + j * BM);
 #pragma unroll
-                            for (int j = 0; j < W / 4; ++j)
-                                v[4 * j] += q[j].x, v[4 * j + 1] += q[j].y, v[4 * j + 2] += q[j].z, v[4 * j + 3] += q[j].w;
+                            for (int j = 0; j < W; ++j) v[j] += q[j];
                         }
                     }
-                    finish<GLU>(p, v, xs + c0 + c, sc, b, tok0 + c0 + c, ns - c0 - c, o, live, up);
+                    finish<GLU>(p, v, xs + c, sc, b, tok0 + c, ns - c, o, live, up);
                 }
-                if (whole) give();
             }
-            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[t & 1]));
             i = end;
         }
     }
@@ -805,12 +740,11 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     const int n_sms = sm_count(t.device);
     long long grid = (p.items + 3ll) / 4;
     if (grid > n_sms) grid = n_sms;
-    constexpr int kFixed = 1024 + Fmt<FMT>::CODES * C_BYTES + kMiscBytes;
-    static_assert((kSmemLimit - kFixed) / (kMaxN * BK) >= Fmt<FMT>::GROUPS && Fmt<FMT>::CODES >= Fmt<FMT>::GROUPS, "rings");
-    int stages = (kSmemLimit - kFixed) / (N * BK);
+    const int per = N * BK + C_BYTES;
+    int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
     if (stages > kMaxStages) stages = kMaxStages;
     p.stages = stages;
-    size_t smem = kFixed + (size_t)stages * N * BK;
+    size_t smem = 1024 + (size_t)stages * per + kMiscBytes;
     if (smem < kSmemFloor) smem = kSmemFloor;
     cudaError_t e = allow_dynamic_smem((const void *)qgemm_q8_kernel<FMT, GLU>, kSmemLimit);
     if (e != cudaSuccess) return e;
