@@ -625,6 +625,13 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
             const float sc = live ? (up ? p.scale_u[o] : p.scale_g[o]) * unit : 0.f;
             const float *bias = up ? p.bias_u : p.bias_g;
             const float b = live && bias ? bias[o] : 0.f;
+            // the residual's lines into L2 while the MMAs run (64 bytes per row and warp)
+            if (p.res && whole) {
+                const int ob = p.type == B200Q_T_F32 ? 4 : 2, o0 = mt * 128 + quarter * 32;
+                if (o0 < p.O)
+                    for (int c = lane; c < ns; c += 32)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"((const char *)p.res + ((tok0 + c) * p.ldr + o0) * ob));
+            }
             // one decision for the four warps, and xs is written
             if (named_sync_or(1, kEpi, !mbar_wait(smem_u32(&acc_full[t & 1]), (t >> 1) & 1, abort))) break;
             tc_fence_after();
@@ -673,7 +680,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     } else {
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
                         for (int z = 0; z < pieces; ++z) {
                             const float *pz = planes + (z ? (long long)z * 2 * p.N * BM : pl0) + c * BM;
                             float q[W];
@@ -740,6 +747,8 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     const int n_sms = sm_count(t.device);
     long long grid = (p.items + 3ll) / 4;
     if (grid > n_sms) grid = n_sms;
+    // few tiles: whole CTAs per tile, so that a CTA holds one part of one tile
+    if (tiles <= n_sms && tiles * (n_sms / tiles) <= grid) grid = tiles * (n_sms / tiles);
     const int per = N * BK + C_BYTES;
     int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
     if (stages > kMaxStages) stages = kMaxStages;
