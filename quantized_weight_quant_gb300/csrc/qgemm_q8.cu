@@ -59,11 +59,14 @@ __device__ unsigned int g_q8_err = 0;
 
 // PIECES: E4M3 values per code.  CB: code bytes per row and k-block.
 // GROUPS: A buffers, and groups of four dequantizing warps (one per tensor-
-// memory lane quarter); group g fills buffer g with every GROUPS-th item.
+// memory lane quarter); group g fills buffer g with every GROUPS-th item.  A
+// group takes ~1400 cycles per item, most of them waits; three hide that, and
+// leave the epilogue the registers that a fourth would take (6144 x 12288 int4
+// over 1571 rows with a residual: 163 us with three, 180 us with four).
 template <int FMT> struct Fmt;
 template <> struct Fmt<B200Q_I8> { static constexpr int PIECES = 2, CB = 128, GROUPS = 2; };
-template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 4; };
-template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 4; };
+template <> struct Fmt<B200Q_I4> { static constexpr int PIECES = 1, CB = 64, GROUPS = 3; };
+template <> struct Fmt<B200Q_I2> { static constexpr int PIECES = 1, CB = 32, GROUPS = 3; };
 template <int FMT> struct Roles {
     static constexpr int kWEpi = kWDeq + 4 * Fmt<FMT>::GROUPS;
     static constexpr int kThreads = (kWEpi + kEpiWarps) * 32;
