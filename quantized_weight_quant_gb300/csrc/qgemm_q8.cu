@@ -9,8 +9,9 @@
 // sums are the tensor cores' f32.
 //
 // Work is cut into (output tile, 128-column k-block) items, tile-major, and
-// every CTA takes one contiguous run of them (one CTA per SM), so that the
-// last wave is as full as the others.  A tile that one CTA holds whole goes
+// every CTA takes one contiguous run of them (one CTA per SM): whole tiles
+// where that is nearly even, otherwise runs that cut tiles, so that the last
+// wave is as full as the others.  A tile that one CTA holds whole goes
 // straight to y; a shared one is written as f32 planes (one per CTA), and the
 // CTA whose arrival completes the tile adds the planes in CTA order and runs
 // the epilogue.  No CTA waits for another, and the order of the additions does
@@ -358,10 +359,11 @@ struct Q8Params {
     int O, S, N, nk, n_tiles, act, type;
     int stages;
     int items;                     // tiles * nk
+    int grain;                     // a CTA's run is a multiple of this many items: 1, or nk (whole tiles)
 };
 
 __device__ __forceinline__ int run_start(const Q8Params &p, int c) {
-    return (int)((long long)c * p.items / (long long)gridDim.x);
+    return (int)((long long)c * (p.items / p.grain) / (long long)gridDim.x) * p.grain;
 }
 __device__ __forceinline__ int owner_of(const Q8Params &p, int i) {
     return (int)(((i + 1ll) * (long long)gridDim.x - 1) / p.items);
@@ -752,6 +754,14 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     if (grid > n_sms) grid = n_sms;
     // few tiles: whole CTAs per tile, so that a CTA holds one part of one tile
     if (tiles <= n_sms && tiles * (n_sms / tiles) <= grid) grid = tiles * (n_sms / tiles);
+    // Whole tiles per CTA where the last, uneven round costs less than cutting
+    // tiles does: a CTA's two shared tiles take it about as long as N / 3 items
+    // (6144 x 12288 over 1571 rows, N = 176, 288 items per CTA instead of 273:
+    // 127 us whole, 163 us cut; 32 rows of the 12288 x 6144 pair, N = 32, 96
+    // instead of 61: 35 us whole, 29 us cut).
+    const long long rounds = (tiles + grid - 1) / grid;
+    const bool even = tiles >= grid && rounds * p.nk - p.items / grid <= N / 3;
+    p.grain = even ? p.nk : 1;
     const int per = N * BK + C_BYTES;
     int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
     if (stages > kMaxStages) stages = kMaxStages;
@@ -761,7 +771,7 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     cudaError_t e = allow_dynamic_smem((const void *)qgemm_q8_kernel<FMT, GLU>, kSmemLimit);
     if (e != cudaSuccess) return e;
     void *ws = nullptr;
-    const bool shared = p.items % grid != 0 || (p.items / grid) % p.nk != 0;   // some tile is cut
+    const bool shared = !even && (p.items % grid != 0 || (p.items / grid) % p.nk != 0);   // some tile is cut
     const size_t plane_bytes = (size_t)grid * 2 * N * BM * 4;
     if (shared) {
         e = workspace_alloc(&ws, plane_bytes + (size_t)tiles * 8, st);
