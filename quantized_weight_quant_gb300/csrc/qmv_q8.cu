@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(1024, 1) qmv_q8_kernel(const MvParams p) {
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tig = lane & 3;
     uint8_t *ring = smem + warp * (AHEAD * kSlot) + lane * 16;
-    float *red = reinterpret_cast<float *>(smem + warps * (AHEAD * kSlot));     // [2][warps][M][128]
-    uint8_t *xsm = reinterpret_cast<uint8_t *>(red + 2 * warps * M * 128);
+    float *red = reinterpret_cast<float *>(smem + warps * (AHEAD * kSlot));     // [1 or 2][warps][M][128]
+    uint8_t *xsm = smem + warps * (AHEAD * kSlot + (p.tiles <= (int)gridDim.x ? 1 : 2) * M * 512);
     const int steps = p.ng > warp ? (p.ng - warp + warps - 1) / warps : 0;      // of this warp per tile
 
     // the copy cursor runs AHEAD steps before the arithmetic
@@ -284,13 +284,14 @@ __global__ void __launch_bounds__(1024, 1) qmv_q8_kernel(const MvParams p) {
     }
 }
 
-// Shared memory beside x and the ring: two sets of the warps' sums.
-constexpr long long sums_bytes(int warps, int M) { return (long long)warps * 2 * M * 512; }
+// Shared memory beside x and the ring: the warps' sums, two sets if a CTA takes
+// more than one tile.
+constexpr long long sums_bytes(int warps, int M, bool one) { return (long long)warps * (one ? 1 : 2) * M * 512; }
 
 template <int FMT, bool GLU, bool XH, int AHEAD>
 cudaError_t start(const MvParams &p, int device, int c, int warps, cudaStream_t st, bool *handled) {
     constexpr int M = GLU ? 2 : 1;
-    const size_t smem = (size_t)(p.S * p.pitch + sums_bytes(warps, M)) + (size_t)warps * M * AHEAD * 1024;
+    const size_t smem = (size_t)(p.S * p.pitch + sums_bytes(warps, M, p.tiles <= sm_count(device) * c)) + (size_t)warps * M * AHEAD * 1024;
     cudaError_t e = allow_dynamic_smem((const void *)qmv_q8_kernel<FMT, GLU, XH, AHEAD>, 227 * 1024);
     if (e != cudaSuccess) return e;
     const int slots = sm_count(device) * c;
@@ -336,20 +337,27 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st, bool *handled) {
     p.ng = (int)(t.ld / 64);
     p.act = a.act;
     p.type = a.type;
-    // 32 warps per SM in c CTAs: several, so that one's end of a tile runs under
-    // another's copies; 16 where x leaves no room for more.  x in f16 if it
-    // fits beside a ring of four steps (two of the pair) with two CTAs per SM
-    // or more, as bytes otherwise (12288 x 6144 int4, 8 tokens: f16 with one
-    // CTA 16.1 us, bytes with two 14.9 us; one token, f16: 12.0 us).
-    // Rows are 64 bytes off a 128-byte multiple: two tokens' reads differ in bank.
-    constexpr int kShape[4][2] = {{4, 8}, {2, 16}, {1, 32}, {1, 16}};      // CTAs per SM, warps per CTA
+    // CTAs per SM and warps per CTA.  First choice: every tile has its CTA from
+    // the start (up to eight CTAs of an SM's 32 warps), so that no CTA takes a
+    // second tile while others have none (6144 x 12288 int4, 384 tiles, one
+    // token: 12.0 us with 3 x 10 warps, 13.7 us with 2 x 16 and 304 of the 384
+    // tiles in the first round).  Otherwise 32 warps in a few CTAs that walk
+    // the tiles, 16 where x leaves no room for more.  x in f16 if it fits
+    // beside a ring of four steps (two of the pair) with two CTAs per SM or
+    // more, as bytes otherwise (12288 x 6144 int4, 8 tokens: f16 with one CTA
+    // 16.1 us, bytes with two 14.9 us).  Rows are 64 bytes off a 128-byte
+    // multiple: two tokens' reads differ in bank.
+    const int n_sms = sm_count(t.device), each = (p.tiles + n_sms - 1) / n_sms;
+    const int most = 32 / (each < 8 ? each : 8), steps = (p.ng + most - 1) / most;
+    const int shapes[5][2] = {{each, (p.ng + steps - 1) / steps}, {4, 8}, {2, 16}, {1, 32}, {1, 16}};
     for (int xh = 1; xh >= 0; --xh)
-        for (const auto &sh : kShape) {
-            const int c = sh[0], warps = sh[1];
+        for (int k = each <= 8 ? 0 : 1; k < 5; ++k) {
+            const int c = shapes[k][0], warps = shapes[k][1] < 4 ? 4 : shapes[k][1];     // four finish a tile
             p.pitch = p.ng * (xh ? 8 : 4) * KC + 64;
-            const long long room = 228 * 1024 / c - 1024 - (long long)p.S * p.pitch - sums_bytes(warps, M);
+            const long long room =
+                228 * 1024 / c - 1024 - (long long)p.S * p.pitch - sums_bytes(warps, M, p.tiles <= n_sms * c);
             const long long ahead = room / (warps * M * 1024);
-            if (ahead >= (GLU || !xh ? 2 : 4) && !(xh && c == 1)) {
+            if (ahead >= (GLU || !xh ? 2 : 4) && !(xh && c == 1 && k)) {
                 if (xh) return ahead >= 4 ? start<FMT, GLU, true, 4>(p, t.device, c, warps, st, handled)
                                           : start<FMT, GLU, true, 2>(p, t.device, c, warps, st, handled);
                 return ahead >= 4 ? start<FMT, GLU, false, 4>(p, t.device, c, warps, st, handled)
