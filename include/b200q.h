@@ -6,8 +6,9 @@
  *     y[s,o] = scale[o] * sum_i deq(W[o,i]) * x[s,i]
  *
  * against S activation rows, plus the calls built on it: the gate/up pair,
- * grouped expert calls, RMSNorm glue and MLA decode attention with weight
- * absorption over paged caches.  Sources for the operation: the page "CUDA 后端"
+ * grouped expert calls, RMSNorm glue, MLA decode attention with weight
+ * absorption over paged caches, and the calls on 8-bit activations.
+ * Sources for the operation: the page "CUDA 后端"
  * (colibri-analysis 09), section 1, "设备侧库 backend_cuda.cu" (the resident
  * tensor, `weight_at`, `quant_matmul` and the five extern "C" functions of the
  * backend), and the page "第 8 章 · 02 CUDA/Metal/Vulkan 三后端", section 四
@@ -508,7 +509,11 @@ int b200q_rmsnorm_q8(const void *x, const void *r, void *h, int type, long long 
  * y must not overlap x8, xs or bias.  Numerics: the codes are exact E4M3
  * values (int8 as 16 * high + low), so every product is exact; sums are f32;
  * the epilogue is f32 and rounds once to `type`.  f32 results are within
- * 1e-5 * scale * xs * sum |deq * x8| of the exact sum before the activation.
+ * 1e-5 * scale * xs * sum |deq * x8| of the exact sum before the activation,
+ * and the same call gives the same bits.
+ * Up to 8 rows one launch streams the weights; more rows run on the fp8 tensor
+ * cores, where a call whose output tiles are shared by several blocks takes a
+ * stream-ordered workspace of the library's pool (at most 30 MB).
  * S = 0 is a no-op.  Asynchronous on `stream`.
  */
 int b200q_matmul_q8(const b200q_tensor *t, const void *x8, long long ld8, const float *xs, const float *bias, int act,

@@ -354,7 +354,7 @@ struct Q8Params {
     void *y;
     long long ldr, ldy;
     float *planes;                 // [grid][2][N][128]
-    unsigned long long *cnt;       // [tiles] (token << 10) | arrivals
+    unsigned long long *cnt;       // [tiles] (token << 10) | arrivals; any other tag counts as no arrivals
     unsigned long long token;
     int O, S, N, nk, n_tiles, act, type;
     int stages;
@@ -714,7 +714,18 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                      : "memory");
 }
 
-std::atomic<unsigned long long> g_token{0x51a9e8ull};
+// A launch's 54-bit tag: every launch its own, and spread over all bits (the
+// finalizer of splitmix64: G. Steele, D. Lea, C. Flood, "Fast splittable
+// pseudorandom number generators", 2014), so that what an earlier use left in
+// the workspace does not look like one.  A count returns to 0 when its tile is
+// complete, so a captured launch finds no count of its last replay.
+unsigned long long next_token() {
+    static std::atomic<unsigned long long> launches{0};
+    unsigned long long z = (launches.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull;
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    return (z ^ (z >> 31)) >> 10;
+}
 
 template <int FMT, bool GLU>
 cudaError_t run(const MatQ8 &a, cudaStream_t st) {
@@ -778,7 +789,7 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         p.planes = (float *)ws;
         p.cnt = (unsigned long long *)((char *)ws + plane_bytes);
-        p.token = g_token.fetch_add(1, std::memory_order_relaxed) & ((1ull << 54) - 1);
+        p.token = next_token();
     }
     qgemm_q8_kernel<FMT, GLU><<<(int)grid, Roles<FMT>::kThreads, smem, st>>>(t.q8_map, a.tu ? a.tu->q8_map : t.q8_map, map_x, p);
     count_launch();
@@ -806,12 +817,14 @@ bool q8_map_encode(Tensor &t) {
 }
 
 cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st) {
-    // item numbers are 32-bit: longer batches in parts
-    constexpr int kRows = 1 << 16;
+    // item numbers are 32-bit: longer batches in parts of at most 2^16 rows, fewer for a large tensor
+    const long long row_items = ((a.tg->O + 63ll) / 64) * ((a.tg->I + BK - 1ll) / BK);
+    int part = 1 << 16;
+    while (part > 128 && row_items * ((part + kMaxN - 1) / kMaxN) > 0x7ffffff0ll) part /= 2;
     const long long b = a.type == B200Q_T_F32 ? 4 : 2;
-    for (int s0 = 0; s0 < a.S; s0 += kRows) {
+    for (int s0 = 0; s0 < a.S; s0 += part) {
         MatQ8 c = a;
-        c.S = a.S - s0 < kRows ? a.S - s0 : kRows;
+        c.S = a.S - s0 < part ? a.S - s0 : part;
         c.x8 += s0 * a.ld8;
         c.xs += s0;
         c.y = (char *)a.y + s0 * a.ldy * b;

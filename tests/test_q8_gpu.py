@@ -546,3 +546,33 @@ def test_refusals(q):
     for t in (f32, gs, p.t, p2.t):
         t.free()
     assert q.device_status() == q.OK
+
+
+def test_example_block(q):
+    """The example's block.  Each of its two quantisations rounds by at most 2^-4 of a value, 2^-5 / sqrt(3) in the
+    root mean square of a uniform error over a binade's steps (about 0.025); the three products see the first one
+    in gate and up and the second in down: below 0.025 * (1.5 + 1 + 1) with independent roundings, and the bf16
+    roundings (h, m, y) are far smaller (y - h: 2^-8 of |h| ~ 1.4 against values near 0.5)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "dense_block_q8.py")
+    spec = importlib.util.spec_from_file_location("dense_block_q8", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for e in mod.run(512, 1024, [1, 7, 40], time_it=False):
+        assert 1e-3 < e < 0.0875
+
+
+def test_long_batch_in_parts(q):
+    """More rows than one launch of the tensor-core kernel numbers: the last part's rows and the first's."""
+    import torch
+    O, I, S = 40, 64, (1 << 16) + 9
+    p = _Pair(q, "i4", O, I, 2, True)
+    xq, x, xs = _input8(q, S, I, 3)
+    y, r = torch.zeros(S, O, device="cuda"), _dev(synth.normal_f32((S, O), 5, 6))
+    with p.t:
+        q.matmul_q8(p.t, xq, y, S, bias=p.bias_d, res=r)
+        torch.cuda.synchronize()
+    v, e = p.exact(x, xs)
+    want = v + _np64(r)
+    _check(y, want, e + 2.0 ** -23 * np.abs(want), "f32", "long batch")
