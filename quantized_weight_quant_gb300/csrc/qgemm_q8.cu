@@ -814,19 +814,25 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     const long long tiles = m_tiles * p.n_tiles;
     if (tiles * p.nk > 0x7ffffff0ll) return cudaErrorInvalidValue;
     p.items = (int)(tiles * p.nk);
-    // at least four k-blocks per CTA
+    // At least eight k-blocks per CTA: with fewer, a tile's planes cost more than
+    // the CTAs save (int4, 256 x 7168 over 32 rows: 22 us with four, 15.7 us with
+    // eight; 2048 x 1024 over 64: 11.6 and 9.4 us; with twelve 13.2 us).
     const int n_sms = sm_count(t.device);
-    long long grid = (p.items + 3ll) / 4;
+    long long grid = (p.items + 7ll) / 8;
     if (grid > n_sms) grid = n_sms;
-    // few tiles: whole CTAs per tile, so that a CTA holds one part of one tile
+    // Few tiles: the same number of CTAs for every tile, so that a CTA holds one
+    // part of one tile (512 rows of 6144 x 12288 with a residual: 44.8 us so,
+    // 48.8 us over all SMs; int2 5001 x 4097 over 77 rows: 16.6 and 20.8 us; the
+    // other way round where that leaves many SMs out: int8 8192 x 8192 over 32
+    // rows, 128 CTAs, 29.5 and 27.8 us).
     if (tiles <= n_sms && tiles * (n_sms / tiles) <= grid) grid = tiles * (n_sms / tiles);
     // Whole tiles per CTA where the last, uneven round costs less than cutting
-    // tiles does: a CTA's two shared tiles take it about as long as N / 3 items
-    // (6144 x 12288 over 1571 rows, N = 176, 288 items per CTA instead of 273:
-    // 127 us whole, 163 us cut; 32 rows of the 12288 x 6144 pair, N = 32, 96
-    // instead of 61: 35 us whole, 29 us cut).
+    // tiles does: a CTA's two cut tiles take it about as long as N / 6 items
+    // (6144 x 12288 over 1571 rows with a residual, N = 176, 288 items per CTA
+    // instead of 273: 113 us whole, 120 us cut; 12288 x 6144 over 300 rows,
+    // N = 160, 96 instead of 61: 42.2 us whole, 39.8 us cut).
     const long long rounds = (tiles + grid - 1) / grid;
-    const bool even = tiles >= grid && rounds * p.nk - p.items / grid <= N / 3;
+    const bool even = tiles >= grid && rounds * p.nk - p.items / grid <= N / 6;
     p.grain = even ? p.nk : 1;
     const int per = N * BK + C_BYTES;
     int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
