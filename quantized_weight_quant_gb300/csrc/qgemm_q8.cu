@@ -8,27 +8,34 @@
 // the low field is its own E4M3 byte; B is read as it is.  Products are exact,
 // sums are the tensor cores' f32.
 //
+// Bound: the tensor cores for many rows, the weights' bytes for few; now the
+// hand-over between the roles, ~0.4 us per item at N = 176, and the integer work
+// of the dequantizers: int4 12288 x 6144 over 1571 rows 110 us, 2150 TFLOP/s;
+// the pair 207 us, 2290 TFLOP/s; 6144 x 12288 with a residual 113 us; int2
+// 5001 x 4097 over 77 rows 16.6 us.
+//
 // Work is cut into (output tile, 128-column k-block) items, tile-major, and
 // every CTA takes one contiguous run of them (one CTA per SM): whole tiles
 // where that is nearly even, otherwise runs that cut tiles, so that the last
 // wave is as full as the others.  A tile that one CTA holds whole goes
-// straight to y; a shared one is written as f32 planes (one per CTA), and the
-// CTA whose arrival completes the tile adds the planes in CTA order and runs
-// the epilogue.  No CTA waits for another, and the order of the additions does
-// not depend on the arrivals, so results repeat bit for bit.
+// straight to y; a cut one is written as f32 planes (one per CTA), and the CTA
+// whose arrival completes the tile adds the planes in CTA order and runs the
+// epilogue, with all its dequantizing and epilogue warps, when its run is done.
+// No CTA waits for another, and the order of the additions does not depend on
+// the arrivals, so results repeat bit for bit.
 //
 // Warp roles:
-//   warps 0-2  TMA producers, one thread each: N rows of x8, and the two boxes
-//              of 64 code rows (128-byte swizzle for x8; a TMA takes its
-//              thread ~160 cycles and an mbarrier test ~290, so one thread
-//              for all three copies of an item would be slower than its MMAs);
-//   warp 3     one thread issues the MMAs (kind::f8f6f4, 128 x N x 32, A from
-//              tensor memory, B from shared memory) into one of two
-//              accumulators; one commit per item frees both its stage and its
+//   warps 0-2  TMA producers: N rows of x8, and the two boxes of 64 code rows
+//              (128-byte swizzle for x8; a TMA takes its thread ~160 cycles
+//              and an mbarrier test ~290, so one warp for all three copies of
+//              an item would be slower than its MMAs);
+//   warp 3     issues the MMAs (kind::f8f6f4, 128 x N x 32, A from tensor
+//              memory, B from shared memory) into one of two accumulators of up
+//              to 192 columns; one commit per item frees both its stage and its
 //              A buffer;
-//   warps 4 .. dequantizers, in groups of four: codes -> E4M3 bytes by a
-//              16-entry table lookup in registers (byte permutes), stored to
-//              the group's A buffer in tensor memory, natural K order;
+//   warps 4 .. dequantizers, three groups of four (int8: two): codes -> E4M3
+//              bytes by a 16-entry table lookup in registers (byte permutes),
+//              stored to the group's A buffer in tensor memory, natural K order;
 //   last four  epilogue.
 // The gated pair takes 64 gate and 64 up rows per tile, interleaved by 16 in
 // the lanes, so that a gate and its up value sit in one warp, 16 lanes apart.
@@ -49,7 +56,7 @@ constexpr int BM = 128, BK = 128;
 constexpr int kMaxN = 192;                 // rows of x8 per tile
 constexpr int kProducers = 3, kWMma = 3, kWDeq = 4;
 constexpr int kEpiWarps = 4;
-constexpr int kTmemCols = 512, kAccBase = 128, kAccStride = kMaxN;   // A ring: columns 0..127
+constexpr int kTmemCols = 512, kAccBase = 128, kAccStride = kMaxN;   // A ring: below column 128
 constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 120 * 1024;      // one CTA per SM: it takes the whole tensor memory
 constexpr int kMiscBytes = 512 + 3 * kMaxN * 4;   // barriers and counters, row scales of three tiles

@@ -2,7 +2,9 @@
 // the weights once at memory speed.
 //     y[s,o] = act(scale[o] xs[s] sum_i deq(W[o,i]) x8[s,i] + bias[o]) + res[s,o],  or act(g) u
 //
-// Bound: HBM (the weights).  A weight costs an f32 FMA per row and an integer
+// Bound: HBM (the weights); now a call's start and the integer work on the
+// codes: int4 6144 x 12288, one token, 12.0 us, 3150 GB/s; the 12288 x 6144 pair
+// 19.7 us, 3830 GB/s; int8 8192 x 8192, 8 tokens, 17.6 us, 3810 GB/s.  A weight costs an f32 FMA per row and an integer
 // instruction or more on SIMT; here the products go to the warp-level tensor
 // instruction m16n8k16 (f16 in, f32 sums): 16 weight rows against 8 tokens.
 // The tcgen05 kernel needs 128 weight rows per tile, which leaves too few
