@@ -122,15 +122,15 @@ template <class T, bool ALIGNED> struct Cols {
     int n, tid, D;
     __device__ __forceinline__ int at(int k) const { return (k * n + tid) * kVec<T>; }
     __device__ __forceinline__ bool full(int k) const { return at(k) + kVec<T> <= D; }
-    template <class U>
+    template <class U, bool AL = ALIGNED>
     __device__ __forceinline__ Vec<U> load(const U *p, int c) const {
         constexpr int m = kVec<U>;
         Vec<U> v;
-        if (ALIGNED ? c + m <= D : c >= m && c + 2 * m <= D) {
+        if (AL ? c + m <= D : c >= m && c + 2 * m <= D) {
             const char *a = (const char *)(p + c);
-            const uint32_t sh = ALIGNED ? 0u : (uint32_t)((uintptr_t)a & 15u);
+            const uint32_t sh = AL ? 0u : (uint32_t)((uintptr_t)a & 15u);
             const uint4 *b = reinterpret_cast<const uint4 *>(a - sh);
-            v.q = ALIGNED ? b[0] : shifted(b[0], b[1], sh);
+            v.q = AL ? b[0] : shifted(b[0], b[1], sh);
         } else {
 #pragma unroll
             for (int j = 0; j < m; ++j) v.e[j] = c + j < D ? p[c + j] : from_f<U>(0.f);
@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) rmsnorm_q8
 #pragma unroll
         for (int k = 0; k < NV; ++k) rv[k] = cols.load(r, cols.at(k));
     }
+    const bool w16 = ALIGNED || (uintptr_t)a.w % 16 == 0;      // its one row needs no shift where x's rows do
     float v[NV][E], ss = 0.f, m = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -226,7 +227,8 @@ __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) rmsnorm_q8
         float g[E];
 #pragma unroll
         for (int j = 0; j < E; j += 4) {
-            const Vec<float> wv = cols.load(a.w, cols.at(k) + j);
+            const Vec<float> wv = w16 ? cols.template load<float, true>(a.w, cols.at(k) + j)
+                                      : cols.template load<float, false>(a.w, cols.at(k) + j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) g[j + i] = wv.e[i];
         }
