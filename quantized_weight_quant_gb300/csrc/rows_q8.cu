@@ -9,7 +9,7 @@
 // Bound: HBM for long batches (8192 x 12288 f32 80.5 us, 6250 GB/s; 1571 x 6144
 // bf16 with residual 15.8 us, 4290 GB/s in ten waves of short blocks); a call's
 // latency for a few rows (3.5-4 us for 1 to 4 rows in a graph); the integer
-// pipe where rows have to be shifted into place (6007 x 5003 f16 43 us).
+// pipe where rows have to be shifted into place (6007 x 5003 f16 36.5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -116,8 +116,9 @@ __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint3
 // that its bytes of y8 are aligned; a row's last vector may be short.
 // ALIGNED: every wide operand's rows start on 16 bytes.  Otherwise a vector is
 // the two aligned ones around it, shifted into place; next to the ends of a
-// row, where those would reach past it, values are read one by one, and h is
-// written value by value.
+// row, where those would reach past it, values are read one by one.  h is
+// written in aligned vectors too (6007 x 5003 bf16 with residual: 71 us, value by
+// value 98 us).
 template <class T, bool ALIGNED> struct Cols {
     int n, tid, D;
     __device__ __forceinline__ int at(int k) const { return (k * n + tid) * kVec<T>; }
@@ -137,14 +138,29 @@ template <class T, bool ALIGNED> struct Cols {
         }
         return v;
     }
+    // Called by whole warps.  Unaligned rows: a lane writes the aligned 16 bytes
+    // that begin in its left neighbour's vector; the warp's first and last lanes,
+    // and the row's last, write what is left of theirs value by value.
     __device__ __forceinline__ void store(T *p, int k, const Vec<T> &v) const {
-        if (ALIGNED && full(k)) {
-            *reinterpret_cast<uint4 *>(p + at(k)) = v.q;
+        constexpr int m = kVec<T>;
+        const int c = at(k);
+        const bool f = full(k);
+        const uint32_t sh = ALIGNED ? 0u : (uint32_t)((uintptr_t)(p + c) & 15u);
+        int lo = 0, hi = m;                       // values outside lo .. hi-1 are written one by one
+        if (sh == 0) {
+            if (f) *reinterpret_cast<uint4 *>(p + c) = v.q;
         } else {
-#pragma unroll
-            for (int j = 0; j < kVec<T>; ++j)
-                if (at(k) + j < D) p[at(k) + j] = v.e[j];
+            const uint4 left = make_uint4(__shfl_up_sync(0xffffffffu, v.q.x, 1), __shfl_up_sync(0xffffffffu, v.q.y, 1),
+                                          __shfl_up_sync(0xffffffffu, v.q.z, 1), __shfl_up_sync(0xffffffffu, v.q.w, 1));
+            const int lane = threadIdx.x & 31, split = m - (int)(sh / sizeof(T));
+            if (lane == 0) lo = split;
+            if (lane == 31 || c + 2 * m > D) hi = split;
+            if (f && lane != 0) *reinterpret_cast<uint4 *>((char *)(p + c) - sh) = shifted(left, v.q, 16 - sh);
         }
+        if (ALIGNED && f) return;
+#pragma unroll
+        for (int j = 0; j < m; ++j)
+            if (c + j < D && (!f || j < lo || j >= hi)) p[c + j] = v.e[j];
     }
     // E4M3 bytes, in pairs
     __device__ __forceinline__ void store8(uint8_t *y, int k, const uint32_t (&c)[kVec<T> / 2]) const {
@@ -196,15 +212,18 @@ __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) quantize_q
     }
 }
 
-template <class T, int NV, bool ALIGNED>
+// RES: with r or h.  Without either it keeps no sum's operands and no rounded
+// copy (8192 x 12288 f32: 91 us, with the code for both in place 151 us; 6007 x
+// 5003 f16 36.5 and 44.4 us).
+template <class T, int NV, bool ALIGNED, bool RES>
 __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) rmsnorm_q8_kernel(const RowsQ8 a) {
     constexpr int E = kVec<T>;
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= a.S) return;
     const Cols<T, ALIGNED> cols{(int)blockDim.x, (int)threadIdx.x, a.D};
     const T *x = (const T *)a.x + row * a.ldx;
-    const T *r = a.r ? (const T *)a.r + row * a.ldr : nullptr;
-    T *h = a.h ? (T *)a.h + row * a.ldh : nullptr;
+    const T *r = RES && a.r ? (const T *)a.r + row * a.ldr : nullptr;
+    T *h = RES && a.h ? (T *)a.h + row * a.ldh : nullptr;
     uint8_t *y = a.y8 + row * a.ld8;
     Vec<T> xv[NV], rv[NV];
 #pragma unroll
@@ -287,7 +306,8 @@ __global__ void __launch_bounds__(kLongThreads) rows_q8_long_kernel(const RowsQ8
 template <class T, int NV, bool ALIGNED>
 void start(const RowsQ8 &a, dim3 block, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.S + (long long)block.y - 1) / block.y);
-    if (a.w) rmsnorm_q8_kernel<T, NV, ALIGNED><<<grid, block, 0, st>>>(a);
+    if (a.w && (a.r || a.h)) rmsnorm_q8_kernel<T, NV, ALIGNED, true><<<grid, block, 0, st>>>(a);
+    else if (a.w) rmsnorm_q8_kernel<T, NV, ALIGNED, false><<<grid, block, 0, st>>>(a);
     else quantize_q8_kernel<T, NV, ALIGNED><<<grid, block, 0, st>>>(a);
 }
 
