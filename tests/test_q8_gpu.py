@@ -576,3 +576,36 @@ def test_long_batch_in_parts(q):
     v, e = p.exact(x, xs)
     want = v + _np64(r)
     _check(y, want, e + 2.0 ** -23 * np.abs(want), "f32", "long batch")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S,D", SIZES)
+def test_rmsnorm_alone(q, S, D, kind):
+    """Neither residual nor h; w off a vector's boundary for odd D."""
+    import torch
+    x = _dev(_rows(S, D, D + 1), kind)
+    w = _dev(synth.uniform_f32((D + 1,), -1.5, 1.5, D, 4))[D % 2:][:D]
+    out = _fresh(q, S, D)
+    q.rmsnorm_q8(x, w, out, S, D, 1e-6)
+    torch.cuda.synchronize()
+    _check_rows(*_quantised(q, out, D), _norm_ref(_np64(x), None, _np64(w), 1e-6)[1])
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [1, 2, 9, 31, 257, 263, 511, 1025, 2049, 4099])
+@pytest.mark.parametrize("S", [2, 700])
+def test_rmsnorm_odd_rows_in_place(q, S, D, kind):
+    """Rows of D values one after the other, from an odd value on: h over x, every value its own, nothing beside it."""
+    import torch
+    buf = _dev(_rows(1, S * D + 40, D)[0], kind)
+    keep = buf.clone()
+    x, r = buf[3:3 + S * D].view(S, D), _dev(_rows(S, D, D + 2), kind)
+    want = (x.float() + r.float()).to(x.dtype)
+    w = _dev(synth.uniform_f32((D,), 0.5, 1.5, D, 5))
+    _, y = _norm_ref(_np64(x), _np64(r), _np64(w), 1e-6)
+    out = _fresh(q, S, D)
+    q.rmsnorm_q8(x, w, out, S, D, 1e-6, r=r, h=x)
+    torch.cuda.synchronize()
+    keep[3:3 + S * D] = want.view(-1)
+    assert torch.equal(buf, keep)
+    _check_rows(*_quantised(q, out, D), y)
