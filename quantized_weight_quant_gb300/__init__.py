@@ -78,6 +78,8 @@ def _load():
     L.b200q_matmul_q8.restype = ci
     L.b200q_glu_q8.argtypes = [vp, vp, vp, cll, vp, vp, vp, ci, vp, ci, cll, ci, vp]
     L.b200q_glu_q8.restype = ci
+    L.b200q_selftest_q8_plan.argtypes = [ci, ci, ci, ci, ci, ci, vp]
+    L.b200q_selftest_q8_plan.restype = ci
     L.b200q_selftest_timeout.argtypes = [ci, vp]
     L.b200q_selftest_timeout.restype = ci
     L.b200q_silu_mul.argtypes = [vp, vp, vp, cl, vp]
@@ -433,6 +435,17 @@ def glu_q8(tg, tu, xq, y, S: int, act: int = ACT_SILU, bias_g=None, bias_u=None,
     yp, ty, ldy = _wide(y, S, tg.O, "y")
     _check(lib.b200q_glu_q8(_h(tg), _h(tu), cp, ld8, sp, _vec(bias_g, tg.O, "bias_g"), _vec(bias_u, tg.O, "bias_u"),
                             act, yp, ty, ldy, S, _raw_stream(stream)))
+
+
+Q8_PLAN = ("few", "few_grid", "few_warps", "few_smem", "part", "N", "n_tiles", "tiles", "nk", "grid", "items", "grain",
+           "cut", "ok")
+
+
+def selftest_q8_plan(fmt: int, pair: bool, O: int, I: int, S: int, n_sms: int = 152) -> dict:
+    """How matmul_q8 or glu_q8 (pair) would launch (b200q_selftest_q8_plan)."""
+    out = (ctypes.c_longlong * len(Q8_PLAN))()
+    _check(lib.b200q_selftest_q8_plan(fmt, int(pair), O, I, S, n_sms, out))
+    return dict(zip(Q8_PLAN, out))
 
 
 def selftest_timeout(wait_us: int, stream=None) -> None:

@@ -13,6 +13,7 @@
 #include <string>
 #include <vector>
 
+#include "qmat_q8.h"
 #include "qwq_internal.h"
 
 namespace qwq {
@@ -908,6 +909,20 @@ int b200q_glu_q8(const b200q_tensor *tg, const b200q_tensor *tu, const void *x8,
 }
 
 }  // extern "C"
+
+extern "C" int b200q_selftest_q8_plan(int fmt, int pair, int O, int I, int S, int n_sms, long long *out) {
+    const char *who = "b200q_selftest_q8_plan";
+    if (!out || O < 1 || I < 1 || S < 1 || n_sms < 1) return fail(B200Q_EINVAL, "%s: bad argument", who);
+    if (fmt != B200Q_I8 && fmt != B200Q_I4 && fmt != B200Q_I2) return fail(B200Q_EINVAL, "%s: unknown format", who);
+    const long long rb = host_row_bytes(fmt, I);
+    const MvPlan m = plan_mv_q8(fmt, pair != 0, O, (rb + kRowAlign - 1) / kRowAlign * kRowAlign, S, n_sms);
+    const int part = gemm_q8_part(O, I);
+    const GemmPlan g = plan_gemm_q8(fmt, pair != 0, O, I, S < part ? S : part, n_sms);
+    const long long v[B200Q_Q8_PLAN] = {m.fits,  m.grid,   m.warps,  m.smem, part,  g.N,   g.n_tiles,
+                                        g.tiles, g.nk,     g.grid,   g.items, g.grain, g.cut, g.ok};
+    for (int k = 0; k < B200Q_Q8_PLAN; ++k) out[k] = v[k];
+    return B200Q_OK;
+}
 
 extern "C" int b200q_selftest_timeout(int wait_us, void *stream) {
     if (wait_us < 1 || wait_us > 1000000)

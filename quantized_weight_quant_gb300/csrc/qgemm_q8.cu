@@ -790,42 +790,22 @@ unsigned long long next_token() {
 }
 
 template <int FMT, bool GLU>
-cudaError_t run(const MatQ8 &a, cudaStream_t st) {
+GemmPlan plan(int O, int I, int S, int n_sms) {
     constexpr int C_BYTES = BM * Fmt<FMT>::CB;
-    const Tensor &t = *a.tg;
+    GemmPlan r{};
     // rows of x8 per tile: the fewest tiles of at most kMaxN rows, evenly filled
-    const int n_tiles = (a.S + kMaxN - 1) / kMaxN;
-    const int N = ((a.S + n_tiles - 1) / n_tiles + 15) / 16 * 16;
-    CUtensorMap map_x;
-    if (!tmap_encode_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x8, (uint64_t)t.I, (uint64_t)a.S, (uint64_t)a.ld8, BK,
-                        (uint32_t)N, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    Q8Params p{};
-    p.scale_g = t.scales;
-    p.scale_u = a.tu ? a.tu->scales : nullptr;
-    p.bias_g = a.bias_g;
-    p.bias_u = a.bias_u;
-    p.xs = a.xs;
-    p.res = a.res;
-    p.y = a.y;
-    p.ldr = a.ldr;
-    p.ldy = a.ldy;
-    p.O = t.O;
-    p.S = a.S;
-    p.N = N;
-    p.nk = (t.I + BK - 1) / BK;
-    p.n_tiles = (a.S + N - 1) / N;
-    p.act = a.act;
-    p.type = a.type;
-    const long long m_tiles = GLU ? (t.O + 63) / 64 : (t.O + 127) / 128;
-    const long long tiles = m_tiles * p.n_tiles;
-    if (tiles * p.nk > 0x7ffffff0ll) return cudaErrorInvalidValue;
-    p.items = (int)(tiles * p.nk);
+    const int n_tiles = (S + kMaxN - 1) / kMaxN;
+    const int N = r.N = ((S + n_tiles - 1) / n_tiles + 15) / 16 * 16;
+    const int nk = r.nk = (I + BK - 1) / BK;
+    r.n_tiles = (S + N - 1) / N;
+    const long long m_tiles = GLU ? (O + 63) / 64 : (O + 127) / 128;
+    const long long tiles = r.tiles = m_tiles * r.n_tiles;
+    if (tiles * nk > 0x7ffffff0ll) return r;
+    r.items = (int)(tiles * nk);
     // At least eight k-blocks per CTA: with fewer, a tile's planes cost more than
     // the CTAs save (int4, 256 x 7168 over 32 rows: 22 us with four, 15.7 us with
     // eight; 2048 x 1024 over 64: 11.6 and 9.4 us; with twelve 13.2 us).
-    const int n_sms = sm_count(t.device);
-    long long grid = (p.items + 7ll) / 8;
+    long long grid = (r.items + 7ll) / 8;
     if (grid > n_sms) grid = n_sms;
     // Few tiles: the same number of CTAs for every tile, so that a CTA holds one
     // part of one tile (512 rows of 6144 x 12288 with a residual: 44.8 us so,
@@ -839,27 +819,60 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st) {
     // instead of 273: 113 us whole, 120 us cut; 12288 x 6144 over 300 rows,
     // N = 160, 96 instead of 61: 42.2 us whole, 39.8 us cut).
     const long long rounds = (tiles + grid - 1) / grid;
-    const bool even = tiles >= grid && rounds * p.nk - p.items / grid <= N / 6;
-    p.grain = even ? p.nk : 1;
+    const bool even = tiles >= grid && rounds * nk - r.items / grid <= N / 6;
+    r.grid = (int)grid;
+    r.grain = even ? nk : 1;
+    r.cut = !even && (r.items % grid != 0 || (r.items / grid) % nk != 0);
+    r.plane_bytes = r.cut ? grid * 2 * N * BM * 4 : 0;
     const int per = N * BK + C_BYTES;
-    int stages = (kSmemLimit - 1024 - kMiscBytes) / per;
-    if (stages > kMaxStages) stages = kMaxStages;
-    p.stages = stages;
-    size_t smem = 1024 + (size_t)stages * per + kMiscBytes;
-    if (smem < kSmemFloor) smem = kSmemFloor;
+    r.stages = (kSmemLimit - 1024 - kMiscBytes) / per;
+    if (r.stages > kMaxStages) r.stages = kMaxStages;
+    r.smem = 1024 + (size_t)r.stages * per + kMiscBytes;
+    if (r.smem < kSmemFloor) r.smem = kSmemFloor;
+    r.ok = true;
+    return r;
+}
+
+template <int FMT, bool GLU>
+cudaError_t run(const MatQ8 &a, cudaStream_t st) {
+    const Tensor &t = *a.tg;
+    const GemmPlan r = plan<FMT, GLU>(t.O, t.I, a.S, sm_count(t.device));
+    if (!r.ok) return cudaErrorInvalidValue;
+    CUtensorMap map_x;
+    if (!tmap_encode_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x8, (uint64_t)t.I, (uint64_t)a.S, (uint64_t)a.ld8, BK,
+                        (uint32_t)r.N, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    Q8Params p{};
+    p.scale_g = t.scales;
+    p.scale_u = a.tu ? a.tu->scales : nullptr;
+    p.bias_g = a.bias_g;
+    p.bias_u = a.bias_u;
+    p.xs = a.xs;
+    p.res = a.res;
+    p.y = a.y;
+    p.ldr = a.ldr;
+    p.ldy = a.ldy;
+    p.O = t.O;
+    p.S = a.S;
+    p.N = r.N;
+    p.nk = r.nk;
+    p.n_tiles = r.n_tiles;
+    p.act = a.act;
+    p.type = a.type;
+    p.items = r.items;
+    p.grain = r.grain;
+    p.stages = r.stages;
     cudaError_t e = allow_dynamic_smem((const void *)qgemm_q8_kernel<FMT, GLU>, kSmemLimit);
     if (e != cudaSuccess) return e;
     void *ws = nullptr;
-    const bool shared = !even && (p.items % grid != 0 || (p.items / grid) % p.nk != 0);   // some tile is cut
-    const size_t plane_bytes = (size_t)grid * 2 * N * BM * 4;
-    if (shared) {
-        e = workspace_alloc(&ws, plane_bytes + (size_t)tiles * 8, st);
+    if (r.cut) {
+        e = workspace_alloc(&ws, (size_t)r.plane_bytes + (size_t)r.tiles * 8, st);
         if (e != cudaSuccess) return e;
         p.planes = (float *)ws;
-        p.cnt = (unsigned long long *)((char *)ws + plane_bytes);
+        p.cnt = (unsigned long long *)((char *)ws + r.plane_bytes);
         p.token = next_token();
     }
-    qgemm_q8_kernel<FMT, GLU><<<(int)grid, Roles<FMT>::kThreads, smem, st>>>(t.q8_map, a.tu ? a.tu->q8_map : t.q8_map, map_x, p);
+    qgemm_q8_kernel<FMT, GLU><<<r.grid, Roles<FMT>::kThreads, r.smem, st>>>(t.q8_map, a.tu ? a.tu->q8_map : t.q8_map, map_x, p);
     count_launch();
     e = cudaGetLastError();
     if (ws) {
@@ -884,11 +897,25 @@ bool q8_map_encode(Tensor &t) {
                                      : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
-cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st) {
-    // item numbers are 32-bit: longer batches in parts of at most 2^16 rows, fewer for a large tensor
-    const long long row_items = ((a.tg->O + 63ll) / 64) * ((a.tg->I + BK - 1ll) / BK);
+GemmPlan plan_gemm_q8(int fmt, bool pair, int O, int I, int S, int n_sms) {
+    switch (fmt) {
+    case B200Q_I8: return pair ? plan<B200Q_I8, true>(O, I, S, n_sms) : plan<B200Q_I8, false>(O, I, S, n_sms);
+    case B200Q_I4: return pair ? plan<B200Q_I4, true>(O, I, S, n_sms) : plan<B200Q_I4, false>(O, I, S, n_sms);
+    case B200Q_I2: return pair ? plan<B200Q_I2, true>(O, I, S, n_sms) : plan<B200Q_I2, false>(O, I, S, n_sms);
+    }
+    return GemmPlan{};
+}
+
+// Item numbers are 32-bit: longer batches in parts of at most 2^16 rows, fewer for a large tensor.
+int gemm_q8_part(int O, int I) {
+    const long long row_items = ((O + 63ll) / 64) * ((I + BK - 1ll) / BK);
     int part = 1 << 16;
     while (part > 128 && row_items * ((part + kMaxN - 1) / kMaxN) > 0x7ffffff0ll) part /= 2;
+    return part;
+}
+
+cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st) {
+    const int part = gemm_q8_part(a.tg->O, a.tg->I);
     const long long b = a.type == B200Q_T_F32 ? 4 : 2;
     for (int s0 = 0; s0 < a.S; s0 += part) {
         MatQ8 c = a;

@@ -8,6 +8,27 @@
 
 namespace qwq {
 
+// How a call is launched, from its sizes and the number of SMs alone (host
+// arithmetic: what the launchers use and b200q_selftest_q8_plan reports).
+struct MvPlan {                // the few-row kernel
+    bool fits;                 // false: x does not fit in shared memory, or too many rows
+    bool xh;                   // x staged in f16
+    int ahead, warps, pitch, grid, tiles, ng;
+    long long smem;
+};
+struct GemmPlan {              // one launch of the tcgen05 kernel
+    bool ok;                   // false: more items than 32 bits number
+    int N, n_tiles, nk;        // rows of x8 per tile, tiles along them, k-blocks
+    int items, grid, grain, stages;
+    long long tiles;
+    bool cut;                  // some tile is shared by several CTAs
+    long long plane_bytes;
+    size_t smem;
+};
+MvPlan plan_mv_q8(int fmt, bool pair, int O, long long ld, int S, int n_sms);
+GemmPlan plan_gemm_q8(int fmt, bool pair, int O, int I, int S, int n_sms);
+int gemm_q8_part(int O, int I);         // rows of x8 per launch
+
 // v, activated.  f32 expf / erff; for large |v| the exponentials
 // overflow or vanish to the activation's limits.  __fdividef (2 ulp) gives 0
 // where silu's denominator passes 2^126, v < -87, where silu is below 1e-36.

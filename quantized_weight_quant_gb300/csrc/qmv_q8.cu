@@ -290,17 +290,54 @@ __global__ void __launch_bounds__(1024, 1) qmv_q8_kernel(const MvParams p) {
 // more than one tile.
 constexpr long long sums_bytes(int warps, int M, bool one) { return (long long)warps * (one ? 1 : 2) * M * 512; }
 
+// CTAs per SM and warps per CTA.  First choice: every tile has its CTA from
+// the start (up to eight CTAs of an SM's 32 warps), so that no CTA takes a
+// second tile while others have none (6144 x 12288 int4, 384 tiles, one
+// token: 12.0 us with 3 x 10 warps, 13.7 us with 2 x 16 and 304 of the 384
+// tiles in the first round).  Otherwise 32 warps in a few CTAs that walk
+// the tiles, 16 where x leaves no room for more.  x in f16 if it fits
+// beside a ring of four steps (two of the pair) with two CTAs per SM or
+// more, as bytes otherwise (12288 x 6144 int4, 8 tokens: f16 with one CTA
+// 16.1 us, bytes with two 14.9 us).  Rows are 64 bytes off a 128-byte
+// multiple: two tokens' reads differ in bank.
+template <int FMT, bool GLU>
+MvPlan plan(int O, long long ld, int S, int n_sms) {
+    constexpr int KC = Fmt<FMT>::KC, M = GLU ? 2 : 1;
+    MvPlan r{};
+    r.tiles = (O + kTileRows - 1) / kTileRows;
+    r.ng = (int)(ld / 64);
+    const int each = (r.tiles + n_sms - 1) / n_sms;
+    const int most = 32 / (each < 8 ? each : 8), steps = (r.ng + most - 1) / most;
+    const int shapes[5][2] = {{each, (r.ng + steps - 1) / steps}, {4, 8}, {2, 16}, {1, 32}, {1, 16}};
+    for (int xh = 1; xh >= 0; --xh)
+        for (int k = each <= 8 ? 0 : 1; k < 5; ++k) {
+            const int c = shapes[k][0], warps = shapes[k][1] < 4 ? 4 : shapes[k][1];     // four finish a tile
+            const int pitch = r.ng * (xh ? 8 : 4) * KC + 64;
+            const long long sums = sums_bytes(warps, M, r.tiles <= n_sms * c);
+            const long long room = 228 * 1024 / c - 1024 - (long long)S * pitch - sums;
+            const long long ahead = room / (warps * M * 1024);
+            if (ahead >= (GLU || !xh ? 2 : 4) && !(xh && c == 1 && k)) {
+                r.fits = true;
+                r.xh = xh;
+                r.ahead = ahead >= 4 ? 4 : 2;
+                r.warps = warps;
+                r.pitch = pitch;
+                r.grid = r.tiles < n_sms * c ? r.tiles : n_sms * c;
+                r.smem = S * pitch + sums + (long long)warps * M * r.ahead * 1024;
+                return r;
+            }
+        }
+    return r;                                           // x does not fit
+}
+
 template <int FMT, bool GLU, bool XH, int AHEAD>
-cudaError_t start(const MvParams &p, int device, int c, int warps, cudaStream_t st, bool *handled) {
-    constexpr int M = GLU ? 2 : 1;
-    const size_t smem = (size_t)(p.S * p.pitch + sums_bytes(warps, M, p.tiles <= sm_count(device) * c)) + (size_t)warps * M * AHEAD * 1024;
+cudaError_t start(const MvParams &p, const MvPlan &r, cudaStream_t st) {
     cudaError_t e = allow_dynamic_smem((const void *)qmv_q8_kernel<FMT, GLU, XH, AHEAD>, 227 * 1024);
     if (e != cudaSuccess) return e;
-    const int slots = sm_count(device) * c;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.tiles < slots ? p.tiles : slots);
-    cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3(r.grid);
+    cfg.blockDim = dim3(r.warps * 32);
+    cfg.dynamicSmemBytes = (size_t)r.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -309,14 +346,15 @@ cudaError_t start(const MvParams &p, int device, int c, int warps, cudaStream_t 
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, qmv_q8_kernel<FMT, GLU, XH, AHEAD>, p);
     count_launch();
-    *handled = true;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int FMT, bool GLU>
 cudaError_t run(const MatQ8 &a, cudaStream_t st, bool *handled) {
-    constexpr int KC = Fmt<FMT>::KC, M = GLU ? 2 : 1;
     const Tensor &t = *a.tg;
+    const MvPlan r = plan<FMT, GLU>(t.O, t.ld, a.S, sm_count(t.device));
+    if (!r.fits) return cudaSuccess;
+    *handled = true;
     MvParams p{};
     p.codes[0] = t.codes;
     p.scale[0] = t.scales;
@@ -335,41 +373,26 @@ cudaError_t run(const MatQ8 &a, cudaStream_t st, bool *handled) {
     p.O = t.O;
     p.I = t.I;
     p.S = a.S;
-    p.tiles = (t.O + kTileRows - 1) / kTileRows;
-    p.ng = (int)(t.ld / 64);
+    p.tiles = r.tiles;
+    p.ng = r.ng;
     p.act = a.act;
     p.type = a.type;
-    // CTAs per SM and warps per CTA.  First choice: every tile has its CTA from
-    // the start (up to eight CTAs of an SM's 32 warps), so that no CTA takes a
-    // second tile while others have none (6144 x 12288 int4, 384 tiles, one
-    // token: 12.0 us with 3 x 10 warps, 13.7 us with 2 x 16 and 304 of the 384
-    // tiles in the first round).  Otherwise 32 warps in a few CTAs that walk
-    // the tiles, 16 where x leaves no room for more.  x in f16 if it fits
-    // beside a ring of four steps (two of the pair) with two CTAs per SM or
-    // more, as bytes otherwise (12288 x 6144 int4, 8 tokens: f16 with one CTA
-    // 16.1 us, bytes with two 14.9 us).  Rows are 64 bytes off a 128-byte
-    // multiple: two tokens' reads differ in bank.
-    const int n_sms = sm_count(t.device), each = (p.tiles + n_sms - 1) / n_sms;
-    const int most = 32 / (each < 8 ? each : 8), steps = (p.ng + most - 1) / most;
-    const int shapes[5][2] = {{each, (p.ng + steps - 1) / steps}, {4, 8}, {2, 16}, {1, 32}, {1, 16}};
-    for (int xh = 1; xh >= 0; --xh)
-        for (int k = each <= 8 ? 0 : 1; k < 5; ++k) {
-            const int c = shapes[k][0], warps = shapes[k][1] < 4 ? 4 : shapes[k][1];     // four finish a tile
-            p.pitch = p.ng * (xh ? 8 : 4) * KC + 64;
-            const long long room =
-                228 * 1024 / c - 1024 - (long long)p.S * p.pitch - sums_bytes(warps, M, p.tiles <= n_sms * c);
-            const long long ahead = room / (warps * M * 1024);
-            if (ahead >= (GLU || !xh ? 2 : 4) && !(xh && c == 1 && k)) {
-                if (xh) return ahead >= 4 ? start<FMT, GLU, true, 4>(p, t.device, c, warps, st, handled)
-                                          : start<FMT, GLU, true, 2>(p, t.device, c, warps, st, handled);
-                return ahead >= 4 ? start<FMT, GLU, false, 4>(p, t.device, c, warps, st, handled)
-                                  : start<FMT, GLU, false, 2>(p, t.device, c, warps, st, handled);
-            }
-        }
-    return cudaSuccess;                                 // x does not fit: not handled here
+    p.pitch = r.pitch;
+    if (r.xh) return r.ahead == 4 ? start<FMT, GLU, true, 4>(p, r, st) : start<FMT, GLU, true, 2>(p, r, st);
+    return r.ahead == 4 ? start<FMT, GLU, false, 4>(p, r, st) : start<FMT, GLU, false, 2>(p, r, st);
 }
 
 }  // namespace
+
+MvPlan plan_mv_q8(int fmt, bool pair, int O, long long ld, int S, int n_sms) {
+    if (S > kTokens) return MvPlan{};
+    switch (fmt) {
+    case B200Q_I8: return pair ? plan<B200Q_I8, true>(O, ld, S, n_sms) : plan<B200Q_I8, false>(O, ld, S, n_sms);
+    case B200Q_I4: return pair ? plan<B200Q_I4, true>(O, ld, S, n_sms) : plan<B200Q_I4, false>(O, ld, S, n_sms);
+    case B200Q_I2: return pair ? plan<B200Q_I2, true>(O, ld, S, n_sms) : plan<B200Q_I2, false>(O, ld, S, n_sms);
+    }
+    return MvPlan{};
+}
 
 // S <= 8; *handled = false where x does not fit in shared memory.
 cudaError_t launch_mv_q8(const MatQ8 &a, cudaStream_t st, bool *handled) {
