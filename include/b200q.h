@@ -536,12 +536,12 @@ int b200q_glu_q8(const b200q_tensor *tg, const b200q_tensor *tu, const void *x8,
  * How b200q_matmul_q8 (pair = 0) or b200q_glu_q8 (pair = 1) would launch on a
  * GPU of n_sms multiprocessors; host arithmetic, needs no GPU.  out receives
  * B200Q_Q8_PLAN numbers: few-row kernel: takes the call (0 / 1), blocks, warps
- * per block, shared memory; tensor-core kernel: rows per launch, and of the
- * first launch rows per tile, tiles along the rows, tiles, k-blocks per tile,
+ * per block, shared memory; tensor-core kernel: rows per launch, launches, and
+ * of the first launch rows per tile, tiles along the rows, tiles, k-blocks per tile,
  * blocks, items (tiles x k-blocks), a block's run is a multiple of this many
  * items, tiles are shared by blocks (0 / 1), the sizes are taken (0 / 1).
  */
-enum { B200Q_Q8_PLAN = 14 };
+enum { B200Q_Q8_PLAN = 15 };
 int b200q_selftest_q8_plan(int fmt, int pair, int O, int I, int S, int n_sms, long long *out);
 
 /*

@@ -437,7 +437,7 @@ def glu_q8(tg, tu, xq, y, S: int, act: int = ACT_SILU, bias_g=None, bias_u=None,
                             act, yp, ty, ldy, S, _raw_stream(stream)))
 
 
-Q8_PLAN = ("few", "few_grid", "few_warps", "few_smem", "part", "N", "n_tiles", "tiles", "nk", "grid", "items", "grain",
+Q8_PLAN = ("few", "few_grid", "few_warps", "few_smem", "part", "launches", "N", "n_tiles", "tiles", "nk", "grid", "items", "grain",
            "cut", "ok")
 
 

@@ -918,8 +918,8 @@ extern "C" int b200q_selftest_q8_plan(int fmt, int pair, int O, int I, int S, in
     const MvPlan m = plan_mv_q8(fmt, pair != 0, O, (rb + kRowAlign - 1) / kRowAlign * kRowAlign, S, n_sms);
     const int part = gemm_q8_part(O, I);
     const GemmPlan g = plan_gemm_q8(fmt, pair != 0, O, I, S < part ? S : part, n_sms);
-    const long long v[B200Q_Q8_PLAN] = {m.fits,  m.grid,   m.warps,  m.smem, part,  g.N,   g.n_tiles,
-                                        g.tiles, g.nk,     g.grid,   g.items, g.grain, g.cut, g.ok};
+    const long long v[B200Q_Q8_PLAN] = {m.fits,  m.grid,   m.warps,  m.smem, part,    gemm_q8_parts(S, part), g.N,
+                                        g.n_tiles, g.tiles, g.nk,   g.grid, g.items, g.grain, g.cut, g.ok};
     for (int k = 0; k < B200Q_Q8_PLAN; ++k) out[k] = v[k];
     return B200Q_OK;
 }

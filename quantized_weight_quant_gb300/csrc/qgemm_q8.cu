@@ -794,11 +794,11 @@ GemmPlan plan(int O, int I, int S, int n_sms) {
     constexpr int C_BYTES = BM * Fmt<FMT>::CB;
     GemmPlan r{};
     // rows of x8 per tile: the fewest tiles of at most kMaxN rows, evenly filled
-    const int n_tiles = (S + kMaxN - 1) / kMaxN;
-    const int N = r.N = ((S + n_tiles - 1) / n_tiles + 15) / 16 * 16;
-    const int nk = r.nk = (I + BK - 1) / BK;
-    r.n_tiles = (S + N - 1) / N;
-    const long long m_tiles = GLU ? (O + 63) / 64 : (O + 127) / 128;
+    const int n_tiles = (int)((S + (kMaxN - 1ll)) / kMaxN);
+    const int N = r.N = (int)(((S + (n_tiles - 1ll)) / n_tiles + 15) / 16 * 16);
+    const int nk = r.nk = (int)((I + (BK - 1ll)) / BK);
+    r.n_tiles = (int)((S + (N - 1ll)) / N);
+    const long long m_tiles = GLU ? (O + 63ll) / 64 : (O + 127ll) / 128;
     const long long tiles = r.tiles = m_tiles * r.n_tiles;
     if (tiles * nk > 0x7ffffff0ll) return r;
     r.items = (int)(tiles * nk);
@@ -908,18 +908,22 @@ GemmPlan plan_gemm_q8(int fmt, bool pair, int O, int I, int S, int n_sms) {
 
 // Item numbers are 32-bit: longer batches in parts of at most 2^16 rows, fewer for a large tensor.
 int gemm_q8_part(int O, int I) {
-    const long long row_items = ((O + 63ll) / 64) * ((I + BK - 1ll) / BK);
+    const long long row_items = ((O + 63ll) / 64) * ((I + (BK - 1ll)) / BK);
     int part = 1 << 16;
     while (part > 128 && row_items * ((part + kMaxN - 1) / kMaxN) > 0x7ffffff0ll) part /= 2;
     return part;
 }
 
+int gemm_q8_parts(int S, int part) { return (int)((S + (part - 1ll)) / part); }
+
 cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st) {
     const int part = gemm_q8_part(a.tg->O, a.tg->I);
     const long long b = a.type == B200Q_T_F32 ? 4 : 2;
-    for (int s0 = 0; s0 < a.S; s0 += part) {
+    const int parts = gemm_q8_parts(a.S, part);
+    for (int k = 0; k < parts; ++k) {
+        const long long s0 = (long long)k * part;
         MatQ8 c = a;
-        c.S = a.S - s0 < part ? a.S - s0 : part;
+        c.S = (int)(a.S - s0 < part ? a.S - s0 : part);
         c.x8 += s0 * a.ld8;
         c.xs += s0;
         c.y = (char *)a.y + s0 * a.ldy * b;

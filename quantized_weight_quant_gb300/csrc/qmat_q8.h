@@ -28,6 +28,7 @@ struct GemmPlan {              // one launch of the tcgen05 kernel
 MvPlan plan_mv_q8(int fmt, bool pair, int O, long long ld, int S, int n_sms);
 GemmPlan plan_gemm_q8(int fmt, bool pair, int O, int I, int S, int n_sms);
 int gemm_q8_part(int O, int I);         // rows of x8 per launch
+int gemm_q8_parts(int S, int part);     // launches
 
 // v, activated.  f32 expf / erff; for large |v| the exponentials
 // overflow or vanish to the activation's limits.  __fdividef (2 ulp) gives 0

@@ -304,24 +304,24 @@ template <int FMT, bool GLU>
 MvPlan plan(int O, long long ld, int S, int n_sms) {
     constexpr int KC = Fmt<FMT>::KC, M = GLU ? 2 : 1;
     MvPlan r{};
-    r.tiles = (O + kTileRows - 1) / kTileRows;
+    r.tiles = (int)((O + (kTileRows - 1ll)) / kTileRows);
     r.ng = (int)(ld / 64);
-    const int each = (r.tiles + n_sms - 1) / n_sms;
+    const int each = (int)((r.tiles + (n_sms - 1ll)) / n_sms);
     const int most = 32 / (each < 8 ? each : 8), steps = (r.ng + most - 1) / most;
     const int shapes[5][2] = {{each, (r.ng + steps - 1) / steps}, {4, 8}, {2, 16}, {1, 32}, {1, 16}};
     for (int xh = 1; xh >= 0; --xh)
         for (int k = each <= 8 ? 0 : 1; k < 5; ++k) {
             const int c = shapes[k][0], warps = shapes[k][1] < 4 ? 4 : shapes[k][1];     // four finish a tile
-            const int pitch = r.ng * (xh ? 8 : 4) * KC + 64;
+            const long long pitch = (long long)r.ng * (xh ? 8 : 4) * KC + 64;      // past 2^31 for the longest rows
             const long long sums = sums_bytes(warps, M, r.tiles <= n_sms * c);
-            const long long room = 228 * 1024 / c - 1024 - (long long)S * pitch - sums;
+            const long long room = 228 * 1024 / c - 1024 - S * pitch - sums;
             const long long ahead = room / (warps * M * 1024);
             if (ahead >= (GLU || !xh ? 2 : 4) && !(xh && c == 1 && k)) {
                 r.fits = true;
                 r.xh = xh;
                 r.ahead = ahead >= 4 ? 4 : 2;
                 r.warps = warps;
-                r.pitch = pitch;
+                r.pitch = (int)pitch;
                 r.grid = r.tiles < n_sms * c ? r.tiles : n_sms * c;
                 r.smem = S * pitch + sums + (long long)warps * M * r.ahead * 1024;
                 return r;

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kLongThreads) rows_q8_long_kernel(const RowsQ8
     uint8_t *y = a.y8 + row * a.ld8;
     float ss = 0.f;
     unsigned m = 0;
-    for (int d = threadIdx.x; d < a.D; d += kLongThreads) {
+    const unsigned D = a.D;                      // d passes 2^31 - 1 by up to a block
+    for (unsigned d = threadIdx.x; d < D; d += kLongThreads) {
         const float v = r ? to_f<T>(x[d]) + to_f<T>(r[d]) : to_f<T>(x[d]);
         ss = fmaf(v, v, ss);
         m = max(m, magnitude(a.w ? v * a.w[d] : v));
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kLongThreads) rows_q8_long_kernel(const RowsQ8
     if (a.w) norm_scale(a, ss, __uint_as_float(m), s, f);
     if (threadIdx.x == 0) a.ys[row] = s;
     const float rs = 1.f / s;
-    for (int d = threadIdx.x; d < a.D; d += kLongThreads) {
+    for (unsigned d = threadIdx.x; d < D; d += kLongThreads) {
         const float v = r ? to_f<T>(x[d]) + to_f<T>(r[d]) : to_f<T>(x[d]);
         if (h) h[d] = from_f<T>(v);                             // after this thread's last read of x[d], r[d]
         y[d] = (uint8_t)e4m3x2(a.w ? v * a.w[d] * f.x * f.y : div_by(v, s, rs), 0.f);
@@ -326,7 +327,7 @@ cudaError_t run(const RowsQ8 &a, cudaStream_t st) {
         return !p || ((uintptr_t)p % 16 == 0 && ld * (long long)sizeof(T) % 16 == 0);
     };
     const bool aligned = ok(a.x, a.ldx) && ok(a.r, a.ldr) && ok(a.h, a.ldh) && (uintptr_t)a.w % 16 == 0;
-    const int units = (a.D + E - 1) / E;             // 16-byte vectors of a row
+    const int units = (int)((a.D + (E - 1ll)) / E);           // 16-byte vectors of a row
     int dev = 0;
     cudaGetDevice(&dev);
     // Few rows: as many threads as there are vectors, the shortest chain (6144

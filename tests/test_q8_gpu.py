@@ -609,3 +609,20 @@ def test_rmsnorm_odd_rows_in_place(q, S, D, kind):
     keep[3:3 + S * D] = want.view(-1)
     assert torch.equal(buf, keep)
     _check_rows(*_quantised(q, out, D), y)
+
+
+def test_longest_row_to_8_bits(q):
+    """2^31 - 1 columns: column numbers pass 31 bits in the last step of the walk."""
+    import torch
+    D = 2 ** 31 - 1
+    x = torch.zeros(1, D, dtype=torch.float16, device="cuda")
+    for d, v in ((0, -224.0), (2 ** 30 + 5, 3.0), (D - 1, 448.0)):
+        x[0, d] = v
+    out = q.Q8Rows(1, D)
+    out.codes.fill_(0x5A)
+    q.quantize_q8(x, out, 1, D)
+    torch.cuda.synchronize()
+    assert float(out.scales[0]) == 1.0
+    got = [int(out.codes[0, d]) for d in (0, 2 ** 30 + 5, D - 1, D)]
+    assert got == [0xF6, 0x44, 0x7E, 0x5A]                  # -224, 3, 448, not written
+    assert sum(int(torch.count_nonzero(c)) for c in out.codes[0].split(2 ** 28)) == 4

@@ -45,3 +45,26 @@ def test_plans_are_whole(q):
         assert starts[0] == 0 and starts[-1] == p["items"] and all(a < b for a, b in zip(starts, starts[1:])), what
         shared = any(s % p["nk"] for s in starts)
         assert shared == bool(p["cut"]), what
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("pair", [0, 1])
+@pytest.mark.parametrize("fmt", [1, 2, 3])
+@pytest.mark.parametrize("I", [2 ** 30 - 1, 2 ** 30, 2 ** 30 + 77, INT_MAX - 75000, INT_MAX - 200, INT_MAX - 64, INT_MAX])
+def test_longest_rows(q, fmt, pair, I):
+    """Rows of up to 2^31 - 1 codes: x never fits in the few-row kernel's shared memory, and the k-blocks are counted."""
+    for S in range(1, 9):
+        p = q.selftest_q8_plan(fmt, pair, 40, I, S)
+        assert p["few"] == 0, (S, p)
+        assert p["ok"] and p["nk"] == (I + 127) // 128 and p["items"] == p["tiles"] * p["nk"], (S, p)
+
+
+def test_most_rows(q):
+    """Batches of up to 2^31 - 1 rows are cut into launches that end."""
+    for S in (1, 2 ** 16, 2 ** 16 + 1, INT_MAX - 2 ** 16, INT_MAX - 1, INT_MAX):
+        p = q.selftest_q8_plan(2, 0, 40, 64, S)
+        assert p["part"] == 2 ** 16 and p["launches"] == -(-S // 2 ** 16), (S, p)
+    p = q.selftest_q8_plan(1, 0, INT_MAX, 64, 9)
+    assert p["tiles"] == -(-INT_MAX // 128)
