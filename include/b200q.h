@@ -545,6 +545,16 @@ enum { B200Q_Q8_PLAN = 15 };
 int b200q_selftest_q8_plan(int fmt, int pair, int O, int I, int S, int n_sms, long long *out);
 
 /*
+ * Self test of how the tensor-core kernel of the 8-bit products gives up: sets
+ * the limit of its waits on the current device to wait_ns nanoseconds, 0 ..
+ * 2 * 10^9 (-1: back to the 2 s it starts with), and records `status` as a
+ * kernel of it would (B200Q_OK: nothing), for b200q_device_status to report.
+ * With a limit of 0 a call with long rows gives up: y is not whole, and the
+ * status is B200Q_ETIMEOUT.  Synchronizes the device.
+ */
+int b200q_selftest_q8(long long wait_ns, int status);
+
+/*
  * Self test of the bounded waits: one kernel waits, at most wait_us
  * microseconds (1 .. 10^6), on an mbarrier that nothing arrives on, gives up
  * and records B200Q_ETIMEOUT the way a kernel whose copies never land does.

@@ -80,6 +80,8 @@ def _load():
     L.b200q_glu_q8.restype = ci
     L.b200q_selftest_q8_plan.argtypes = [ci, ci, ci, ci, ci, ci, vp]
     L.b200q_selftest_q8_plan.restype = ci
+    L.b200q_selftest_q8.argtypes = [cll, ci]
+    L.b200q_selftest_q8.restype = ci
     L.b200q_selftest_timeout.argtypes = [ci, vp]
     L.b200q_selftest_timeout.restype = ci
     L.b200q_silu_mul.argtypes = [vp, vp, vp, cl, vp]
@@ -446,6 +448,12 @@ def selftest_q8_plan(fmt: int, pair: bool, O: int, I: int, S: int, n_sms: int = 
     out = (ctypes.c_longlong * len(Q8_PLAN))()
     _check(lib.b200q_selftest_q8_plan(fmt, int(pair), O, I, S, n_sms, out))
     return dict(zip(Q8_PLAN, out))
+
+
+def selftest_q8(wait_ns: int = -1, status: int = OK) -> None:
+    """The limit of the 8-bit tensor-core kernel's waits (-1: its own 2 s), and a
+    status for device_status() to report (b200q_selftest_q8)."""
+    _check(lib.b200q_selftest_q8(wait_ns, status))
 
 
 def selftest_timeout(wait_us: int, stream=None) -> None:

@@ -29,6 +29,7 @@ cudaError_t decode_take_error(unsigned int *code);
 cudaError_t launch_tcs(const Tensor &t, const float *x, float *y, int S, cudaStream_t st, bool *handled);
 cudaError_t tcs_take_error(unsigned int *code);
 cudaError_t q8_take_error(unsigned int *code);
+cudaError_t q8_selftest(long long wait_ns, unsigned int code);
 size_t noalloc_capacity();
 cudaError_t launch_prefill_tc_noalloc(const Tensor &t, const float *x, float *y, int S, cudaStream_t st);
 cudaError_t prefill_take_error(unsigned int *code);
@@ -921,6 +922,17 @@ extern "C" int b200q_selftest_q8_plan(int fmt, int pair, int O, int I, int S, in
     const long long v[B200Q_Q8_PLAN] = {m.fits,  m.grid,   m.warps,  m.smem, part,    gemm_q8_parts(S, part), g.N,
                                         g.n_tiles, g.tiles, g.nk,   g.grid, g.items, g.grain, g.cut, g.ok};
     for (int k = 0; k < B200Q_Q8_PLAN; ++k) out[k] = v[k];
+    return B200Q_OK;
+}
+
+extern "C" int b200q_selftest_q8(long long wait_ns, int status) {
+    const char *who = "b200q_selftest_q8";
+    if (wait_ns < -1 || wait_ns > 2000000000ll)
+        return fail(B200Q_EINVAL, "%s: wait_ns must be in [-1, 2 * 10^9] (got %lld)", who, wait_ns);
+    if (status > 0 || status < B200Q_ETIMEOUT) return fail(B200Q_EINVAL, "%s: unknown status %d", who, status);
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = q8_selftest(wait_ns, (unsigned)-status);
+    if (e != cudaSuccess) return cuda_fail(e, who);
     return B200Q_OK;
 }
 

@@ -61,9 +61,10 @@ constexpr int kSmemLimit = 232448;
 constexpr int kSmemFloor = 120 * 1024;      // one CTA per SM: it takes the whole tensor memory
 constexpr int kMiscBytes = 512 + 3 * kMaxN * 4;   // barriers and counters, row scales of three tiles
 constexpr int kMaxStages = 12;
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr long long kWaitNs = 2000000000ll, kDrainNs = kWaitNs / 4;
 
 __device__ unsigned int g_q8_err = 0;
+__device__ long long g_q8_wait_ns = kWaitNs;      // limit of the waits; b200q_selftest_q8 shortens it
 
 // PIECES: E4M3 values per code.  CB: code bytes per row and k-block.
 // GROUPS: A buffers, and groups of four dequantizing warps (one per tensor-
@@ -111,15 +112,17 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Waits for a phase; gives up after kWaitNs, or soon after another role has.
+__device__ __forceinline__ long long wait_limit() { return *(volatile long long *)&g_q8_wait_ns; }
+
+// Waits for a phase; gives up after the limit, or soon after another role has.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     unsigned long long t0 = 0;
     for (uint32_t it = 0;; ++it) {
         if (mbar_test(bar, parity)) return true;
-        if ((it & 63) == 63) {
+        if ((it & 7) == 7) {
             if (*abort) return false;
             if (t0 == 0) t0 = global_ns();
-            else if ((long long)(global_ns() - t0) > (long long)kWaitNs) {
+            else if ((long long)(global_ns() - t0) > wait_limit()) {
                 atomicExch(&g_q8_err, (unsigned)(-B200Q_ETIMEOUT));
                 *abort = 1;
                 return false;
@@ -129,10 +132,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // Waits whether or not the CTA is winding down (copies and MMAs in flight must
-// finish before it leaves), for a quarter of kWaitNs at most.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = global_ns();
-    while (!mbar_test(bar, parity) && (long long)(global_ns() - t0) < (long long)(kWaitNs / 4)) {
+// finish before it leaves), up to kDrainNs after t0, the start of the role's
+// draining.  (A stage that one producer filled and another gave up on never
+// completes: its copies land within that time.)
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsigned long long t0) {
+    while (!mbar_test(bar, parity) && (long long)(global_ns() - t0) < kDrainNs) {
     }
 }
 
@@ -244,7 +248,7 @@ __device__ __forceinline__ bool cnt_wait(uint32_t addr, uint32_t want, volatile 
         if ((it & 255) == 255) {
             if (*abort) return false;
             if (t0 == 0) t0 = global_ns();
-            else if ((long long)(global_ns() - t0) > (long long)kWaitNs) {
+            else if ((long long)(global_ns() - t0) > wait_limit()) {
                 atomicExch(&g_q8_err, (unsigned)(-B200Q_ETIMEOUT));
                 *abort = 1;
                 return false;
@@ -612,8 +616,9 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         }
         __syncwarp();
         // the last copies land before the CTA may leave (a completed phase returns at once)
+        const unsigned long long t0 = global_ns();
         for (int k = issued < kStages ? 0 : issued - kStages; k < issued; ++k)
-            mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1));
+            mbar_drain(smem_u32(&full[k % kStages]), (uint32_t)((k / kStages) & 1), t0);
     } else if (warp == kWMma) {
         // ---------------- MMA issuer: the whole warp walks the items, one lane issues
         const bool leader = elect_one();
@@ -656,7 +661,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         // everything issued, also before giving up, and its arrivals in shared memory land before the CTA may leave
         __syncwarp();
         if (leader) mma_commit(smem_u32(fin));
-        mbar_drain(smem_u32(fin), 0);
+        mbar_drain(smem_u32(fin), 0, global_ns());
     } else if (warp < kWEpi) {
         // ---------------- dequantizers: group g, items g, g + GROUPS, ..., one thread per row
         const int quarter = warp & 3, g = (warp - kWDeq) >> 2;
@@ -943,6 +948,13 @@ cudaError_t q8_take_error(unsigned int *code) {
     unsigned int zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(code, g_q8_err, sizeof(unsigned int));
     if (e == cudaSuccess && *code) e = cudaMemcpyToSymbol(g_q8_err, &zero, sizeof(unsigned int));
+    return e;
+}
+
+cudaError_t q8_selftest(long long wait_ns, unsigned int code) {
+    const long long ns = wait_ns < 0 ? kWaitNs : wait_ns;
+    cudaError_t e = cudaMemcpyToSymbol(g_q8_wait_ns, &ns, sizeof ns);
+    if (e == cudaSuccess && code) e = cudaMemcpyToSymbol(g_q8_err, &code, sizeof code);
     return e;
 }
 

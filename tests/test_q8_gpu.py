@@ -626,3 +626,41 @@ def test_longest_row_to_8_bits(q):
     got = [int(out.codes[0, d]) for d in (0, 2 ** 30 + 5, D - 1, D)]
     assert got == [0xF6, 0x44, 0x7E, 0x5A]                  # -224, 3, 448, not written
     assert sum(int(torch.count_nonzero(c)) for c in out.codes[0].split(2 ** 28)) == 4
+
+
+def _long_call(q):
+    """Rows so long that every block of the tensor-core kernel walks for more than 0.1 ms, in one tile that all share."""
+    import torch
+    O, I, S = 40, 10_000_000, 9
+    codes = synth.rng(1, 2).integers(0, 256, (O, I // 4), dtype=np.uint8)
+    t = q.tensor_upload(q.I2, O, I, codes, np.ones(O, np.float32))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    xq = q.Q8Rows(S, I)
+    xq.codes.copy_(torch.randint(0, 0x50, xq.codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+    xq.scales.fill_(0.5)
+    return t, xq, O, S
+
+
+def test_giving_up_is_reported(q):
+    """A wait that runs out ends the kernel with a status; the next call is whole again."""
+    import torch
+    t, xq, O, S = _long_call(q)
+    want, y = torch.empty(S, O, device="cuda"), torch.empty(S, O, device="cuda")
+    with t:
+        q.matmul_q8(t, xq, want, S)
+        assert q.device_status() == q.OK
+        try:
+            q.selftest_q8(0)
+            q.matmul_q8(t, xq, y, S)
+            with pytest.raises(q.B200QError) as e:
+                q.device_status()
+            assert e.value.status == q.ETIMEOUT
+        finally:
+            q.selftest_q8(-1)
+        q.matmul_q8(t, xq, y, S)
+        assert q.device_status() == q.OK
+        assert torch.equal(y, want)
+    for bad in ((-2, 0), (1 << 40, 0), (-1, 1), (-1, -9)):
+        with pytest.raises(q.B200QError):
+            q.selftest_q8(*bad)
