@@ -380,6 +380,33 @@ __device__ __forceinline__ int owner_of(const Q8Params &p, int i) {
     return (int)(((i + 1ll) * (long long)gridDim.x - 1) / p.items);
 }
 
+// One more CTA has written its plane of a cut tile; true for the last.
+__device__ __forceinline__ bool arrive(const Q8Params &p, int tile) {
+    const int t0 = tile * p.nk, pieces = owner_of(p, t0 + p.nk - 1) - owner_of(p, t0) + 1;
+    const unsigned long long tag = p.token << 10;
+    unsigned long long old = *(volatile unsigned long long *)&p.cnt[tile];
+    for (;;) {
+        const int n = (old >> 10) == p.token ? (int)(old & 1023) + 1 : 1;
+        const unsigned long long prev = cas_acq_rel(&p.cnt[tile], old, n == pieces ? 0ull : tag | (unsigned)n);
+        if (prev == old) return n == pieces;
+        old = prev;
+    }
+}
+
+// A CTA that gave up arrives at its cut tiles from item i on all the same, with
+// nothing written: their outputs are lost, which the status says, but every
+// count is back at 0 when the launch ends.  (A count that stayed would go on
+// under the same tag in a captured launch's next replay, and complete its tile
+// before the planes are there.)
+__device__ __forceinline__ void arrive_rest(const Q8Params &p, int i, int i1) {
+    if (!p.planes) return;
+    while (i < i1) {
+        const int tile = i / p.nk, t0 = tile * p.nk, end = min(t0 + p.nk, i1);
+        if (i != t0 || end != t0 + p.nk) arrive(p, tile);
+        i = end;
+    }
+}
+
 template <class T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
@@ -577,7 +604,10 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     // all columns are this CTA's, so they start at 0; anything else would be addressed wrongly below
     constexpr uint32_t tmem_base = 0;
     if (*tmem_slot != tmem_base) {
-        if (threadIdx.x == 0) atomicExch(&g_q8_err, (unsigned)(-B200Q_ECUDA));
+        if (threadIdx.x == 0) {
+            atomicExch(&g_q8_err, (unsigned)(-B200Q_ECUDA));
+            arrive_rest(p, i0, i1);
+        }
         __syncthreads();
         if (warp == kWMma)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols)
@@ -697,8 +727,8 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         constexpr int kEpi = kEpiWarps * 32, W = GLU ? 16 : 8;
         const int quarter = warp & 3, et = threadIdx.x - kWEpi * 32;
         const int arow = quarter * 32 + lane;
-        int t = 0;
-        for (int i = i0; i < i1; ++t) {
+        int t = 0, i = i0;
+        for (; i < i1; ++t) {
             const int tile = i / p.nk, t0 = tile * p.nk, t1 = t0 + p.nk;
             const int end = min(t1, i1);
             const bool whole = i == t0 && end == t1;
@@ -739,27 +769,15 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < W; ++j) pl[(c + j) * BM] = v[j];
                 }
-                const int pieces = owner_of(p, t1 - 1) - owner_of(p, t0) + 1;
                 named_sync(1, kEpi);
-                if (et == 0) {
-                    const unsigned long long tag = p.token << 10;
-                    unsigned long long old = *(volatile unsigned long long *)&p.cnt[tile];
-                    int n;
-                    for (;;) {
-                        n = (old >> 10) == p.token ? (int)(old & 1023) + 1 : 1;
-                        const unsigned long long nv = n == pieces ? 0ull : tag | (unsigned)n;
-                        const unsigned long long prev = cas_acq_rel(&p.cnt[tile], old, nv);
-                        if (prev == old) break;
-                        old = prev;
-                    }
-                    completed[t != 0] = n == pieces;           // only a CTA's first and last tiles are cut
-                }
+                if (et == 0) completed[t != 0] = arrive(p, tile);      // only a CTA's first and last tiles are cut
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&acc_empty[t & 1]));
             i = end;
         }
+        if (et == 0) arrive_rest(p, i, i1);
     }
 
     // Cut tiles that this CTA completed, with the dequantizers' help (their work is done): 176 rows of
@@ -784,8 +802,9 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
 // A launch's 54-bit tag: every launch its own, and spread over all bits (the
 // finalizer of splitmix64: G. Steele, D. Lea, C. Flood, "Fast splittable
 // pseudorandom number generators", 2014), so that what an earlier use left in
-// the workspace does not look like one.  A count returns to 0 when its tile is
-// complete, so a captured launch finds no count of its last replay.
+// the workspace does not look like one.  A count returns to 0 when all of its
+// tile's CTAs have arrived, which those that give up do too, so a captured
+// launch finds no count of its last replay.
 unsigned long long next_token() {
     static std::atomic<unsigned long long> launches{0};
     unsigned long long z = (launches.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull;

@@ -664,3 +664,38 @@ def test_giving_up_is_reported(q):
     for bad in ((-2, 0), (1 << 40, 0), (-1, 1), (-1, -9)):
         with pytest.raises(q.B200QError):
             q.selftest_q8(*bad)
+
+
+def test_replay_after_giving_up(q):
+    """A captured call whose blocks partly gave up leaves nothing behind that its next replay takes for its own."""
+    import torch
+    t, xq, O, S = _long_call(q)
+    inputs = [xq.codes.clone(), xq.codes.flip(0).clone()]
+    want, y = [torch.empty(S, O, device="cuda") for _ in inputs], torch.empty(S, O, device="cuda")
+    with t:
+        for c, w in zip(inputs, want):
+            xq.codes.copy_(c)
+            q.matmul_q8(t, xq, w, S)
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            q.matmul_q8(t, xq, y, S, stream=st)
+        gave_up = 0
+        for k in range(40):
+            xq.codes.copy_(inputs[k % 2])
+            q.selftest_q8(5000 * k)
+            graph.replay()
+            try:
+                q.device_status()
+            except q.B200QError as e:
+                assert e.status == q.ETIMEOUT
+                gave_up += 1
+            finally:
+                q.selftest_q8(-1)
+            xq.codes.copy_(inputs[1 - k % 2])
+            y.fill_(float("nan"))
+            graph.replay()
+            assert q.device_status() == q.OK
+            assert torch.equal(y, want[1 - k % 2]), "after a limit of %d ns" % (5000 * k)
+        assert gave_up
