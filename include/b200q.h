@@ -488,7 +488,7 @@ int b200q_quantize_q8(const void *x, int type, long long ldx, void *y8, long lon
  *   y8, ys as in b200q_quantize_q8; they must not overlap x, r, h, w or each other
  *   eps    >= 0 and finite
  * A row that holds an infinity or a NaN, or whose sum of squares exceeds f32,
- * gets the scale NaN.
+ * gets the scale NaN, and so does every row where w holds a NaN.
  * S = 0 is a no-op.  Asynchronous on `stream`; one launch, no workspace.
  */
 int b200q_rmsnorm_q8(const void *x, const void *r, void *h, int type, long long ldx, long long ldr, long long ldh,

@@ -98,6 +98,14 @@ __device__ __forceinline__ void norm_scale(const RowsQ8 &a, float ss, float m, f
 
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }   // orders as |v|, NaN last
 
+// The larger, or NaN if either is one (fmaxf drops a NaN: a weight that is one
+// would leave the scale finite).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The 16 bytes from offset sh (0..15) on of two neighbouring vectors.  sh is
 // the same for all vectors of a row.
 __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint32_t sh) {
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) rmsnorm_q8
         for (int j = 0; j < E; ++j) {
             ss = fmaf(v[k][j], v[k][j], ss);
             v[k][j] *= g[j];
-            m = fmaxf(m, fabsf(v[k][j]));
+            m = max_nan(m, fabsf(v[k][j]));
         }
     }
     unsigned mb = __float_as_uint(m);

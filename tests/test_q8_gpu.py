@@ -699,3 +699,19 @@ def test_replay_after_giving_up(q):
             assert q.device_status() == q.OK
             assert torch.equal(y, want[1 - k % 2]), "after a limit of %d ns" % (5000 * k)
         assert gave_up
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("res", [False, True], ids=["x", "x+r"])
+@pytest.mark.parametrize("S,D", [(3, 5), (400, 96), (2, 501), (2, 6144), (3, 5003), (2, 20000)])
+def test_rmsnorm_with_a_bad_weight(q, S, D, kind, res):
+    """The scale is the largest |y| / 448: where a weight is NaN or infinite it is not finite in any row."""
+    import torch
+    x, r = _dev(_rows(S, D, D), kind), _dev(synth.normal_f32((S, D), D, 2), kind) if res else None
+    for bad in (float("nan"), float("inf")):
+        w = _dev(synth.uniform_f32((D,), 0.5, 1.5, D, 3))
+        w[D // 2] = bad
+        out = _fresh(q, S, D)
+        q.rmsnorm_q8(x, w, out, S, D, 1e-6, r=r)
+        torch.cuda.synchronize()
+        assert not torch.isfinite(out.scales).any()
