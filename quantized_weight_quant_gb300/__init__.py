@@ -313,7 +313,8 @@ class Q8Rows:
     """S activation rows of D values in 8 bits, on the device: `codes`, uint8
     [S, ld] E4M3 bytes (ld: D rounded up to 16; bytes past D are unused), and
     `scales`, f32 [S].  A row stands for codes * scale.  Both may be replaced
-    by tensors of the caller's (views of larger buffers, say)."""
+    by tensors of the caller's (views of larger buffers, say), or changed in
+    place (resize_, set_): every call looks at what they are then."""
 
     def __init__(self, S: int, D: int, device="cuda"):
         import torch
@@ -333,6 +334,7 @@ class Q8Rows:
         self._codes, self._values = c, c[:, :self.D].view(torch.float8_e4m3fn)
         self._rows, self._cp = (c.shape[0] if c.is_cuda else -1), c.data_ptr()
         self._ld = c.stride(0) if c.shape[0] > 1 else max(c.stride(0), c.shape[1])
+        self._cshape, self._cstride = c.shape, c.stride()
 
     @property
     def scales(self):
@@ -344,9 +346,19 @@ class Q8Rows:
         if s.dtype != torch.float32 or s.dim() != 1 or not s.is_contiguous():
             raise ValueError("8-bit rows: expected contiguous float32 scales [rows]")
         self._scales, self._sp, self._srows = s, s.data_ptr(), (s.shape[0] if s.is_cuda else -1)
+        self._sshape, self._sstride = s.shape, s.stride()
+
+    def _look(self):
+        """Takes the tensors as they are now, if they were changed in place."""
+        c, s = self._codes, self._scales
+        if c.data_ptr() != self._cp or c.shape != self._cshape or c.stride() != self._cstride:
+            self.codes = c
+        if s.data_ptr() != self._sp or s.shape != self._sshape or s.stride() != self._sstride:
+            self.scales = s
 
     def values(self):
         """The codes as E4M3 numbers, float8_e4m3fn [S, D] (a view)."""
+        self._look()
         return self._values
 
 
@@ -379,6 +391,7 @@ def _q8(a, S: int, D: int):
     """(codes pointer, row stride, scales pointer) of a Q8Rows."""
     if not isinstance(a, Q8Rows):
         raise TypeError("8-bit rows: expected a Q8Rows")
+    a._look()
     if a.D != D or a._rows < S or a._srows < S:
         raise ValueError("8-bit rows: expected %d CUDA rows of %d columns" % (S, D))
     return a._cp, a._ld, a._sp
@@ -392,14 +405,21 @@ def _vec(a, n: int, name: str) -> int:
     return _dptr(a)
 
 
+_RAW = None
+
+
 def _raw_stream(stream) -> int:
     """_stream, without building a torch stream object for the default."""
-    if stream is None:
+    global _RAW
+    if stream is not None:
+        return _stream(stream)
+    if _RAW is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch._C._cuda_getDevice())
-    return _stream(stream)
+        if raw is None or not torch.cuda.is_initialized():
+            return _stream(None)
+        _RAW = raw, torch._C._cuda_getDevice
+    return _RAW[0](_RAW[1]())
 
 
 def quantize_q8(x, out, S: int, D: int, stream=None) -> None:

@@ -63,3 +63,27 @@ def test_binding_refusals(q):
         q.quantize_q8([1.0], None, 1, 1)
     rows = q.Q8Rows(3, 50, device="cpu")
     assert rows.codes.shape == (3, 64) and rows.values().shape == (3, 50)
+
+
+def test_rows_changed_in_place(q):
+    """codes and scales are the caller's to resize or to point elsewhere: nothing goes by an earlier address."""
+    import torch
+    rows = q.Q8Rows(3, 50, device="cpu")
+    old = rows.codes.data_ptr()
+    new = torch.full((5, 80), 0x38, dtype=torch.uint8)
+    rows.codes.set_(new)
+    assert rows.values().data_ptr() == new.data_ptr() != old
+    assert rows.values().shape == (5, 50) and (rows.values().float() == 1).all()
+    rows._look()
+    assert rows._cp == new.data_ptr() and rows._ld == 80
+    scales = torch.ones(7)
+    rows.scales.set_(scales)
+    rows._look()
+    assert rows._sp == scales.data_ptr()
+    rows.codes.resize_(2, 40)
+    with pytest.raises(ValueError):
+        rows.values()                                 # 40 columns for 50
+    rows = q.Q8Rows(3, 50, device="cpu")
+    rows.scales.set_(torch.ones(6)[::2])
+    with pytest.raises(ValueError):
+        rows._look()                                  # not contiguous

@@ -715,3 +715,26 @@ def test_rmsnorm_with_a_bad_weight(q, S, D, kind, res):
         q.rmsnorm_q8(x, w, out, S, D, 1e-6, r=r)
         torch.cuda.synchronize()
         assert not torch.isfinite(out.scales).any()
+
+
+def test_rows_changed_in_place(q):
+    """A call reads and writes the tensors that a Q8Rows holds now, and counts their rows now."""
+    import torch
+    S, D = 4, 96
+    x, out = _dev(_rows(S, D, 1)), q.Q8Rows(S, D)
+    q.quantize_q8(x, out, S, D)
+    codes, scales = out.codes, out.scales
+    before = codes.clone(), scales.clone()
+    kept = codes.view(codes.shape), scales.view(scales.shape)      # the old memory stays allocated
+    codes.set_(torch.zeros(S, 112, dtype=torch.uint8, device="cuda"))
+    scales.set_(torch.zeros(S, device="cuda"))
+    q.quantize_q8(2 * x, out, S, D)
+    torch.cuda.synchronize()
+    assert torch.equal(codes[:, :D], before[0][:, :D]) and torch.equal(scales, 2 * before[1])
+    assert torch.equal(kept[0], before[0]) and torch.equal(kept[1], before[1])
+    codes.resize_(S - 1, 112)
+    with pytest.raises(ValueError):
+        q.quantize_q8(x, out, S, D)
+    q.quantize_q8(x, out, S - 1, D)
+    torch.cuda.synchronize()
+    assert torch.equal(scales[:S - 1], before[1][:S - 1])
