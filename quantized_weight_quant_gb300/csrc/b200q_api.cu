@@ -250,6 +250,8 @@ int b200q_device_status(void) {
     if (e == cudaSuccess) e = tcs_take_error(&c);
     if (e == cudaSuccess) e = q8_take_error(&d);
     if (e != cudaSuccess) return cuda_fail(e, "b200q_device_status");
+    if (d == (unsigned)(-B200Q_ECUDA))
+        return fail(B200Q_ECUDA, "b200q_device_status: an 8-bit product found its tensor memory at another base than 0");
     if (a || b || c || d || m == (unsigned)(-B200Q_ETIMEOUT))
         return fail(B200Q_ETIMEOUT, "b200q_device_status: a kernel gave up on a bounded wait");
     if (m) return fail(B200Q_EINVAL, "b200q_device_status: an MLA call met a NULL or unaligned cache page");

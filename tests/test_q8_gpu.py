@@ -738,3 +738,13 @@ def test_rows_changed_in_place(q):
     q.quantize_q8(x, out, S - 1, D)
     torch.cuda.synchronize()
     assert torch.equal(scales[:S - 1], before[1][:S - 1])
+
+
+def test_status_codes(q):
+    """What the tensor-core kernel records is reported as what it is, once."""
+    for status, words in ((q.ECUDA, "tensor memory"), (q.ETIMEOUT, "bounded wait")):
+        q.selftest_q8(-1, status)
+        with pytest.raises(q.B200QError, match=words) as e:
+            q.device_status()
+        assert e.value.status == status
+        assert q.device_status() == q.OK
