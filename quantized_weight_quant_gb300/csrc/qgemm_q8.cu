@@ -826,24 +826,38 @@ GemmPlan plan(int O, int I, int S, int n_sms) {
     const long long tiles = r.tiles = m_tiles * r.n_tiles;
     if (tiles * nk > 0x7ffffff0ll) return r;
     r.items = (int)(tiles * nk);
-    // At least eight k-blocks per CTA: with fewer, a tile's planes cost more than
-    // the CTAs save (int4, 256 x 7168 over 32 rows: 22 us with four, 15.7 us with
-    // eight; 2048 x 1024 over 64: 11.6 and 9.4 us; with twelve 13.2 us).
-    long long grid = (r.items + 7ll) / 8;
-    if (grid > n_sms) grid = n_sms;
-    // Few tiles: the same number of CTAs for every tile, so that a CTA holds one
-    // part of one tile (512 rows of 6144 x 12288 with a residual: 44.8 us so,
-    // 48.8 us over all SMs; int2 5001 x 4097 over 77 rows: 16.6 and 20.8 us; the
-    // other way round where that leaves many SMs out: int8 8192 x 8192 over 32
-    // rows, 128 CTAs, 29.5 and 27.8 us).
-    if (tiles <= n_sms && tiles * (n_sms / tiles) <= grid) grid = tiles * (n_sms / tiles);
-    // Whole tiles per CTA where the last, uneven round costs less than cutting
-    // tiles does: a CTA's two cut tiles take it about as long as N / 6 items
-    // (6144 x 12288 over 1571 rows with a residual, N = 176, 288 items per CTA
-    // instead of 273: 113 us whole, 120 us cut; 12288 x 6144 over 300 rows,
-    // N = 160, 96 instead of 61: 42.2 us whole, 39.8 us cut).
-    const long long rounds = (tiles + grid - 1) / grid;
-    const bool even = tiles >= grid && rounds * nk - r.items / grid <= N / 6;
+    // Three ways to share the items out.  Counted is what the busiest CTA has to
+    // do, in items, and for the planes and the join 12 items with one shared tile
+    // and 17 + N / 16 with two (int8, whose items take longer, three quarters of
+    // that and 11).  Fitted to 714 calls timed in every form, 512 to 19456 outputs,
+    // 512 to 12288 columns, 16 to 512 rows: the form taken is 0.3 % slower than the
+    // fastest on average, 9 % at most.
+    const int one_shared = FMT == B200Q_I8 ? 11 : 12, two_shared = (17 + N / 16) * (FMT == B200Q_I8 ? 3 : 4) / 4;
+    // Whole tiles, with an uneven last round (6144 x 12288 over 1571 rows with a
+    // residual, 288 items instead of 273: 113 us, 120 us in even runs; int4 12288 x
+    // 256 over 176 rows, 96 CTAs: 11.7 us, 33.0 us in runs of eight items).
+    long long grid = tiles < n_sms ? tiles : n_sms;
+    long long least = (tiles + grid - 1) / grid * nk;
+    bool even = true;
+    // Few tiles: the same number of CTAs for every tile, each with one part of
+    // one tile, of eight items at least (int2 5001 x 4097 over 77 rows, three
+    // CTAs a tile: 16.9 us, 20.8 us in even runs over all SMs).
+    const long long k = n_sms / tiles;
+    if (k > 1 && nk / k >= 8 && (nk + k - 1) / k + one_shared < least) {
+        least = (nk + k - 1) / k + one_shared;
+        grid = tiles * k;
+        even = false;
+    }
+    // Even runs over all SMs, of eight items at least, with a shared tile at both
+    // ends (int4 10240 x 12288 over 16 rows, 51 items instead of 96: 26.5 us, 34.7
+    // us with 80 whole tiles; int8 8192 x 8192 over 32 rows, 27 items instead of
+    // 32: 27.8 us, 29.5 us with two CTAs a tile; the other way round the pair 5120
+    // x 6144 over 192 rows, 31.8 us, and 26.5 us whole).
+    const long long runs = r.items < 8ll * n_sms ? (r.items + 7ll) / 8 : n_sms;
+    if ((r.items + runs - 1) / runs + two_shared < least) {
+        grid = runs;
+        even = false;
+    }
     r.grid = (int)grid;
     r.grain = even ? nk : 1;
     r.cut = !even && (r.items % grid != 0 || (r.items / grid) % nk != 0);

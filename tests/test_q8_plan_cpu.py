@@ -68,3 +68,46 @@ def test_most_rows(q):
         assert p["part"] == 2 ** 16 and p["launches"] == -(-S // 2 ** 16), (S, p)
     p = q.selftest_q8_plan(1, 0, INT_MAX, 64, 9)
     assert p["tiles"] == -(-INT_MAX // 128)
+
+
+def _form(p):
+    """whole tiles, equal parts of a tile, or even runs"""
+    if not p["cut"]:
+        return "whole"
+    return "parts" if p["grid"] % p["tiles"] == 0 else "runs"
+
+
+# Calls whose forms were timed against one another: the fastest, us of all three
+# (None: that form is not to be had or is another one).
+TIMED = [
+    (2, 0, 10240, 12288, 16, "runs", 34.7, None, 26.5),
+    (2, 0, 10240, 12288, 96, "runs", 37.6, None, 29.9),
+    (2, 0, 10240, 12288, 192, "runs", 44.8, None, 37.3),
+    (2, 0, 5120, 12288, 300, "runs", 40.9, None, 33.0),
+    (1, 0, 12288, 8192, 16, "runs", 41.3, None, 34.2),
+    (1, 0, 5120, 8192, 300, "runs", 45.4, None, 37.0),
+    (1, 0, 8192, 8192, 32, "runs", None, 29.5, 27.8),
+    (1, 1, 5120, 6144, 16, "runs", 32.5, None, 26.0),
+    (1, 1, 5120, 6144, 48, "runs", 33.5, None, 27.0),
+    (2, 0, 11008, 4096, 32, "whole", 16.5, None, 19.1),
+    (2, 1, 4096, 2048, 16, "whole", 10.4, 12.9, None),
+    (2, 1, 4096, 2048, 144, "whole", 13.5, 16.6, None),
+    (2, 0, 6144, 12288, 1571, "whole", 113, None, 120),
+    (2, 0, 12288, 256, 176, "whole", 11.7, None, 33.0),
+    (2, 0, 512, 512, 300, "whole", 11.5, None, 17.5),
+    (2, 1, 5120, 6144, 192, "whole", 26.5, None, 31.8),
+    (2, 1, 5120, 6144, 96, "whole", 22.4, None, 25.4),
+    (1, 0, 5120, 8192, 192, "parts", 47.4, 31.6, 33.7),
+    (3, 0, 5001, 4097, 77, "parts", None, 16.9, 20.8),
+    (3, 0, 5001, 4097, 16, "parts", None, 13.7, 16.2),
+]
+
+
+@pytest.mark.parametrize("fmt,pair,O,I,S,form,whole,parts,runs", TIMED)
+def test_the_faster_form_is_taken(q, fmt, pair, O, I, S, form, whole, parts, runs):
+    times = {k: v for k, v in (("whole", whole), ("parts", parts), ("runs", runs)) if v}
+    assert min(times, key=times.get) == form
+    p = q.selftest_q8_plan(fmt, pair, O, I, S)
+    assert _form(p) == form, p
+    if form == "whole":
+        assert p["grid"] == min(p["tiles"], SMS), p                # no SM idle while tiles wait
