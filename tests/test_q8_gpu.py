@@ -748,3 +748,22 @@ def test_status_codes(q):
             q.device_status()
         assert e.value.status == status
         assert q.device_status() == q.OK
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("op", ["mm", "glu"])
+def test_runs_of_several_tiles(q, op, fmt, kind):
+    """Runs that begin and end inside a tile and hold whole tiles between: what large pairs and prompts take.  Seen from
+    the plan, so that the case stays one: blocks whose last tile is shared and the third of their run, and the fourth."""
+    import torch
+    O, I, S = (2560 if op == "glu" else 5120) + 20, 5121, 1408
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    p = q.selftest_q8_plan(FMTS[fmt], op == "glu", O, I, S, sms)
+    starts = [c * p["items"] // p["grid"] for c in range(p["grid"] + 1)]
+    last = {(b - 1) // p["nk"] - a // p["nk"] for a, b in zip(starts, starts[1:]) if a % p["nk"] and b % p["nk"]}
+    assert p["cut"] and p["grain"] == 1 and {2, 3} <= last, p
+    if op == "mm":
+        _mm(q, fmt, O, I, S, kind, "silu", bias=True, res=True, seed=21)
+    else:
+        _glu(q, fmt, O, I, S, kind, "gelu", bg=True, bu=True, seed=22)
