@@ -510,9 +510,16 @@ int b200q_rmsnorm_q8(const void *x, const void *r, void *h, int type, long long 
  *   y      DEVICE pointer, S rows of O values of `type` (stride ldy), written whole
  * y must not overlap x8, xs or bias.  Numerics: the codes are exact E4M3
  * values (int8 as 16 * high + low), so every product is exact; sums are f32;
- * the epilogue is f32 and rounds once to `type`.  f32 results are within
- * 1e-5 * scale * xs * sum |deq * x8| of the exact sum before the activation,
- * and the same call gives the same bits.
+ * the epilogue is f32 (scale * xs first, so that product should not leave f32)
+ * and rounds once to `type`.  f32 results are within E * scale * xs * sum |deq * x8|
+ * of the exact sum before the activation, E = 1e-5 + I * 2^-26 (int8:
+ * 1e-5 + I * 2^-25).  The second part is for rows whose products have one sign:
+ * the tensor cores drop what lies below the running sum's last bits, and of one
+ * sign that adds up.  (Found: at most 2.1 units in the last place per 32 columns,
+ * int8, whose codes are two operands, 3.5; the bound allows 4 and 8.  9.4e-5 and
+ * 2.5e-4 at 12288 and 32768 columns, int8 1.6e-4 and 4.3e-4.)  Where the signs
+ * mix, the sum is far below sum |deq * x8| and results stay within 1e-5 of it.
+ * The same call gives the same bits.
  * Up to 8 rows one launch streams the weights; more rows run on the fp8 tensor
  * cores, where a call whose output tiles are shared by several blocks takes a
  * stream-ordered workspace of the library's pool (at most 30 MB).

@@ -767,3 +767,50 @@ def test_runs_of_several_tiles(q, op, fmt, kind):
         _mm(q, fmt, O, I, S, kind, "silu", bias=True, res=True, seed=21)
     else:
         _glu(q, fmt, O, I, S, kind, "gelu", bg=True, bu=True, seed=22)
+
+
+def _one_sign(q, fmt, O, I, S, seed, sign, head, top):
+    """Codes of one sign, bytes of one sign below `top`, and `head` columns of the largest of both first."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    most = {"i8": (127, -128), "i4": (7, -8), "i2": (1, -2)}[fmt][sign < 0]
+    w = torch.randint(min(sign, most), max(sign, most) + 1, (O, I), generator=g, device="cuda", dtype=torch.int16)
+    c = torch.randint(1, top, (S, I), generator=g, device="cuda", dtype=torch.uint8)
+    w[:, :head], c[:, :head] = most, 0x7E
+    if fmt == "i8":
+        codes = w.to(torch.int8).view(torch.uint8)
+    else:
+        n, bits = 8 // BITS[fmt], BITS[fmt]
+        u = (w + 2 ** (bits - 1)).to(torch.uint8).view(O, I // n, n)
+        codes = sum(u[:, :, k] << (bits * k) for k in range(n)).to(torch.uint8)
+    xq = q.Q8Rows(S, I)
+    xq.codes[:, :I] = c
+    xq.scales.fill_(1.0)
+    return q.tensor_upload(FMTS[fmt], O, I, codes.cpu().numpy(), np.ones(O, np.float32)), w, xq
+
+
+@pytest.mark.parametrize("S", [2, 1408])
+@pytest.mark.parametrize("I", [12288, 32768])
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_long_rows_of_one_sign(q, fmt, I, S):
+    """The error bound where the running sum is as large as the sum of the magnitudes all along: what each step of the
+    tensor cores drops adds up.  Tolerance, per sum |deq x8|: 1e-5, and 4 units in the last place of f32 (2^-23 each) per
+    32 columns, twice for int8, whose codes are two operands."""
+    import torch
+    O = 2432
+    tol = 1e-5 + I * 2.0 ** -26 * (2 if fmt == "i8" else 1)
+    if S > 8:
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        p = q.selftest_q8_plan(FMTS[fmt], False, O, I, S, sms)
+        assert sms != 152 or not p["cut"], p                           # one accumulator holds a whole row's sum
+    y = torch.empty(S, O, device="cuda")
+    pick = [s for s in (0, 1, S // 2, S - 1)]
+    for sign, head, top in ((1, 0, 0x7F), (-1, 0, 0x7F), (1, 512, 0x28), (-1, 64, 0x28), (1, 64, 0x40)):
+        t, w, xq = _one_sign(q, fmt, O, I, S, 7, sign, head, top)
+        with t:
+            q.matmul_q8(t, xq, y, S)
+            torch.cuda.synchronize()
+        want = xq.values()[pick].double() @ w.double().t()             # |want| = sum |deq x8|: one sign
+        off = float(((y[pick].double() - want).abs() / want.abs()).max())
+        assert off <= tol, (sign, head, top, off, tol)
