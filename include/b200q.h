@@ -480,7 +480,11 @@ int b200q_quantize_q8(const void *x, int type, long long ldx, void *y8, long lon
  *     h = x + r (r NULL: h = x),  y = h * w / sqrt(mean_d h^2 + eps)
  *     ys[s] = max(max_d |y| / 448, 2^-126),  y8 = e4m3(y / ys[s])
  * Everything is f32 from the first addition on: y and its scale come from the
- * f32 sum, h is rounded to `type` only where it is stored.
+ * f32 sum, h is rounded to `type` only where it is stored.  y / ys is taken as
+ * 448 h w / max_d |h w|, from which the row's root cancels, before ys is rounded
+ * (a scale of 2^-126: y / 2^-126); a value within f32 rounding of the middle
+ * between two codes may get either.  eps = 0: a row of zeros, or one whose
+ * squares vanish in f32, gets a scale that is not finite.
  *   x, r   DEVICE pointers to rows of D values of `type` (strides ldx, ldr)
  *   h      DEVICE pointer receiving h (stride ldh), or NULL; it may be x or r
  *          itself with the same stride, but must not partially overlap them

@@ -814,3 +814,38 @@ def test_long_rows_of_one_sign(q, fmt, I, S):
         want = xq.values()[pick].double() @ w.double().t()             # |want| = sum |deq x8|: one sign
         off = float(((y[pick].double() - want).abs() / want.abs()).max())
         assert off <= tol, (sign, head, top, off, tol)
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S,D", [(1, 6144), (700, 5003), (3, 20000), (2000, 96)])
+def test_rows_same_bits_each_time(q, S, D, kind):
+    """Sums and maxima in a fixed order: rows, scales and h repeat bit for bit."""
+    import torch
+    x, r, w = _dev(_rows(S, D, 1), kind), _dev(synth.normal_f32((S, D), 1, 2), kind), _dev(synth.uniform_f32((D,), 0.5, 1.5, 1, 3))
+    first = None
+    for _ in range(5):
+        a, b, h = _fresh(q, S, D), _fresh(q, S, D), torch.empty_like(x)
+        q.rmsnorm_q8(x, w, a, S, D, 1e-6, r=r, h=h)
+        q.quantize_q8(x, b, S, D)
+        got = a.codes, a.scales, b.codes, b.scales, h
+        first = first or got
+        assert all(torch.equal(u, v) for u, v in zip(first, got))
+
+
+def test_norm_codes_are_the_nearest(q):
+    """Codes of 448 h w / max |h w| in 64 bits.  f32 has three roundings there (h w, the factor, their product, 2^-24 each):
+    a code may differ only where the exact quotient is that close to the middle between two codes."""
+    import torch
+    S, D = 900, 6144
+    x, w = _dev(_rows(S, D, 8), "bf16"), _dev(synth.uniform_f32((D,), 0.5, 1.5, 8, 3))
+    out = _fresh(q, S, D)
+    q.rmsnorm_q8(x, w, out, S, D, 1e-6)
+    torch.cuda.synchronize()
+    hw = _np64(x) * _np64(w)
+    t = hw * (448 / np.abs(hw).max(1, keepdims=True))
+    v, _ = _quantised(q, out, D)
+    off = v != _e4m3_round(t)
+    _, e = np.frexp(np.abs(t))
+    half = 2.0 ** (np.maximum(e - 1, -6) - 4.0)
+    assert np.all(np.abs(v - t)[off] <= half[off] + 3 * 2.0 ** -24 * np.abs(t)[off])
+    assert off.sum() <= S * D * 1e-5
