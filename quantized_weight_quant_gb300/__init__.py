@@ -358,7 +358,9 @@ class Q8Rows:
 
     def values(self):
         """The codes as E4M3 numbers, float8_e4m3fn [S, D] (a view)."""
-        self._look()
+        c = self._codes
+        if c.data_ptr() != self._cp or c.shape != self._cshape or c.stride() != self._cstride:
+            self.codes = c
         return self._values
 
 
