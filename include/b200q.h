@@ -526,7 +526,8 @@ int b200q_rmsnorm_q8(const void *x, const void *r, void *h, int type, long long 
  * The same call gives the same bits.
  * Up to 8 rows one launch streams the weights; more rows run on the fp8 tensor
  * cores, where a call whose output tiles are shared by several blocks takes a
- * stream-ordered workspace of the library's pool (at most 30 MB).
+ * stream-ordered workspace of the library's pool (at most 30 MB for the blocks'
+ * sums, and 8 bytes per output tile).
  * S = 0 is a no-op.  Asynchronous on `stream`.
  */
 int b200q_matmul_q8(const b200q_tensor *t, const void *x8, long long ld8, const float *xs, const float *bias, int act,

@@ -10,14 +10,15 @@
 //
 // Bound: the tensor cores for many rows, the weights' bytes for few; now the
 // hand-over between the roles, ~0.4 us per item at N = 176, and the integer work
-// of the dequantizers: int4 12288 x 6144 over 1571 rows 110 us, 2150 TFLOP/s;
-// the pair 207 us, 2290 TFLOP/s; 6144 x 12288 with a residual 113 us; int2
-// 5001 x 4097 over 77 rows 16.6 us.
+// of the dequantizers.  In a graph: int4 12288 x 6144 over 1571 rows 110 us, 2150
+// TFLOP/s; the pair 207 us, 2290 TFLOP/s (call by call, with one set of weights,
+// 221 us); 6144 x 12288 with a residual 112 us (115 us), int8 187 us; int2 5001 x
+// 4097 over 77 rows 16.9 us (18.4 us).
 //
 // Work is cut into (output tile, 128-column k-block) items, tile-major, and
-// every CTA takes one contiguous run of them (one CTA per SM): whole tiles
-// where that is nearly even, otherwise runs that cut tiles, so that the last
-// wave is as full as the others.  A tile that one CTA holds whole goes
+// every CTA takes one contiguous run of them (one CTA per SM at most): whole
+// tiles, an equal part of one tile, or even runs that begin and end inside
+// tiles, whichever is done first (plan()).  A tile that one CTA holds whole goes
 // straight to y; a cut one is written as f32 planes (one per CTA), and the CTA
 // whose arrival completes the tile adds the planes in CTA order and runs the
 // epilogue, with all its dequantizing and epilogue warps, when its run is done.

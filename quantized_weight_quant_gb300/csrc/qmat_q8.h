@@ -33,6 +33,10 @@ int gemm_q8_parts(int S, int part);     // launches
 // v, activated.  f32 expf / erff; for large |v| the exponentials
 // overflow or vanish to the activation's limits.  __fdividef (2 ulp) gives 0
 // where silu's denominator passes 2^126, v < -87, where silu is below 1e-36.
+// Against 64 bits silu is 2.2e-7 off at most for v > -80 (with / instead 2.1e-7),
+// gelu_tanh 1.3e-6 for v > -4.  Not /, whose slow path the epilogue would carry:
+// the pair 12288 x 6144 over 1571 rows 215 us instead of 207, a gelu_tanh product
+// of that size 157 instead of 120.
 template <int ACT>
 __device__ __forceinline__ float act_q8(float v) {
     if constexpr (ACT == B200Q_ACT_RELU) return v < 0.f ? 0.f : v;      // keeps a NaN
