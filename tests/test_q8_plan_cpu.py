@@ -111,3 +111,26 @@ def test_the_faster_form_is_taken(q, fmt, pair, O, I, S, form, whole, parts, run
     assert _form(p) == form, p
     if form == "whole":
         assert p["grid"] == min(p["tiles"], SMS), p                # no SM idle while tiles wait
+
+
+def test_shared_tiles_and_their_planes(q):
+    """What the kernel derives from a plan by itself: which block owns an item, which blocks share a tile, and in which of
+    its two planes a block holds its part."""
+    cut = 0
+    for fmt, pair, O, I, S in _draws(3000, 2):
+        p = q.selftest_q8_plan(fmt, pair, O, I, S)
+        if not p["cut"]:
+            continue
+        cut += 1
+        n, nk, what = p["items"], p["nk"], (fmt, pair, O, I, S, p)
+        starts = [c * n // p["grid"] for c in range(p["grid"] + 1)]
+        owner = lambda i: ((i + 1) * p["grid"] - 1) // n
+        for c in range(p["grid"]):
+            assert owner(starts[c]) == c == owner(starts[c + 1] - 1), what
+            for tile in range(starts[c] // nk + 1, (starts[c + 1] - 1) // nk):
+                assert owner(tile * nk) == owner(tile * nk + nk - 1) == c, what      # between its ends a block has whole tiles
+        for tile in {s // nk for s in starts[1:-1] if s % nk}:
+            first, last = owner(tile * nk), owner(tile * nk + nk - 1)
+            assert 0 <= first < last < p["grid"] and last - first + 1 < 1024, what
+            assert all(starts[c] // nk == tile for c in range(first + 1, last + 1)), what   # first plane, but for the first block
+    assert cut > 500
