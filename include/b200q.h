@@ -7,7 +7,8 @@
  *
  * against S activation rows, plus the calls built on it: the gate/up pair,
  * grouped expert calls, RMSNorm glue, MLA decode attention with weight
- * absorption over paged caches, and the calls on 8-bit activations.
+ * absorption over paged caches, the calls on 8-bit activations, and the calls of
+ * a mixture-of-experts block whose routing stays on the device.
  * Sources for the operation: the page "CUDA 后端"
  * (colibri-analysis 09), section 1, "设备侧库 backend_cuda.cu" (the resident
  * tensor, `weight_at`, `quant_matmul` and the five extern "C" functions of the
@@ -354,7 +355,8 @@ int b200q_tensor_info(const b200q_tensor *t, int *fmt, int *O, int *I, int *devi
  * library gave up on a bounded device-side wait since the last call
  * (B200Q_ETIMEOUT; such a kernel leaves its outputs incomplete), met a NULL or
  * unaligned KV-cache page (B200Q_EINVAL, b200q_mla_absorb and
- * b200q_kv_append; the call's outputs are then undefined), or a CUDA error
+ * b200q_kv_append; the call's outputs are then undefined), met an expert
+ * number outside the layer (B200Q_EINVAL, b200q_moe_experts), or a CUDA error
  * (B200Q_ECUDA).  Clears the record.  B200Q_OK otherwise.
  */
 int b200q_device_status(void);
@@ -565,6 +567,123 @@ int b200q_selftest_q8_plan(int fmt, int pair, int O, int I, int S, int n_sms, lo
  * status is B200Q_ETIMEOUT.  Synchronizes the device.
  */
 int b200q_selftest_q8(long long wait_ns, int status);
+
+/*
+ * ---- A mixture-of-experts block on the device ----
+ *
+ * The decode step of a layer of routed experts without the host in between:
+ * the router's scores become expert numbers and weights in device memory, the
+ * experts' products read them there, and one call carries the residual stream
+ * from one block to the next.  Every call is asynchronous on `stream` and can be
+ * captured in a CUDA graph; the routing of a replay is what its logits give then.
+ * The pages run one expert at a time, chosen on the host; the formulas here are
+ * the library's own.
+ */
+
+/* Score functions of b200q_moe_route: exp(l) / sum exp(l), 1 / (1 + e^-l). */
+enum { B200Q_SCORE_SOFTMAX = 0, B200Q_SCORE_SIGMOID = 1 };
+
+/*
+ * The k experts of each token and their weights, from the router's logits:
+ *     s[e] = score(l[e]),  c[e] = s[e] + bias[e]  (bias NULL: c has the logits' order)
+ *     n_group > 1: the experts are n_group groups of E / n_group neighbours; a
+ *         group's value is the sum of its group_top largest c (group_top = 1: the
+ *         largest); the topk_group groups of the largest values stay
+ *     ids[j] = the experts of the k largest c that stay, descending
+ *     w[j]   = s[ids[j]], divided by the sum of the row's s[ids] if norm, times scale
+ * Equal values go to the lowest index, of groups and of experts.  The order is
+ * that of the formula in 64 bits: where f32 values are too near each other to
+ * tell, the row is decided again in 64 bits.
+ *   logits  DEVICE pointer, S rows of E values of `type` (B200Q_T_*), ld >= E
+ *           values apart, aligned to the type
+ *   bias    DEVICE pointer to E floats, or NULL; it takes part in the choice
+ *           only, not in the weights
+ *   E       1 .. 1024;  k  1 .. min(E, 32)
+ *   n_group 1 .. 32, divides E; 1 <= topk_group <= n_group; group_top 1 or 2, at
+ *           most E / n_group
+ *   ids     DEVICE pointer to [S, k] int, wts to [S, k] floats
+ * An expert whose logit (or bias) is -infinity is masked: it is never chosen and
+ * does not count in its group's value; where fewer than k are left the last ids
+ * are -1, with weight 0.  A NaN among a row's logits, or in the bias, makes the
+ * row's weights NaN (such an expert is not chosen), and so does a logit of
+ * +infinity under the softmax (its score counts as 0 beside a bias).  ids and wts must not overlap
+ * each other, the logits or the bias.  Weights are f32, within 2e-6 of the
+ * formula's, relative.  S = 0 is a no-op.  One launch, no workspace.
+ */
+int b200q_moe_route(const void *logits, int type, long long ld, const float *bias, int S, int E, int k, int score,
+                    int n_group, int topk_group, int group_top, int norm, float scale, int *ids, float *wts,
+                    void *stream);
+
+typedef struct b200q_experts b200q_experts;   /* opaque: the resident experts of one layer */
+
+/*
+ * The experts of a layer, from E triples of resident tensors: gate[e] and up[e]
+ * [F, D], down[e] [D, F], all of one quantized format (int8, int4, int2) with
+ * per-row scales, on the current device; 1 <= E <= 1024.  gate, up and down are
+ * HOST arrays of E handles, read during the call only; the same tensor may stand
+ * in several places.  The handle holds a device table of the tensors' addresses,
+ * not the tensors: they have to outlive it and its last call.  A shared expert
+ * is one more entry, whose number every token has among its ids.  Copies
+ * synchronously.  Returns NULL (and sets the last error) on a bad argument or when
+ * memory runs out.
+ */
+b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q_tensor *const *up,
+                                    const b200q_tensor *const *down, int E);
+
+/* Frees the table (NULL is a no-op).  No queued kernel may still read it. */
+void b200q_experts_free(b200q_experts *ex);
+
+/*
+ * The experts' layer for a few tokens:
+ *     y[s] = res[s] + sum_j wts[s,j] * down_e . (act(gate_e . x[s]) * (up_e . x[s])),   e = ids[s,j]
+ *   x       DEVICE pointer, S rows of D values of `type` (stride ldx), aligned to
+ *           the type
+ *   ids     DEVICE pointer to [S, k] int: expert numbers, or -1 for a slot that is
+ *           empty (its weight is not read into any sum).  An expert may stand
+ *           in a row twice; both count.  Any other number leaves its slot empty
+ *           and is reported by b200q_device_status (B200Q_EINVAL)
+ *   wts     DEVICE pointer to [S, k] floats
+ *   k       1 .. 32
+ *   act     B200Q_ACT_*
+ *   res     DEVICE pointer, S rows of D values of `type` (stride ldr), or NULL; it
+ *           may be y itself with the same stride, but must not partially overlap it
+ *   y       DEVICE pointer, S rows of D values of `type` (stride ldy), written
+ *           whole; a row whose slots are all empty is res, or 0
+ * y must not overlap x, ids or wts; ids and wts may be what b200q_moe_route has
+ * just written on the stream.  Rows do not depend on each other, and the same
+ * call gives the same bits.
+ */
+int b200q_moe_experts(const b200q_experts *ex, const void *x, int type, long long ldx, const int *ids,
+                      const float *wts, int k, int act, const void *res, long long ldr, void *y, long long ldy, int S,
+                      void *stream);
+
+/*
+ * From one block to the next: the norm after a block, its gate, the scaled
+ * residual, and the norm before the next block, in one pass over the rows:
+ *     p  = m * w_post / sqrt(mean_d m^2 + eps)      (w_post NULL: p = m)
+ *     h' = res_scale * h + out_scale * gate * p     (h NULL: 0; gate NULL: 1)
+ *     y  = h' * w / sqrt(mean_d h'^2 + eps)
+ *   m, h    DEVICE pointers to S rows of D values of `type` (strides ldm, ldh)
+ *   gate    DEVICE pointer of `type`, or NULL.  gate_cols = D: S rows of D
+ *           values, ldg apart (ldg 0: one row for all); gate_cols = 1: one value
+ *           per row, ldg apart (0: one for all)
+ *   h_out   DEVICE pointer receiving h' (stride ldo), or NULL; it may be h or m
+ *           itself with the same stride, but must not partially overlap them
+ *   w_post, w   DEVICE pointers to D floats
+ *   y       DEVICE pointer, S rows of D values of `ytype` (stride ldy), or NULL (w
+ *           is then not read).  At least one of h_out and y is given
+ *   eps     >= 0 and finite; the scales are finite
+ * Rows are aligned to their type.  y must not overlap any other operand, h_out
+ * must not overlap gate, w_post or w.  Everything is f32 between the reads and
+ * the writes: y comes from the f32 h', which is rounded to `type` only where it is
+ * stored.  Within 1e-5 of the formula, |h'| taken as res_scale |h| + |out_scale
+ * gate p|.  A NaN or an infinity in a row makes that row's y not finite or
+ * NaN.  S = 0 is a no-op.  One launch, no workspace.
+ */
+int b200q_block_norm(const void *m, int type, long long ldm, const void *h, long long ldh, const void *gate,
+                     long long ldg, int gate_cols, const float *w_post, float res_scale, float out_scale, void *h_out,
+                     long long ldo, const float *w, void *y, int ytype, long long ldy, int S, int D, float eps,
+                     void *stream);
 
 /*
  * Self test of the bounded waits: one kernel waits, at most wait_us

@@ -22,6 +22,8 @@ GROUP_MAX = 16
 T_F32, T_F16, T_BF16 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 FORMATS = {"f32": F32, "i8": I8, "i4": I4, "i2": I2}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +80,16 @@ def _load():
     L.b200q_matmul_q8.restype = ci
     L.b200q_glu_q8.argtypes = [vp, vp, vp, cll, vp, vp, vp, ci, vp, ci, cll, ci, vp]
     L.b200q_glu_q8.restype = ci
+    L.b200q_moe_route.argtypes = [vp, ci, cll, vp, ci, ci, ci, ci, ci, ci, ci, ci, cf, vp, vp, vp]
+    L.b200q_moe_route.restype = ci
+    L.b200q_experts_create.argtypes = [vp, vp, vp, ci]
+    L.b200q_experts_create.restype = vp
+    L.b200q_experts_free.argtypes = [vp]
+    L.b200q_experts_free.restype = None
+    L.b200q_moe_experts.argtypes = [vp, vp, ci, cll, vp, vp, ci, ci, vp, cll, vp, cll, ci, vp]
+    L.b200q_moe_experts.restype = ci
+    L.b200q_block_norm.argtypes = [vp, ci, cll, vp, cll, vp, cll, ci, vp, cf, cf, vp, cll, vp, vp, ci, cll, ci, ci, cf, vp]
+    L.b200q_block_norm.restype = ci
     L.b200q_selftest_q8_plan.argtypes = [ci, ci, ci, ci, ci, ci, vp]
     L.b200q_selftest_q8_plan.restype = ci
     L.b200q_selftest_q8.argtypes = [cll, ci]
@@ -482,6 +494,114 @@ def selftest_timeout(wait_us: int, stream=None) -> None:
     """A kernel waits wait_us on an mbarrier nothing completes and records a
     timeout (b200q_selftest_timeout); device_status() then reports it."""
     _check(lib.b200q_selftest_timeout(wait_us, _stream(stream)))
+
+
+_INT32 = None
+
+
+def _slots(ids, wts, S: int, k: int):
+    """(ids, wts) pointers of contiguous int32 and float32 [S or more, k] CUDA tensors."""
+    global _INT32
+    if _INT32 is None:
+        import torch
+        _INT32 = (torch.Tensor, torch.int32, torch.float32)
+    for a, t, name in ((ids, _INT32[1], "ids"), (wts, _INT32[2], "wts")):
+        if not isinstance(a, _INT32[0]):
+            raise TypeError("%s: expected a torch CUDA tensor" % name)
+        if not a.is_cuda:
+            raise ValueError("%s: expected a CUDA tensor, got a %s tensor" % (name, a.device))
+        shape = a.shape
+        if a.dtype != t or len(shape) != 2 or shape[0] < S or shape[1] != k or not a.is_contiguous():
+            raise ValueError("%s: expected contiguous %s [%d, %d]" % (name, t, S, k))
+    return ids.data_ptr(), wts.data_ptr()
+
+
+def moe_route(logits, ids, wts, S: int, E: int, k: int, score: int = SCORE_SOFTMAX, bias=None, n_group: int = 1,
+              topk_group: int = 1, group_top: int = 1, norm: bool = True, scale: float = 1.0, stream=None) -> None:
+    """The k experts of each token and their weights from the router's logits
+    [S, E] (b200q_moe_route): ids int32 [S, k], wts float32 [S, k]."""
+    lp, t, ld = _wide(logits, S, E, "logits")
+    ip, wp = _slots(ids, wts, S, k)
+    _check(lib.b200q_moe_route(lp, t, ld, _vec(bias, E, "bias"), S, E, k, score, n_group, topk_group, group_top,
+                               int(norm), scale, ip, wp, _raw_stream(stream)))
+
+
+def experts_create(gate, up, down) -> int:
+    """A handle on the experts of a layer (b200q_experts_create) from equal-length
+    sequences of tensors, which have to outlive it; free it with experts_free."""
+    if not (len(gate) == len(up) == len(down)):
+        raise ValueError("gate, up and down must have the same length")
+    h = lib.b200q_experts_create(*(_ptr_array(a, _h) for a in (gate, up, down)), len(gate))
+    if not h:
+        msg = last_error()
+        raise B200QError(ENOMEM if "memory" in msg else EINVAL, msg)
+    return h
+
+
+def experts_free(ex) -> None:
+    if isinstance(ex, Experts):
+        ex.free()
+    else:
+        lib.b200q_experts_free(ex)
+
+
+class Experts:
+    """The resident experts of one layer: gate, up [F, D] and down [D, F] are
+    sequences of QTensors, kept alive here (but not freed with it)."""
+
+    def __init__(self, gate, up, down):
+        self.handle = None
+        self.tensors = (list(gate), list(up), list(down))
+        self.handle = experts_create(*self.tensors)
+        self.E, self.F, self.D = len(self.tensors[0]), self.tensors[0][0].O, self.tensors[0][0].I
+
+    def free(self):
+        if self.handle:
+            lib.b200q_experts_free(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.free()
+        return False
+
+
+def moe_experts(ex, x, ids, wts, y, S: int, k: int, act: int = ACT_SILU, res=None, stream=None) -> None:
+    """y[s] = res[s] + sum_j wts[s,j] * down_e . (act(gate_e . x[s]) * (up_e . x[s])),
+    e = ids[s,j], -1 an empty slot (b200q_moe_experts).  ex: an Experts; x, y and
+    res: [S, D] float32 / float16 / bfloat16, any row stride."""
+    if not isinstance(ex, Experts):
+        raise TypeError("expected an Experts")
+    xp, t, ldx = _wide(x, S, ex.D, "x")
+    yp, _, ldy = _wide(y, S, ex.D, "y", t)
+    rp, _, ldr = _wide(res, S, ex.D, "res", t) if res is not None else (0, t, 0)
+    ip, wp = _slots(ids, wts, S, k)
+    _check(lib.b200q_moe_experts(ex.handle, xp, t, ldx, ip, wp, k, act, rp, ldr, yp, ldy, S, _raw_stream(stream)))
+
+
+def block_norm(m, S: int, D: int, eps: float, h=None, h_out=None, w_post=None, gate=None, res_scale: float = 1.0,
+               out_scale: float = 1.0, w=None, y=None, stream=None) -> None:
+    """p = m * w_post / rms(m), h_out = res_scale * h + out_scale * gate * p,
+    y = h_out * w / rms(h_out) (b200q_block_norm).  m, h, h_out: [S, D] of one
+    type; gate of that type: [S, D], [1, D] or [D] (one row for all), or [S, 1];
+    y: [S, D] of any type."""
+    mp, t, ldm = _wide(m, S, D, "m")
+    hp, _, ldh = _wide(h, S, D, "h", t) if h is not None else (0, t, 0)
+    op, _, ldo = _wide(h_out, S, D, "h_out", t) if h_out is not None else (0, t, 0)
+    yp, ty, ldy = _wide(y, S, D, "y") if y is not None else (0, t, 0)
+    gp, ldg, gc = 0, 0, D
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate[None]
+        gc = gate.shape[1] if gate.dim() == 2 and gate.shape[1] == 1 else D
+        rows = 1 if gate.shape[0] == 1 else S
+        gp, _, ldg = _wide(gate, rows, gc, "gate", t)
+        if rows == 1:
+            ldg = 0
+    _check(lib.b200q_block_norm(mp, t, ldm, hp, ldh, gp, ldg, gc, _vec(w_post, D, "w_post"), res_scale, out_scale, op,
+                                ldo, _vec(w, D, "w"), yp, ty, ldy, S, D, eps, _raw_stream(stream)))
 
 
 KV_PAGE_TOKENS = 64

@@ -243,18 +243,20 @@ long long b200q_workspace_allocations(void) { return g_ws_allocs.load(std::memor
 int b200q_device_status(void) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "b200q_device_status");
-    unsigned int a = 0, b = 0, m = 0, c = 0, d = 0;
+    unsigned int a = 0, b = 0, m = 0, c = 0, d = 0, x = 0;
     e = decode_take_error(&a);
     if (e == cudaSuccess) e = prefill_take_error(&b);
     if (e == cudaSuccess) e = mla_take_error(&m);
     if (e == cudaSuccess) e = tcs_take_error(&c);
     if (e == cudaSuccess) e = q8_take_error(&d);
+    if (e == cudaSuccess) e = moe_take_error(&x);
     if (e != cudaSuccess) return cuda_fail(e, "b200q_device_status");
     if (d == (unsigned)(-B200Q_ECUDA))
         return fail(B200Q_ECUDA, "b200q_device_status: an 8-bit product found its tensor memory at another base than 0");
     if (a || b || c || d || m == (unsigned)(-B200Q_ETIMEOUT))
         return fail(B200Q_ETIMEOUT, "b200q_device_status: a kernel gave up on a bounded wait");
     if (m) return fail(B200Q_EINVAL, "b200q_device_status: an MLA call met a NULL or unaligned cache page");
+    if (x) return fail(B200Q_EINVAL, "b200q_device_status: an experts' call met an expert number outside the layer");
     return B200Q_OK;
 }
 
@@ -909,6 +911,199 @@ int b200q_glu_q8(const b200q_tensor *tg, const b200q_tensor *tu, const void *x8,
     return run_mat_q8(MatQ8{reinterpret_cast<const Tensor *>(tg), reinterpret_cast<const Tensor *>(tu),
                             (const uint8_t *)x8, ld8, xs, bias_g, bias_u, act, nullptr, 0, y, type, ldy, S},
                       stream, who);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool finite(float v) { return v >= -3.4028234e38f && v <= 3.4028234e38f; }
+
+// ids and wts of S tokens: 4-byte aligned, [S, k].
+int check_slots(const void *ids, const void *wts, const char *who) {
+    if (!ids || !wts) return fail(B200Q_EINVAL, "%s: ids and wts must not be NULL", who);
+    if ((uintptr_t)ids % 4 || (uintptr_t)wts % 4) return fail(B200Q_EINVAL, "%s: ids and wts must be 4-byte aligned", who);
+    return B200Q_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int b200q_moe_route(const void *logits, int type, long long ld, const float *bias, int S, int E, int k, int score,
+                    int n_group, int topk_group, int group_top, int norm, float scale, int *ids, float *wts,
+                    void *stream) {
+    const char *who = "b200q_moe_route";
+    if (S < 0) return fail(B200Q_EINVAL, "%s: S must be >= 0 (got %d)", who, S);
+    if (!type_bytes(type)) return fail(B200Q_EINVAL, "%s: unknown element type %d", who, type);
+    if (E < 1 || E > kRouteMaxE) return fail(B200Q_EINVAL, "%s: E must be in [1, %d] (got %d)", who, kRouteMaxE, E);
+    if (k < 1 || k > kRouteMaxK || k > E)
+        return fail(B200Q_EINVAL, "%s: k must be in [1, min(E, %d)] (got %d)", who, kRouteMaxK, k);
+    if (score != B200Q_SCORE_SOFTMAX && score != B200Q_SCORE_SIGMOID)
+        return fail(B200Q_EINVAL, "%s: unknown score %d", who, score);
+    if (n_group < 1 || n_group > kRouteMaxGroups || E % n_group)
+        return fail(B200Q_EINVAL, "%s: n_group must be in [1, %d] and divide E (got %d)", who, kRouteMaxGroups, n_group);
+    if (topk_group < 1 || topk_group > n_group)
+        return fail(B200Q_EINVAL, "%s: topk_group must be in [1, n_group] (got %d)", who, topk_group);
+    if (group_top < 1 || group_top > 2 || group_top > E / n_group)
+        return fail(B200Q_EINVAL, "%s: group_top must be 1 or 2 and at most E / n_group (got %d)", who, group_top);
+    if (!finite(scale)) return fail(B200Q_EINVAL, "%s: scale must be finite", who);
+    if (S == 0) return B200Q_OK;
+    int rc = check_rows(logits, E, ld, type, S, "logits", who);
+    if (!rc) rc = check_slots(ids, wts, who);
+    if (rc) return rc;
+    if ((uintptr_t)bias % 4) return fail(B200Q_EINVAL, "%s: the bias must be 4-byte aligned", who);
+    const Rows l = rows_of(logits, E, ld, type_bytes(type));
+    const size_t n = (size_t)S * k * 4, eb = (size_t)E * 4;
+    if (overlaps_vec(l, S, ids, n) || overlaps_vec(l, S, wts, n) || overlap(ids, n, wts, n) ||
+        (bias && (overlap(ids, n, bias, eb) || overlap(wts, n, bias, eb))))
+        return fail(B200Q_EINVAL, "%s: ids and wts must not overlap each other, the logits or the bias", who);
+    cudaError_t e = launch_moe_route(Route{logits, type, ld, bias, S, E, k, score, n_group, topk_group, group_top,
+                                           norm != 0, scale, ids, wts},
+                                     (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return B200Q_OK;
+}
+
+b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q_tensor *const *up,
+                                    const b200q_tensor *const *down, int E) {
+    const char *who = "b200q_experts_create";
+    g_err.clear();
+    if (E < 1 || E > kMoeMaxExperts) {
+        fail(B200Q_EINVAL, "%s: E must be in [1, %d] (got %d)", who, kMoeMaxExperts, E);
+        return nullptr;
+    }
+    if (!gate || !up || !down) {
+        fail(B200Q_EINVAL, "%s: NULL host array", who);
+        return nullptr;
+    }
+    const b200q_tensor *const *all[3] = {gate, up, down};
+    Expert *host = new (std::nothrow) Expert[E];
+    Experts *ex = new (std::nothrow) Experts();
+    int rc = host && ex ? B200Q_OK : fail(B200Q_ENOMEM, "%s: out of host memory", who);
+    for (int e = 0; e < E && rc == B200Q_OK; ++e)
+        for (int m = 0; m < 3 && rc == B200Q_OK; ++m) {
+            rc = check_q8_tensor(all[m][e], who);
+            if (rc) break;
+            const Tensor &t = *reinterpret_cast<const Tensor *>(all[m][e]);
+            if (e == 0 && m == 0) {
+                ex->E = E, ex->fmt = t.fmt, ex->device = t.device, ex->F = t.O, ex->D = t.I, ex->ld_in = t.ld;
+            }
+            if (e == 0 && m == 2) ex->ld_out = t.ld;
+            if (t.fmt != ex->fmt || t.O != (m == 2 ? ex->D : ex->F) || t.I != (m == 2 ? ex->F : ex->D))
+                rc = fail(B200Q_EINVAL, "%s: %s %d is not [%d, %d] in the first tensor's format", who,
+                          m == 0 ? "gate" : m == 1 ? "up" : "down", e, m == 2 ? ex->D : ex->F, m == 2 ? ex->F : ex->D);
+            host[e].codes[m] = t.codes;
+            host[e].scales[m] = t.scales;
+        }
+    if (rc == B200Q_OK) {
+        cudaStream_t st = nullptr;
+        cudaError_t c = cudaMalloc((void **)&ex->table, (size_t)E * sizeof(Expert));
+        if (c == cudaSuccess) c = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+        if (c == cudaSuccess) c = cudaMemcpyAsync(ex->table, host, (size_t)E * sizeof(Expert), cudaMemcpyHostToDevice, st);
+        if (c == cudaSuccess) c = cudaStreamSynchronize(st);
+        if (st) cudaStreamDestroy(st);
+        if (c != cudaSuccess) {
+            rc = cuda_fail(c, who);
+            cudaGetLastError();
+            cudaFree(ex->table);
+        }
+    }
+    delete[] host;
+    if (rc != B200Q_OK) {
+        delete ex;
+        return nullptr;
+    }
+    return reinterpret_cast<b200q_experts *>(ex);
+}
+
+void b200q_experts_free(b200q_experts *h) {
+    if (!h) return;
+    Experts *ex = reinterpret_cast<Experts *>(h);
+    int cur = -1;
+    cudaGetDevice(&cur);
+    if (cur != ex->device) cudaSetDevice(ex->device);
+    cudaFree(ex->table);
+    if (cur != ex->device && cur >= 0) cudaSetDevice(cur);
+    delete ex;
+}
+
+int b200q_moe_experts(const b200q_experts *h, const void *x, int type, long long ldx, const int *ids,
+                      const float *wts, int k, int act, const void *res, long long ldr, void *y, long long ldy, int S,
+                      void *stream) {
+    const char *who = "b200q_moe_experts";
+    if (!h) return fail(B200Q_EINVAL, "%s: the experts' handle is NULL", who);
+    const Experts &ex = *reinterpret_cast<const Experts *>(h);
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    if (dev != ex.device)
+        return fail(B200Q_EINVAL, "%s: the experts live on device %d but device %d is current", who, ex.device, dev);
+    if (S < 0) return fail(B200Q_EINVAL, "%s: S must be >= 0 (got %d)", who, S);
+    if (!type_bytes(type)) return fail(B200Q_EINVAL, "%s: unknown element type %d", who, type);
+    if (k < 1 || k > kMoeMaxK) return fail(B200Q_EINVAL, "%s: k must be in [1, %d] (got %d)", who, kMoeMaxK, k);
+    if (act < B200Q_ACT_NONE || act > B200Q_ACT_SILU) return fail(B200Q_EINVAL, "%s: unknown activation %d", who, act);
+    if (S == 0) return B200Q_OK;
+    int rc = check_rows(x, ex.D, ldx, type, S, "x", who);
+    if (!rc) rc = check_rows(y, ex.D, ldy, type, S, "y", who);
+    if (!rc && res) rc = check_rows(res, ex.D, ldr, type, S, "res", who);
+    if (!rc) rc = check_slots(ids, wts, who);
+    if (rc) return rc;
+    const int b = type_bytes(type);
+    const Rows ry = rows_of(y, ex.D, ldy, b), rx = rows_of(x, ex.D, ldx, b), rr = rows_of(res, ex.D, ldr, b);
+    const size_t n = (size_t)S * k * 4;
+    if (rows_overlap(ry, rx, S) || overlaps_vec(ry, S, ids, n) || overlaps_vec(ry, S, wts, n))
+        return fail(B200Q_EINVAL, "%s: y must not overlap x, ids or wts", who);
+    if (res && !(res == y && (ldr == ldy || S == 1)) && rows_overlap(ry, rr, S))
+        return fail(B200Q_EINVAL, "%s: res may be y (same stride) but must not partially overlap it", who);
+    e = launch_moe_experts(Moe{&ex, x, type, ldx, ids, wts, k, act, res, ldr, y, ldy, S}, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return B200Q_OK;
+}
+
+int b200q_block_norm(const void *m, int type, long long ldm, const void *h, long long ldh, const void *gate,
+                     long long ldg, int gate_cols, const float *w_post, float res_scale, float out_scale, void *h_out,
+                     long long ldo, const float *w, void *y, int ytype, long long ldy, int S, int D, float eps,
+                     void *stream) {
+    const char *who = "b200q_block_norm";
+    if (S < 0 || D < 1) return fail(B200Q_EINVAL, "%s: need S >= 0 and D >= 1 (got S=%d, D=%d)", who, S, D);
+    if (!type_bytes(type)) return fail(B200Q_EINVAL, "%s: unknown element type %d", who, type);
+    if (y && !type_bytes(ytype)) return fail(B200Q_EINVAL, "%s: unknown element type %d of y", who, ytype);
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(B200Q_EINVAL, "%s: eps must be finite and >= 0", who);
+    if (!finite(res_scale) || !finite(out_scale)) return fail(B200Q_EINVAL, "%s: the scales must be finite", who);
+    if (gate && gate_cols != 1 && gate_cols != D)
+        return fail(B200Q_EINVAL, "%s: gate_cols must be 1 or D (got %d)", who, gate_cols);
+    if (S == 0) return B200Q_OK;
+    if (!h_out && !y) return fail(B200Q_EINVAL, "%s: h_out or y must be given", who);
+    if (y && !w) return fail(B200Q_EINVAL, "%s: y needs w", who);
+    const int b = type_bytes(type);
+    int rc = check_rows(m, D, ldm, type, S, "m", who);
+    if (!rc && h) rc = check_rows(h, D, ldh, type, S, "h", who);
+    if (!rc && gate) rc = check_rows(gate, ldg == 0 ? 0 : gate_cols, ldg, type, S, "gate", who);
+    if (!rc && h_out) rc = check_rows(h_out, D, ldo, type, S, "h_out", who);
+    if (!rc && y) rc = check_rows(y, D, ldy, ytype, S, "y", who);
+    if (rc) return rc;
+    if ((uintptr_t)w_post % 4 || (y && (uintptr_t)w % 4))
+        return fail(B200Q_EINVAL, "%s: w_post and w must be 4-byte aligned", who);
+    const Rows rm = rows_of(m, D, ldm, b), rh = rows_of(h, D, ldh, b), ro = rows_of(h_out, D, ldo, b);
+    const Rows ry = rows_of(y, D, ldy, type_bytes(ytype));
+    const size_t wb = (size_t)D * 4, gb = gate ? ((size_t)(S - 1) * ldg + gate_cols) * b : 0;
+    if (y && (rows_overlap(ry, rm, S) || (h && rows_overlap(ry, rh, S)) || (h_out && rows_overlap(ry, ro, S)) ||
+              overlaps_vec(ry, S, gate, gb) || overlaps_vec(ry, S, w_post, wb) || overlaps_vec(ry, S, w, wb)))
+        return fail(B200Q_EINVAL, "%s: y must not overlap another operand", who);
+    if (h_out) {
+        const bool om = h_out == m && (ldo == ldm || S == 1), oh = h_out == h && (ldo == ldh || S == 1);
+        if ((!om && rows_overlap(ro, rm, S)) || (h && !oh && rows_overlap(ro, rh, S)) ||
+            overlaps_vec(ro, S, gate, gb) || overlaps_vec(ro, S, w_post, wb) || (y && overlaps_vec(ro, S, w, wb)))
+            return fail(B200Q_EINVAL,
+                        "%s: h_out may be h or m (same stride) but must not partially overlap them, or the gate or a weight",
+                        who);
+    }
+    cudaError_t e = launch_block_norm(BlockNorm{m, h, gate, h_out, y, type, ytype, ldm, ldh, ldg, ldo, ldy, gate_cols,
+                                                w_post, w, res_scale, out_scale, eps, S, D},
+                                      (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return B200Q_OK;
 }
 
 }  // extern "C"

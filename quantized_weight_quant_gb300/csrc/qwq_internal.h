@@ -155,4 +155,64 @@ cudaError_t launch_mat_q8(const MatQ8 &a, cudaStream_t st);
 cudaError_t launch_mv_q8(const MatQ8 &a, cudaStream_t st, bool *handled);
 cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st);
 
+// ---- the mixture-of-experts block
+
+// Scores, grouped top-k and weights of S tokens over E experts.
+struct Route {
+    const void *logits;
+    int type;
+    long long ld;              // values
+    const float *bias;         // or nullptr
+    int S, E, k, score, n_group, topk_group, group_top;
+    bool norm;
+    float scale;
+    int *ids;
+    float *wts;
+};
+constexpr int kRouteMaxE = 1024, kRouteMaxK = 32, kRouteMaxGroups = 32;
+cudaError_t launch_moe_route(const Route &a, cudaStream_t st);
+
+// The resident matrices of one expert, as the kernels read them.
+struct Expert {
+    const uint8_t *codes[3];   // gate, up [F, D], down [D, F]
+    const float *scales[3];
+};
+struct Experts {
+    int E, D, F, fmt, device;
+    long long ld_in, ld_out;   // row strides of gate / up and of down, bytes
+    Expert *table;             // device, [E]
+};
+constexpr int kMoeMaxExperts = 1024, kMoeMaxK = 32;
+
+// y = res + sum_j w_j down_e(act(gate_e x) * (up_e x)), e = ids[s, j].
+struct Moe {
+    const Experts *ex;
+    const void *x;
+    int type;
+    long long ldx;             // values
+    const int *ids;
+    const float *wts;
+    int k, act;
+    const void *res;
+    long long ldr;
+    void *y;
+    long long ldy;
+    int S;
+};
+cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st);
+cudaError_t moe_take_error(unsigned int *code);
+
+// p = m [* w_post / rms(m)], h' = res_scale h + out_scale gate p, y = h' w / rms(h').
+struct BlockNorm {
+    const void *m, *h, *gate;
+    void *h_out, *y;
+    int type, ytype;
+    long long ldm, ldh, ldg, ldo, ldy;   // values
+    int gate_cols;                       // D, or 1: one gate per row
+    const float *w_post, *w;
+    float res_scale, out_scale, eps;
+    int S, D;
+};
+cudaError_t launch_block_norm(const BlockNorm &a, cudaStream_t st);
+
 }  // namespace qwq
