@@ -1,0 +1,74 @@
+// Shared by the files of the experts' layer.
+#pragma once
+
+#include "qwq_internal.h"
+
+namespace qwq {
+
+constexpr int kMoePairs = 1024;               // slots of a launch at most
+constexpr int kMoeTokens = 64;                // tokens of a launch at most
+
+// One of the two products: gate and up of the tokens' rows, or down of h.
+struct MoeStream {
+    const Expert *table;
+    const int *ids;
+    const void *x;                            // gate and up: the tokens' rows
+    const float *in;                          // down: h [P][F], or the slices' sums of gate and up [ns_in][P][2][F]
+    float *out;                               // gate and up: what down reads; down: [ns][P][D]
+    unsigned int *err;                        // where a wrong id is recorded
+    long long ldx, ld;                        // values; bytes of a row of codes
+    int P, k, E, type, act;                   // P = S * k
+    int K, rows, F;                           // columns of the product's rows; its rows (F or D)
+    int lines, ns, ns_in;                     // 128-byte lines of a row, slices of them
+    int tiles;                                // of the rows
+    int nc, pitch;                            // columns of a chunk, bytes of one in shared memory
+    bool down;
+    // many columns: rows in f16 as prepared, their scales and sums
+    const uint8_t *cols;                      // [rows][pieces][lines][16 KC]
+    const float2 *info;                       // inverse scale, zero point times sum
+};
+
+// How a product is launched: its kernel, columns of a chunk, slices, shared memory.
+struct MoeWay {
+    int kind;                                 // 0 few columns, 1 few columns and a deep ring, 2 many columns
+    int nc, ns, pitch;
+    size_t smem;
+};
+template <int FMT> MoeWay moe_way(int kind, int pieces, int S, int lines);
+
+template <int FMT> cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int grid, cudaStream_t st);
+// rows of the tokens, or of h, prepared for many columns
+template <int FMT> cudaError_t moe_launch_prepare(const MoeStream &p, int rows, uint8_t *cols, float2 *info, cudaStream_t st);
+
+// One translation unit per format has these.
+#define MOE_FORMAT(F)                                                                                          \
+    template <> MoeWay moe_way<F>(int kind, int pieces, int S, int lines);                                     \
+    extern template cudaError_t moe_launch_stream<F>(const MoeStream &, const MoeWay &, int, cudaStream_t);    \
+    extern template cudaError_t moe_launch_prepare<F>(const MoeStream &, int, uint8_t *, float2 *, cudaStream_t)
+MOE_FORMAT(B200Q_I8);
+MOE_FORMAT(B200Q_I4);
+MOE_FORMAT(B200Q_I2);
+#undef MOE_FORMAT
+
+// f16 pieces of a column: f32 needs two for its 24 bits; h of f16 rows two, so
+// that its rounding is below y's; f16 and bf16 are exact in one.
+inline int moe_pieces(int type, bool down) { return type == B200Q_T_F32 || (down && type == B200Q_T_F16) ? 2 : 1; }
+
+template <class K, class... P>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const P &...p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p...);
+    count_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace qwq

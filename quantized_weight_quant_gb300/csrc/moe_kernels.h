@@ -1,0 +1,826 @@
+// Kernels of the experts' layer (moe_experts.cu has the overview): the plan that
+// every block makes from the ids, and the products of each expert's matrices with
+// its columns.  One translation unit per format instantiates them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "codes_f16.h"
+#include "moe.h"
+#include "qmat_q8.h"
+
+namespace qwq {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRedPitch = 20;                 // floats of a column's 16 sums in shared memory: no bank conflicts
+
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ---------------------------------------------------------------- plan
+// The slots in the order of their experts, in chunks of at most nc columns.
+struct Plan {
+    unsigned short order[kMoePairs];          // slots, by expert
+    unsigned short expert[kMoePairs], first[kMoePairs];   // of chunk c: its expert, its first place in order
+    unsigned char n[kMoePairs];               // and its columns
+    int chunks;
+};
+struct PlanScratch {
+    int count[kMoeMaxExperts];                // slots of an expert, then their first place
+    unsigned short rank[kMoePairs];           // of a slot among its expert's
+    short id[kMoePairs];
+};
+
+// Ends with a barrier.
+__device__ __forceinline__ void make_plan(const MoeStream &p, Plan &pl, PlanScratch &sc) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int e = tid; e < p.E; e += blockDim.x) sc.count[e] = 0;
+    for (int i = tid; i < p.P; i += blockDim.x) {
+        int e = p.ids[i];
+        if (e < -1 || e >= p.E) {
+            if (!p.down && blockIdx.x == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_EINVAL));
+            e = -1;
+        }
+        sc.id[i] = (short)e;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // ranks in the order of the slots
+        for (int i0 = 0; i0 < p.P; i0 += 32) {
+            const int i = i0 + lane, e = i < p.P ? sc.id[i] : -1;
+            const unsigned same = __match_any_sync(kAll, e);
+            const int before = e >= 0 ? sc.count[e] : 0;
+            __syncwarp();
+            if (e >= 0) {
+                sc.rank[i] = (unsigned short)(before + __popc(same & ((1u << lane) - 1)));
+                if (lane == __ffs(same) - 1) sc.count[e] = before + __popc(same);
+            }
+            __syncwarp();
+        }
+        // first places and chunks
+        int place = 0, chunk = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane, c = e < p.E ? sc.count[e] : 0, m = (c + p.nc - 1) / p.nc;
+            int a = c, b = m;                  // sums up to and with this lane's
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int va = __shfl_up_sync(kAll, a, o), vb = __shfl_up_sync(kAll, b, o);
+                if (lane >= o) a += va, b += vb;
+            }
+            const int f = place + a - c;
+            if (e < p.E) sc.count[e] = f;
+            for (int j = 0; j < m; ++j) {
+                const int at = chunk + b - m + j;
+                pl.expert[at] = (unsigned short)e;
+                pl.first[at] = (unsigned short)(f + j * p.nc);
+                pl.n[at] = (unsigned char)min(p.nc, c - j * p.nc);
+            }
+            place += __shfl_sync(kAll, a, 31);
+            chunk += __shfl_sync(kAll, b, 31);
+        }
+        if (lane == 0) pl.chunks = chunk;
+    }
+    __syncthreads();
+    for (int i = tid; i < p.P; i += blockDim.x)
+        if (sc.id[i] >= 0) pl.order[sc.count[sc.id[i]] + sc.rank[i]] = (unsigned short)i;
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- columns
+template <class T> __device__ __forceinline__ float as_float(T v);
+template <> __device__ __forceinline__ float as_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ float as_float<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Eight values of a row from column c on, 0 past the row.
+template <class T>
+__device__ __forceinline__ void row8(const T *r, int c, int K, float (&v)[8]) {
+    union {
+        uint4 q[sizeof(T) / 2];
+        T e[8];
+    } u;
+    if (c + 8 <= K && (uintptr_t)(r + c) % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u.q[i] = reinterpret_cast<const uint4 *>(r + c)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = as_float<T>(u.e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < K ? as_float<T>(r[c + i]) : 0.f;
+    }
+}
+
+// Eight values of slot `slot`'s column of the product from column c on: of its
+// token's row, or h, or act(gate) * up from the slices' sums.
+__device__ __forceinline__ void column8(const MoeStream &p, int slot, int c, float (&v)[8]) {
+    if (!p.down) {
+        const long long at = (long long)(slot / p.k) * p.ldx;
+        if (p.type == B200Q_T_F32) row8((const float *)p.x + at, c, p.K, v);
+        else if (p.type == B200Q_T_F16) row8((const __half *)p.x + at, c, p.K, v);
+        else row8((const __nv_bfloat16 *)p.x + at, c, p.K, v);
+        return;
+    }
+    if (p.ns_in == 1) {
+        row8(p.in + (long long)slot * p.F, c, p.F, v);
+        return;
+    }
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+    for (int s = 0; s < p.ns_in; ++s) {
+        const float *g = p.in + ((long long)s * p.P + slot) * 2 * p.F;
+        float a[8], b[8];
+        row8(g, c, p.F, a);
+        row8(g + p.F, c, p.F, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += a[i], u[i] += b[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_q8(v[i], p.act) * u[i];
+}
+
+// The power of two that brings a column's largest magnitude (its bits) to
+// [2^14, 2^15); at most 2^126, so that the inverse is a normal number.
+__device__ __forceinline__ int exponent_for(unsigned top) { return top ? min(126, 14 + 127 - (int)(top >> 23)) : 0; }
+__device__ __forceinline__ float power(int e) { return __uint_as_float((unsigned)(127 + e) << 23); }
+
+// Unit u of a column: the eight values whose 16 bytes stand side by side for
+// the instructions, and where they do.  Per 64 bytes of codes a column has KC / 8
+// pieces of 64 bytes, 16 of them for each of the four threads that share a row.
+template <int FMT>
+__device__ __forceinline__ void unit8(const MoeStream &p, int slot, int k0, int u, float (&v)[8]) {
+    if constexpr (FMT == B200Q_I2) {
+        // a word is 16 codes: the values that its instructions 2j, 2j+1 take, j = u & 1
+        const int c = k0 + 16 * (u >> 1), j = u & 1;
+        float lo[8], hi[8];
+        column8(p, slot, c, lo);
+        column8(p, slot, c + 8, hi);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            v[4 * t] = j ? lo[2 + t] : lo[t];
+            v[4 * t + 1] = j ? hi[2 + t] : hi[t];
+            v[4 * t + 2] = j ? lo[6 + t] : lo[4 + t];
+            v[4 * t + 3] = j ? hi[6 + t] : hi[4 + t];
+        }
+    } else {
+        column8(p, slot, k0 + 8 * u, v);
+    }
+}
+template <int FMT>
+__device__ __forceinline__ int unit_at(int u) {
+    if constexpr (FMT == B200Q_I2) return (u >> 5) * 512 + (((u >> 1) & 3) * 2 + (u & 1)) * 64 + ((u >> 3) & 3) * 16;
+    constexpr int V = Fmt<FMT>::KC / 8;        // units of a thread's 16 bytes of codes
+    return u / (4 * V) * (64 * V) + u % V * 64 + u / V % 4 * 16;
+}
+
+// A unit's values, scaled, as 16 bytes of f16 in the order in which fields()
+// takes a word of codes apart, and what is left of them to `rest`; their sum as
+// they are then.  RAW: two by two they meet fields 0 0 1 1 of a word, or 2 2 3 3
+// (odd units of int2), and are divided by 2^b for a field at bit b.
+template <int FMT, int PC, bool RAW>
+__device__ __forceinline__ float split(const float (&v)[8], float scale, int u, uint4 &hi, uint4 &rest) {
+    __half h[8], l[8];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = v[i] * scale;
+        h[i] = __float2half_rn(f);
+        l[i] = __float2half_rn(f - __half2float(h[i]));
+        sum += __half2float(h[i]) + (PC == 2 ? __half2float(l[i]) : 0.f);
+    }
+    const float d0 = RAW && FMT == B200Q_I2 && (u & 1) ? 1.f / 16.f : 1.f;
+    const float d1 = RAW ? d0 / (float)(1 << kShift<FMT>) : 1.f;
+    auto pack = [](__half a, __half b, float by) {
+        const __half2 m = RAW ? __hmul2(__halves2half2(a, b), __float2half2_rn(by)) : __halves2half2(a, b);
+        return *reinterpret_cast<const uint32_t *>(&m);
+    };
+    if constexpr (FMT == B200Q_I4) {           // pairs (0,4) (2,6) (1,5) (3,7)
+        hi = make_uint4(pack(h[0], h[4], d0), pack(h[2], h[6], d0), pack(h[1], h[5], d1), pack(h[3], h[7], d1));
+        rest = make_uint4(pack(l[0], l[4], d0), pack(l[2], l[6], d0), pack(l[1], l[5], d1), pack(l[3], l[7], d1));
+    } else {
+        hi = make_uint4(pack(h[0], h[1], d0), pack(h[2], h[3], d0), pack(h[4], h[5], d1), pack(h[6], h[7], d1));
+        rest = make_uint4(pack(l[0], l[1], d0), pack(l[2], l[3], d0), pack(l[4], l[5], d1), pack(l[6], l[7], d1));
+    }
+    return sum;
+}
+
+// Sum of a row's products with a column, from the accumulators' a: RAW codes are
+// 2^-24 of theirs, and the zero point times the column's sum comes off.
+template <bool RAW>
+__device__ __forceinline__ float product(float a, float zero, float scale, float unscale) {
+    return (RAW ? fmaf(a, 16777216.f, -zero) : a) * scale * unscale;
+}
+
+// The sums of rows r and r + 8 of a tile (8 of gate and up, or 16 of down) with
+// the column of a slot: written.
+__device__ __forceinline__ void put(const MoeStream &p, int slice, int slot, int tile, int r, float a, float b) {
+    const long long at = (long long)slice * p.P + slot;
+    if (p.down) {
+        const int o = tile * 16 + r;
+        if (o < p.rows) p.out[at * p.rows + o] = a;
+        if (o + 8 < p.rows) p.out[at * p.rows + o + 8] = b;
+    } else {
+        const int f = tile * 8 + r;
+        if (f >= p.rows) return;
+        if (p.ns == 1) {
+            p.out[at * p.rows + f] = act_q8(a, p.act) * b;
+        } else {
+            p.out[at * 2 * p.rows + f] = a;
+            p.out[(at * 2 + 1) * p.rows + f] = b;
+        }
+    }
+}
+
+// The products of a thread's 16 bytes of codes (of MT tiles, rows g and g + 8)
+// with NT x 8 columns, of which the first n are wanted; `from(nt)` is where this
+// thread's column of tile nt has its values, its second pieces `plane` bytes
+// further.  Two pieces: the first ones' sums are taken out of the accumulator
+// after every word of codes, the second ones are in `rest`.
+template <int FMT, int NT, int MT, int PC, bool RAW, class From>
+__device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], int n, From from, int plane, float (&sum)[MT][NT][4],
+                                               float (&acc)[MT][NT][4], float (&rest)[PC == 2 ? MT : 1][PC == 2 ? NT : 1][4]) {
+    constexpr int MMAS = Fmt<FMT>::MMAS;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t a[MT][MMAS][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const uint4 &c0 = q[m][0], &c1 = q[m][1];
+            const uint32_t w0 = w == 0 ? c0.x : w == 1 ? c0.y : w == 2 ? c0.z : c0.w;
+            const uint32_t w1 = w == 0 ? c1.x : w == 1 ? c1.y : w == 2 ? c1.z : c1.w;
+#pragma unroll
+            for (int t = 0; t < MMAS; ++t) {
+                if constexpr (RAW) {
+                    raw_fields<FMT>(w0, t, a[m][t][0], a[m][t][2]);
+                    raw_fields<FMT>(w1, t, a[m][t][1], a[m][t][3]);
+                } else {
+                    fields<FMT>(w0, t, a[m][t][0], a[m][t][2]);
+                    fields<FMT>(w1, t, a[m][t][1], a[m][t][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && nt * 8 >= n) break;
+#pragma unroll
+            for (int pc = 0; pc < PC; ++pc) {
+                const uint8_t *at = from(nt) + pc * plane;
+                auto to = [&](int m) -> float (&)[4] { return pc ? rest[PC == 2 ? m : 0][PC == 2 ? nt : 0] : acc[m][nt]; };
+                if constexpr (MMAS == 1) {
+                    const uint2 b = *reinterpret_cast<const uint2 *>(at + (w >> 1) * 64 + (w & 1) * 8);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma_f16(to(m), a[m][0][0], a[m][0][1], a[m][0][2], a[m][0][3], b.x, b.y);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < MMAS; t += 2) {
+                        const uint4 b = *reinterpret_cast<const uint4 *>(at + (w * (MMAS / 2) + t / 2) * 64);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            mma_f16(to(m), a[m][t][0], a[m][t][1], a[m][t][2], a[m][t][3], b.x, b.y);
+                            mma_f16(to(m), a[m][t + 1][0], a[m][t + 1][1], a[m][t + 1][2], a[m][t + 1][3], b.z, b.w);
+                        }
+                    }
+                }
+            }
+            if constexpr (PC == 2) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[m][nt][i] += acc[m][nt][i], acc[m][nt][i] = 0.f;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- few columns
+// Up to 8 columns of an expert, resident in shared memory.
+constexpr int kFewWarps = 16, kFewColumns = 8;
+
+struct FewColumns {
+    unsigned top[kFewColumns];                 // the largest magnitude
+    float unscale[kFewColumns], zero[kFewColumns];     // the inverse scale; the zero point times the sum
+    float part[512];                           // sums of 32 units each
+};
+
+// AHEAD: lines in a warp's ring.
+template <int AHEAD> struct FewShape {
+    static constexpr int kRing = kFewWarps * AHEAD * 2048;
+    static constexpr int kRedTile = kFewColumns * kRedPitch;           // floats of a warp's tile
+    static constexpr int kRed = 2 * kFewWarps * kRedTile * 4;          // two sets, used in turn; the plan's scratch before
+    static constexpr int kColumnsAt = kRing + kRed;
+    static constexpr int kPlanAt = kColumnsAt + (int)sizeof(FewColumns);
+    static constexpr int kB = (kPlanAt + (int)sizeof(Plan) + 127) / 128 * 128;
+    static_assert(sizeof(PlanScratch) <= kRed, "the plan's scratch lies where the sums will");
+};
+
+// The columns of a chunk, lines l0 .. l1-1, into shared memory.  A warp takes 32
+// units of a column at a time.  Called by the whole block; ends with a barrier.
+template <int FMT, int PC, bool RAW>
+__device__ __forceinline__ void stage(const MoeStream &p, const unsigned short *order, int n, int l0, int l1, uint8_t *B,
+                                      FewColumns &cl) {
+    constexpr int KC = Fmt<FMT>::KC;
+    const int units = (l1 - l0) * KC;          // of a column: KC to a line
+    const int k0 = l0 * 8 * KC;
+    const int blocks = (units + 31) / 32, all = n * blocks;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < kFewColumns) cl.top[threadIdx.x] = 0u;
+    __syncthreads();
+#pragma unroll 2
+    for (int b = warp; b < all; b += kFewWarps) {
+        const int c = b / blocks, u = (b - c * blocks) * 32 + lane;
+        unsigned m = 0;
+        if (u < units) {
+            float v[8];
+            column8(p, order[c], k0 + 8 * u, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        }
+        m = __reduce_max_sync(kAll, m);
+        if (lane == 0) atomicMax(&cl.top[c], m);
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int b = warp; b < all; b += kFewWarps) {
+        const int c = b / blocks, u = (b - c * blocks) * 32 + lane;
+        const float scale = power(exponent_for(cl.top[c]));
+        float sum = 0.f;
+        if (u < units) {
+            float v[8];
+            uint4 hi, rest;
+            unit8<FMT>(p, order[c], k0, u, v);
+            sum = split<FMT, PC, RAW>(v, scale, u, hi, rest);
+            uint8_t *to = B + c * p.pitch + unit_at<FMT>(u);
+            *reinterpret_cast<uint4 *>(to) = hi;
+            if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + p.nc * p.pitch) = rest;
+        }
+        if constexpr (RAW) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            if (lane == 0) cl.part[b] = sum;
+        }
+    }
+    __syncthreads();
+    if (warp < n) {
+        float sum = 0.f;
+        if constexpr (RAW) {
+            for (int b = lane; b < blocks; b += 32) sum += cl.part[warp * blocks + b];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        }
+        if (lane == 0) {
+            cl.unscale[warp] = power(-exponent_for(cl.top[warp]));
+            cl.zero[warp] = sum * kZeroPoint<FMT>;
+        }
+    }
+    __syncthreads();
+}
+
+// Warps that share a tile, of a block that has t tiles of `per` lines: the share
+// of the warps' lines that are used, in rounds of 16 / wk tiles; sharing costs a
+// barrier and an addition per tile.
+__device__ __forceinline__ int warps_per_tile(float t, int per) {
+    int best = 1;
+    float most = 0.f;
+    for (int wk = 1; wk <= kFewWarps && wk <= per; wk *= 2) {
+        const float g = (float)(kFewWarps / wk);
+        const float used = t / (ceilf(t / g) * g) * (float)per / (float)((per + wk - 1) / wk * wk) *
+                           (1.f - 0.02f * (float)(wk > 1 ? wk : 0));
+        if (used > most) most = used, best = wk;
+    }
+    return best;
+}
+
+template <int FMT, int PC, bool RAW, int AHEAD>
+__global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid_constant__ MoeStream p) {
+    using Sh = FewShape<AHEAD>;
+    constexpr int KC = Fmt<FMT>::KC;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *red = reinterpret_cast<float *>(smem + Sh::kRing);
+    FewColumns &cl = *reinterpret_cast<FewColumns *>(smem + Sh::kColumnsAt);
+    Plan &pl = *reinterpret_cast<Plan *>(smem + Sh::kPlanAt);
+    uint8_t *B = smem + Sh::kB;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+
+    // The ids may come from the kernel before gate and up; down follows them, and
+    // they were there when gate and up began.
+    if (!p.down) dependency_wait();
+    make_plan(p, pl, *reinterpret_cast<PlanScratch *>(red));
+    const long long all = (long long)pl.chunks * p.ns * p.tiles;
+    const long long lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+    const int wk = warps_per_tile((float)all / (float)gridDim.x, p.lines / p.ns);
+    const int kw = warp % wk, wm = warp / wk, groups = kFewWarps / wk;
+
+    // the copy cursor: this warp's next line
+    const long long first_end = (lo / p.tiles + 1) * p.tiles;
+    long long fu = lo + wm, fend = hi < first_end ? hi : first_end;         // its tile, the end of its slice's
+    int fcs = (int)(lo / p.tiles), fchunk = -1, fline = 0, fl1 = 0, fslot = 0;
+    const uint8_t *rows0 = nullptr, *rows1 = nullptr;                       // rows g and g + 8 of tile 0
+    const uint8_t *f0 = nullptr, *f1 = nullptr;                             // the next line of the cursor's
+    const long long tile_bytes = (p.down ? 16 : 8) * p.ld;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (AHEAD * 2048) + lane * 16;
+    const int step = wk * 128;
+    auto open = [&]() {                        // the cursor's tile, or a later one that has a line for this warp
+        while (true) {
+            if (fu >= fend) {
+                if (fend >= hi) return;        // none is left
+                ++fcs;
+                fu = fend + wm;
+                fend = hi < fend + p.tiles ? hi : fend + p.tiles;
+                continue;
+            }
+            const int c = p.ns == 1 ? fcs : fcs / p.ns, sl = fcs - c * p.ns;
+            fline = (int)((long long)sl * p.lines / p.ns) + kw;
+            fl1 = (int)((long long)(sl + 1) * p.lines / p.ns);
+            if (fline >= fl1) {
+                fu += groups;
+                continue;
+            }
+            if (c != fchunk) {
+                const Expert &e = p.table[pl.expert[c]];
+                rows0 = (p.down ? e.codes[2] : e.codes[0]) + g * p.ld + tig * 16;
+                rows1 = (p.down ? e.codes[2] + 8 * p.ld : e.codes[1]) + g * p.ld + tig * 16;
+                fchunk = c;
+            }
+            const long long off = (fu - (long long)fcs * p.tiles) * tile_bytes + fline * 128;
+            f0 = rows0 + off;
+            f1 = rows1 + off;
+            return;
+        }
+    };
+    auto copy_line = [&]() {
+        if (fu < fend) {
+            const uint32_t to = ring + fslot * 2048;
+            copy16(to, f0);
+            copy16(to + 512, f1);
+            copy16(to + 1024, f0 + 64);
+            copy16(to + 1536, f1 + 64);
+            f0 += step;
+            f1 += step;
+            if (++fslot == AHEAD) fslot = 0;
+            if ((fline += wk) >= fl1) {
+                fu += groups;
+                open();
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");           // empty at the end: the waits count groups
+    };
+    open();
+#pragma unroll 1
+    for (int i = 0; i < AHEAD; ++i) copy_line();
+
+    if (p.down) dependency_wait();
+    let_dependents_start();
+
+    const uint8_t *slots = smem + warp * (AHEAD * 2048) + lane * 16;
+    const int colat = min(g, p.nc - 1) * p.pitch + tig * 16;           // a column past the chunk's is computed and not stored
+    int slot = 0, set = 0;
+    for (long long u0 = lo; u0 < hi;) {        // the block's tiles of one slice
+        const int cs = (int)(u0 / p.tiles), c = cs / p.ns, slice = cs - c * p.ns;
+        const long long base = (long long)cs * p.tiles, u1 = hi < base + p.tiles ? hi : base + p.tiles;
+        const int l0 = (int)((long long)slice * p.lines / p.ns), l1 = (int)((long long)(slice + 1) * p.lines / p.ns);
+        const unsigned short *order = pl.order + pl.first[c];
+        const int n = pl.n[c];
+        const Expert &e = p.table[pl.expert[c]];
+        const float *s0 = p.down ? e.scales[2] : e.scales[0], *s1 = p.down ? e.scales[2] + 8 : e.scales[1];
+        __syncthreads();                       // the columns before are read
+        stage<FMT, PC, RAW>(p, order, n, l0, l1, B, cl);
+        const int r = wk == 1 ? g : tid & 7;
+        auto finish = [&](int tile, int col, float a, float b, float sa, float sb) {
+            const float un = cl.unscale[col], z = cl.zero[col];
+            put(p, slice, order[col], tile, r, product<RAW>(a, z, sa, un), product<RAW>(b, z, sb, un));
+        };
+        for (long long u = u0 + wm; u < u1; u += groups) {
+            const int tile = (int)(u - base);
+            // the scales of rows r and r + 8, fetched now, used at the end; rows past the last have scale 0
+            const float sa = s0[tile * (p.down ? 16 : 8) + r], sb = s1[tile * (p.down ? 16 : 8) + r];
+            float sum[1][1][4] = {};
+            const uint8_t *xb = B + kw * (16 * KC) + colat;
+#pragma unroll 1
+            for (int line = l0 + kw; line < l1; line += wk, xb += wk * (16 * KC)) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+                uint4 q[2][1][2];              // [64 bytes][tile][row half]
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i >> 1][0][i & 1] = *reinterpret_cast<const uint4 *>(slots + slot * 2048 + i * 512);
+                if (++slot == AHEAD) slot = 0;
+                copy_line();                   // into the slot just read: this thread's own
+                float acc[1][1][4] = {}, rest[1][1][4] = {};
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    chunk_products<FMT, 1, 1, PC, RAW>(q[half], n, [&](int) { return xb + half * (8 * KC); }, p.nc * p.pitch, sum, acc,
+                                                       rest);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[0][0][i] += PC == 2 ? rest[0][0][i] : acc[0][0][i];
+            }
+            const float (&s)[4] = sum[0][0];
+            if (wk == 1) {
+                if (2 * tig < n) finish(tile, 2 * tig, s[0], s[2], sa, sb);
+                if (2 * tig + 1 < n) finish(tile, 2 * tig + 1, s[1], s[3], sa, sb);
+            } else {
+                // [column][row] of this warp's part, added over the tile's warps in order; the two sets
+                // take turns, so that one barrier per tile is enough
+                float *to = red + (set * kFewWarps + warp) * Sh::kRedTile + 2 * tig * kRedPitch + g;
+                to[0] = s[0], to[kRedPitch] = s[1], to[8] = s[2], to[kRedPitch + 8] = s[3];
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + wm), "r"(wk * 32) : "memory");
+                for (int col = (kw * 32 + lane) >> 3; col < n; col += wk * 4) {
+                    const float *from = red + (set * kFewWarps + wm * wk) * Sh::kRedTile + col * kRedPitch + r;
+                    float a = 0.f, b = 0.f;
+                    for (int w = 0; w < wk; ++w) a += from[w * Sh::kRedTile], b += from[w * Sh::kRedTile + 8];
+                    finish(tile, col, a, b, sa, sb);
+                }
+                set ^= 1;
+            }
+        }
+        u0 = u1;
+    }
+}
+
+// ---------------------------------------------------------------- many columns
+// Up to 32 columns of an expert, prepared in memory once and copied line by line
+// beside the codes, in stages that the whole block shares: a warp keeps the sums
+// of 32 rows with all columns over the rows' whole length.
+constexpr int kManyWarps = 8, kManyThreads = 32 * kManyWarps;
+template <int FMT, int PC> constexpr int kManyColumns = FMT == B200Q_I2 && PC == 2 ? 16 : 32;
+template <int FMT, int PC> constexpr int kManyStages = FMT == B200Q_I8 || (FMT == B200Q_I4 && PC == 1) ? 4 : 3;
+template <int FMT, int PC> struct ManyShape {
+    static constexpr int kPitch = 16 * Fmt<FMT>::KC + 64;              // of a column's line: no bank conflicts
+    static constexpr int kPlane = kManyColumns<FMT, PC> * kPitch;
+    static constexpr int kCodes = kManyWarps * 4096;
+    static constexpr int kStage = kCodes + PC * kPlane;
+    static constexpr int kPlanAt = kManyStages<FMT, PC> * kStage;      // the plan's scratch lies in the stages before
+    static constexpr int kInfoAt = (kPlanAt + (int)sizeof(Plan) + 15) / 16 * 16;
+    static constexpr int kBytes = kInfoAt + 2 * 32 * 8;
+};
+
+// A row of the tokens, or of h, per block, as pieces of f16 in the order of the
+// instructions; what the sums need of it to info.
+template <int FMT, int PC, bool RAW>
+__global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant__ MoeStream p, uint8_t *cols, float2 *info) {
+    constexpr int KC = Fmt<FMT>::KC;
+    __shared__ unsigned tops[8];
+    __shared__ float sums[8];
+    dependency_wait();
+    let_dependents_start();
+    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (p.down) {
+        const int e = p.ids[row];
+        if (e < 0 || e >= p.E) return;         // an empty slot has no h
+    }
+    const int slot = p.down ? row : row * p.k, units = p.lines * KC;
+    unsigned m = 0;
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += 256) {
+        float v[8];
+        column8(p, slot, 8 * u, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    m = __reduce_max_sync(kAll, m);
+    if (lane == 0) tops[warp] = m;
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, tops[w]);
+    const int up = exponent_for(m);
+    const float scale = power(up);
+    uint8_t *to = cols + (long long)row * PC * p.lines * (16 * KC);
+    float sum = 0.f;
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += 256) {
+        float v[8];
+        uint4 hi, rest;
+        unit8<FMT>(p, slot, 0, u, v);
+        sum += split<FMT, PC, RAW>(v, scale, u, hi, rest);
+        *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u)) = hi;
+        if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * (16 * KC) + unit_at<FMT>(u)) = rest;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.f;
+        for (int w = 0; w < 8; ++w) sum += sums[w];
+        info[row] = make_float2(power(-up), RAW ? sum * kZeroPoint<FMT> : 0.f);
+    }
+}
+
+template <int FMT, int PC, bool RAW>
+__global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_constant__ MoeStream p) {
+    using Sh = ManyShape<FMT, PC>;
+    constexpr int KC = Fmt<FMT>::KC, NT = kManyColumns<FMT, PC> / 8, STAGES = kManyStages<FMT, PC>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    Plan &pl = *reinterpret_cast<Plan *>(smem + Sh::kPlanAt);
+    float2 *info = reinterpret_cast<float2 *>(smem + Sh::kInfoAt);     // [2][32], of two chunks in turn
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+
+    // the ids were there when the kernel that prepares the rows began
+    make_plan(p, pl, *reinterpret_cast<PlanScratch *>(smem));
+    dependency_wait();
+    let_dependents_start();
+    const int units = (p.tiles + 1) / 2;       // pairs of tiles
+    const long long all = (long long)pl.chunks * units;
+    const long long lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+
+    // A round: up to 8 units of one chunk, a warp each, over the whole length of
+    // the rows.  A chunk's rounds share its units evenly.
+    struct Round {
+        long long u, end;                      // the first unit, the end of the block's in this chunk
+        int c, n;                              // chunk; units
+    };
+    auto begin = [&](Round &r, long long u) {
+        r.u = u;
+        r.n = 0;
+        if (u >= hi) return;
+        r.c = (int)(u / units);
+        const long long last = (long long)(r.c + 1) * units;
+        r.end = hi < last ? hi : last;
+        const int left = (int)(r.end - u), rounds = (left + kManyWarps - 1) / kManyWarps;
+        r.n = (left + rounds - 1) / rounds;
+    };
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    const long long tile_bytes = (p.down ? 16 : 8) * p.ld, row_bytes = (long long)PC * p.lines * (16 * KC);
+
+    // the copy cursor
+    Round f = {};
+    int fline = 0, fstage = 0, fn = 0;
+    const uint8_t *f0[2] = {}, *f1[2] = {};
+    const unsigned short *forder = nullptr;
+    auto open = [&]() {
+        if (f.n == 0) return;
+        fline = 0;
+        forder = pl.order + pl.first[f.c];
+        fn = pl.n[f.c];
+        if (warp < f.n) {
+            const Expert &e = p.table[pl.expert[f.c]];
+            const int tile = (int)(f.u + warp - (long long)f.c * units) * 2;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {      // a tile past the last reads the last again
+                const long long off = min(tile + m, p.tiles - 1) * tile_bytes + g * p.ld + tig * 16;
+                f0[m] = (p.down ? e.codes[2] : e.codes[0]) + off;
+                f1[m] = (p.down ? e.codes[2] + 8 * p.ld : e.codes[1]) + off;
+            }
+        }
+    };
+    auto copy_line = [&]() {
+        if (f.n) {
+            const uint32_t to = base + fstage * Sh::kStage;
+            if (warp < f.n) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t t = to + warp * 4096 + m * 2048 + lane * 16;
+                    copy16(t, f0[m]);
+                    copy16(t + 512, f1[m]);
+                    copy16(t + 1024, f0[m] + 64);
+                    copy16(t + 1536, f1[m] + 64);
+                    f0[m] += 128;
+                    f1[m] += 128;
+                }
+            }
+            for (int i = tid; i < fn * PC * KC; i += kManyThreads) {   // 16 bytes each
+                const int c = i / (PC * KC), pc = i / KC % PC, j = i % KC, slot = forder[c];
+                const int row = p.down ? slot : slot / p.k;
+                copy16(to + Sh::kCodes + pc * Sh::kPlane + c * Sh::kPitch + j * 16,
+                       p.cols + row * row_bytes + ((long long)pc * p.lines + fline) * (16 * KC) + j * 16);
+            }
+            if (++fstage == STAGES) fstage = 0;
+            if (++fline == p.lines) {
+                begin(f, f.u + f.n);
+                open();
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    begin(f, lo);
+    open();
+    __syncthreads();                           // the plan's scratch is read
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) copy_line();
+
+    int stage = 0, turn = 0, chunk = -1;
+    Round r = {};
+    begin(r, lo);
+    while (r.n) {
+        if (r.c != chunk) {                    // read after this round's first barrier at the earliest
+            turn ^= 1;
+            if (tid < pl.n[r.c]) {
+                const int slot = pl.order[pl.first[r.c] + tid];
+                info[turn * 32 + tid] = p.info[p.down ? slot : slot / p.k];
+            }
+            chunk = r.c;
+        }
+        const int n = pl.n[r.c], tile = (int)(r.u + warp - (long long)r.c * units) * 2;
+        const bool mine = warp < r.n;
+        float sum[2][NT][4] = {}, sa[2] = {}, sb[2] = {};
+        if (mine) {
+            const Expert &e = p.table[pl.expert[r.c]];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int t = min(tile + m, p.tiles - 1) * (p.down ? 16 : 8) + g;
+                sa[m] = (p.down ? e.scales[2] : e.scales[0])[t];
+                sb[m] = (p.down ? e.scales[2] + 8 : e.scales[1])[t];
+            }
+        }
+#pragma unroll 1
+        for (int line = 0; line < p.lines; ++line) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncthreads();                   // this stage is there for all, the one before is read by all
+            copy_line();
+            const uint8_t *at = smem + stage * Sh::kStage;
+            if (++stage == STAGES) stage = 0;
+            if (!mine) continue;
+            float acc[2][NT][4] = {}, rest[PC == 2 ? 2 : 1][PC == 2 ? NT : 1][4] = {};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint4 q[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        q[m][i] = *reinterpret_cast<const uint4 *>(at + warp * 4096 + m * 2048 + half * 1024 + i * 512 + lane * 16);
+                const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
+                chunk_products<FMT, NT, 2, PC, RAW>(q, n, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[m][nt][i] += PC == 2 ? rest[PC == 2 ? m : 0][PC == 2 ? nt : 0][i] : acc[m][nt][i];
+        }
+        if (mine) {
+            const unsigned short *order = pl.order + pl.first[r.c];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = nt * 8 + 2 * tig + j;
+                        if (c < n && tile + m < p.tiles) {
+                            const float2 i = info[turn * 32 + c];
+                            put(p, 0, order[c], tile + m, g, product<RAW>(sum[m][nt][j], i.y, sa[m], i.x),
+                                product<RAW>(sum[m][nt][2 + j], i.y, sb[m], i.x));
+                        }
+                    }
+        }
+        begin(r, r.u + r.n);
+    }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- launches
+template <int FMT, int PC, bool RAW>
+cudaError_t moe_start(const MoeStream &p, const MoeWay &w, int grid, cudaStream_t st) {
+    auto go = [&](auto kernel, int warps) {
+        cudaError_t e = allow_dynamic_smem((const void *)kernel, 227 * 1024);
+        return e != cudaSuccess ? e : launch_dependent(kernel, dim3(grid), 32 * warps, w.smem, st, p);
+    };
+    if (w.kind == 2) return go(moe_many_kernel<FMT, PC, RAW>, kManyWarps);
+    if (w.kind == 1) return go(moe_few_kernel<FMT, PC, RAW, 5>, kFewWarps);
+    return go(moe_few_kernel<FMT, PC, RAW, 3>, kFewWarps);
+}
+
+template <int FMT>
+cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int grid, cudaStream_t st) {
+    if (p.type == B200Q_T_F32) return moe_start<FMT, 2, false>(p, w, grid, st);
+    return moe_pieces(p.type, p.down) == 2 ? moe_start<FMT, 2, true>(p, w, grid, st) : moe_start<FMT, 1, true>(p, w, grid, st);
+}
+
+template <int FMT>
+cudaError_t moe_launch_prepare(const MoeStream &p, int rows, uint8_t *cols, float2 *info, cudaStream_t st) {
+    if (p.type == B200Q_T_F32) return launch_dependent(moe_prepare_kernel<FMT, 2, false>, dim3(rows), 256, 0, st, p, cols, info);
+    return moe_pieces(p.type, p.down) == 2 ? launch_dependent(moe_prepare_kernel<FMT, 2, true>, dim3(rows), 256, 0, st, p, cols, info)
+                                           : launch_dependent(moe_prepare_kernel<FMT, 1, true>, dim3(rows), 256, 0, st, p, cols, info);
+}
+
+// kind 0 and 1: as many columns as there are tokens, at most 8, and slices that
+// keep them within what the ring leaves of the shared memory.
+template <int FMT>
+MoeWay moe_way_of(int kind, int pieces, int S, int lines) {
+    constexpr int KC = Fmt<FMT>::KC;
+    MoeWay w{};
+    w.kind = kind;
+    w.ns = 1;
+    if (kind == 2) {
+        w.nc = pieces == 2 ? kManyColumns<FMT, 2> : kManyColumns<FMT, 1>;
+        w.smem = pieces == 2 ? ManyShape<FMT, 2>::kBytes : ManyShape<FMT, 1>::kBytes;
+        static_assert(ManyShape<FMT, 2>::kBytes <= 227 * 1024 && ManyShape<FMT, 1>::kBytes <= 227 * 1024, "shared memory");
+        return w;
+    }
+    w.nc = S < kFewColumns ? S : kFewColumns;
+    const size_t fixed = kind ? FewShape<5>::kB : FewShape<3>::kB, room = 227 * 1024 - fixed;
+    // a column is 64 bytes off a 128-byte multiple: no bank conflicts; 512 blocks of 32 units have their sums' places
+    auto fits = [&](int ns) {
+        const long long per = (lines + ns - 1) / ns;
+        return (per * 16 * KC + 64) * w.nc * pieces <= (long long)room && (per * KC + 31) / 32 * w.nc <= 512;
+    };
+    while (!fits(w.ns)) ++w.ns;
+    w.pitch = (lines + w.ns - 1) / w.ns * 16 * KC + 64;
+    w.smem = fixed + (size_t)w.pitch * w.nc * pieces;
+    return w;
+}
+
+}  // namespace qwq
