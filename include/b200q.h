@@ -619,7 +619,7 @@ typedef struct b200q_experts b200q_experts;   /* opaque: the resident experts of
 /*
  * The experts of a layer, from E triples of resident tensors: gate[e] and up[e]
  * [F, D], down[e] [D, F], all of one quantized format (int8, int4, int2) with
- * per-row scales, on the current device; 1 <= E <= 1024.  gate, up and down are
+ * per-row scales, on the current device; 1 <= E <= 1024, D and F at most 2^24.  gate, up and down are
  * HOST arrays of E handles, read during the call only; the same tensor may stand
  * in several places.  The handle holds a device table of the tensors' addresses,
  * not the tensors: they have to outlive it and its last call.  A shared expert

@@ -990,7 +990,9 @@ b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q
                 ex->E = E, ex->fmt = t.fmt, ex->device = t.device, ex->F = t.O, ex->D = t.I, ex->ld_in = t.ld;
             }
             if (e == 0 && m == 2) ex->ld_out = t.ld;
-            if (t.fmt != ex->fmt || t.O != (m == 2 ? ex->D : ex->F) || t.I != (m == 2 ? ex->F : ex->D))
+            if (t.O > kMoeMaxSize || t.I > kMoeMaxSize)
+                rc = fail(B200Q_EINVAL, "%s: D and F must be at most %d", who, kMoeMaxSize);
+            else if (t.fmt != ex->fmt || t.O != (m == 2 ? ex->D : ex->F) || t.I != (m == 2 ? ex->F : ex->D))
                 rc = fail(B200Q_EINVAL, "%s: %s %d is not [%d, %d] in the first tensor's format", who,
                           m == 0 ? "gate" : m == 1 ? "up" : "down", e, m == 2 ? ex->D : ex->F, m == 2 ? ex->F : ex->D);
             host[e].codes[m] = t.codes;

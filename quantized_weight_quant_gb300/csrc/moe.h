@@ -8,21 +8,32 @@ namespace qwq {
 constexpr int kMoePairs = 1024;               // slots of a launch at most
 constexpr int kMoeTokens = 64;                // tokens of a launch at most
 
+// Division of a number below 2^31 by a fixed one, without the instructions of a
+// division.
+struct Quotient {
+    unsigned long long by;                    // 2^64 / d + 1; 0: d = 1
+    explicit Quotient(unsigned d = 1) : by(d > 1 ? ~0ull / d + 1 : 0) {}
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int v) const { return by ? (int)__umul64hi((unsigned long long)v, by) : v; }
+#endif
+};
+
 // One of the two products: gate and up of the tokens' rows, or down of h.
 struct MoeStream {
     const Expert *table;
     const int *ids;
     const void *x;                            // gate and up: the tokens' rows
-    const float *in;                          // down: h [P][F], or the slices' sums of gate and up [ns_in][P][2][F]
+    const float *in;                          // down: h [P][ldh], or the slices' sums of gate and up [ns_in][P][2][ldh]
     float *out;                               // gate and up: what down reads; down: [ns][P][D]
     unsigned int *err;                        // where a wrong id is recorded
     long long ldx, ld;                        // values; bytes of a row of codes
     int P, k, E, type, act;                   // P = S * k
-    int K, rows, F;                           // columns of the product's rows; its rows (F or D)
+    int K, rows, ldh;                         // columns of the product's rows; its rows; F rounded up to 8
     int lines, ns, ns_in;                     // 128-byte lines of a row, slices of them
-    int tiles;                                // of the rows
+    int tiles, wk;                            // of the rows; 2^wk warps share one (few columns)
+    Quotient by_tiles, by_grid, by_k;
     int nc, pitch;                            // columns of a chunk, bytes of one in shared memory
-    bool down;
+    bool down, aligned;                       // aligned: the tokens' rows start on 16 bytes
     // many columns: rows in f16 as prepared, their scales and sums
     const uint8_t *cols;                      // [rows][pieces][lines][16 KC]
     const float2 *info;                       // inverse scale, zero point times sum
@@ -30,13 +41,13 @@ struct MoeStream {
 
 // How a product is launched: its kernel, columns of a chunk, slices, shared memory.
 struct MoeWay {
-    int kind;                                 // 0 few columns, 1 few columns and a deep ring, 2 many columns
-    int nc, ns, pitch;
+    int kind;                                 // 0 few columns, 1 few and short ones (two blocks on an SM), 2 many columns
+    int nc, ns, pitch, warps, blocks;         // columns of a chunk, slices, bytes of a column; warps of a block, blocks on an SM
     size_t smem;
 };
 template <int FMT> MoeWay moe_way(int kind, int pieces, int S, int lines);
 
-template <int FMT> cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int grid, cudaStream_t st);
+template <int FMT> cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int n_sms, cudaStream_t st);
 // rows of the tokens, or of h, prepared for many columns
 template <int FMT> cudaError_t moe_launch_prepare(const MoeStream &p, int rows, uint8_t *cols, float2 *info, cudaStream_t st);
 

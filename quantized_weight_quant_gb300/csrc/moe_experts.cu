@@ -84,27 +84,65 @@ int kind_of(int S, int k, int E) {
     return S <= 8 || avg + 2.0 * root <= 8.0 ? 0 : 2;
 }
 
+// log2 of the warps that share a tile, of blocks with t tiles of `per` lines each:
+// the largest share of the warps' lines that is used, in rounds of warps / 2^wk
+// tiles; sharing costs a barrier and an addition per tile.
+int shared_by(int warps, double t, int per) {
+    int best = 0;
+    double most = 0.;
+    for (int wk = 0; 1 << wk <= warps && 1 << wk <= per; ++wk) {
+        const int g = warps >> wk, w = 1 << wk;
+        const double rounds = (double)((long long)(t / g + 0.999)), lines = (per + w - 1) / w * w;
+        const double used = t / ((rounds < 1. ? 1. : rounds) * g) * per / lines * (1. - (wk ? 0.02 * w : 0.));
+        if (used > most) most = used, best = wk;
+    }
+    return best;
+}
+
+// Experts that S tokens with k slots each are expected to have chosen among E.
+double chosen(int S, int k, int E) {
+    double none = 1.;
+    for (int s = 0; s < S; ++s) none *= k < E ? 1. - (double)k / E : 0.;
+    return E * (1. - none);
+}
+
 template <int FMT>
 cudaError_t run(const Moe &a, cudaStream_t st) {
     constexpr int KC = FMT == B200Q_I8 ? 16 : FMT == B200Q_I4 ? 32 : 64;
     const Experts &ex = *a.ex;
-    const int part = kMoePairs / a.k < kMoeTokens ? kMoePairs / a.k : kMoeTokens;      // tokens per launch
-    const int S = a.S < part ? a.S : part, P = S * a.k, b = a.type == B200Q_T_F32 ? 4 : 2;
+    const int b = a.type == B200Q_T_F32 ? 4 : 2;
+    int part = kMoePairs / a.k < kMoeTokens ? kMoePairs / a.k : kMoeTokens;            // tokens per launch
     const int in_lines = (int)(ex.ld_in / 128), out_lines = (int)(ex.ld_out / 128);
     const int pc_in = moe_pieces(a.type, false), pc_out = moe_pieces(a.type, true);
-    int kind = kind_of(S, a.k, ex.E);
-    MoeWay wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
-    if (kind == 1 && (wi.ns > 1 || wo.ns > 1)) {           // the deep ring is not worth slices
-        kind = 0;
+    int S = 0, P = 0, kind = 0;
+    MoeWay wi, wo;
+    for (;; part /= 2) {
+        S = a.S < part ? a.S : part, P = S * a.k, kind = kind_of(S, a.k, ex.E);
         wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
+        if (kind == 1 && (wi.ns > 1 || wo.ns > 1)) {       // two blocks on an SM are not worth slices
+            kind = 0;
+            wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
+        }
+        // tiles of all chunks are numbered in 31 bits; at kMoeMaxSize rows and columns one token's are
+        if (part == 1 || ((long long)P * wi.ns * (ex.F / 8 + 1) < 1 << 30 && (long long)P * wo.ns * (ex.D / 16 + 1) < 1 << 30)) break;
     }
-    const int grid = sm_count(ex.device);
+    const int n_sms = sm_count(ex.device);
+    auto place = [&](MoeStream &p, const MoeWay &w, int n) {
+        p.by_tiles = Quotient(p.tiles);
+        p.by_grid = Quotient(n_sms * w.blocks);
+        p.by_k = Quotient(a.k);
+        p.wk = shared_by(w.warps, chosen(n, a.k, ex.E) * w.ns * p.tiles / (n_sms * w.blocks), p.lines / w.ns);
+        p.ns = w.ns;
+        p.nc = w.nc;
+        p.pitch = w.pitch;
+    };
     void *err = nullptr;
     cudaError_t e = cudaGetSymbolAddress(&err, g_moe_err);
     if (e != cudaSuccess) return e;
+    const int ldh = (ex.F + 7) / 8 * 8;
     // h, the down sums, and for many columns the prepared rows
     auto up16 = [](size_t n) { return (n + 15) / 16 * 16; };
-    const size_t n_h = up16((size_t)wi.ns * P * (wi.ns == 1 ? 1 : 2) * ex.F * 4), n_part = up16((size_t)wo.ns * P * ex.D * 4);
+    const size_t n_h = up16((size_t)wi.ns * P * (wi.ns == 1 ? 1 : 2) * ldh * 4), n_part = up16((size_t)wo.ns * P * ex.D * 4);
     const size_t n_x = kind == 2 ? (size_t)S * pc_in * in_lines * 16 * KC : 0, n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * 16 * KC : 0;
     const size_t n_info = kind == 2 ? up16((size_t)P * 8) : 0;
     uint8_t *ws = nullptr;
@@ -130,16 +168,17 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.type = a.type;
         p.act = a.act;
         p.K = ex.D;
-        p.rows = p.F = ex.F;
+        p.rows = ex.F;
+        p.ldh = ldh;
+        p.aligned = (uintptr_t)p.x % 16 == 0 && a.ldx * b % 16 == 0;
         p.lines = in_lines;
-        p.ns = p.ns_in = wi.ns;
+        p.ns_in = wi.ns;
         p.tiles = (int)((ex.F + 7ll) / 8);
-        p.nc = wi.nc;
-        p.pitch = wi.pitch;
+        place(p, wi, n);
         p.cols = cols;
         p.info = info;
         if (kind == 2) e = moe_launch_prepare<FMT>(p, n, cols, info, st);
-        if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wi, grid, st);
+        if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wi, n_sms, st);
         if (e != cudaSuccess) break;
         p.down = true;
         p.out = sums;
@@ -147,12 +186,10 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.K = ex.F;
         p.rows = ex.D;
         p.lines = out_lines;
-        p.ns = wo.ns;
         p.tiles = (int)((ex.D + 15ll) / 16);
-        p.nc = wo.nc;
-        p.pitch = wo.pitch;
+        place(p, wo, n);
         if (kind == 2) e = moe_launch_prepare<FMT>(p, p.P, cols, info, st);
-        if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wo, grid, st);
+        if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wo, n_sms, st);
         if (e != cudaSuccess) break;
         Sum q{sums, p.ids, a.wts + (long long)s0 * a.k, a.res ? (const char *)a.res + s0 * a.ldr * b : nullptr,
               (char *)a.y + s0 * a.ldy * b, a.ldr, a.ldy, p.P, a.k, ex.E, ex.D, wo.ns, a.type};

@@ -19,6 +19,18 @@ constexpr int kRedPitch = 20;                 // floats of a column's 16 sums in
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Codes pass through L2 once: they go first when room is needed, so that what a
+// call reads again (activations, and the kernels' own instructions) stays.
+__device__ __forceinline__ uint64_t stream_policy() {
+    uint64_t r;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
+    return r;
+}
+__device__ __forceinline__ void copy16_stream(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---------------------------------------------------------------- plan
 // The slots in the order of their experts, in chunks of at most nc columns.
 struct Plan {
@@ -36,15 +48,36 @@ struct PlanScratch {
 // Ends with a barrier.
 __device__ __forceinline__ void make_plan(const MoeStream &p, Plan &pl, PlanScratch &sc) {
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int e = tid; e < p.E; e += blockDim.x) sc.count[e] = 0;
-    for (int i = tid; i < p.P; i += blockDim.x) {
-        int e = p.ids[i];
-        if (e < -1 || e >= p.E) {
-            if (!p.down && blockIdx.x == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_EINVAL));
-            e = -1;
+    auto expert_of = [&](int i) {
+        const int e = p.ids[i];
+        if (e >= 0 && e < p.E) return e;
+        if (e != -1 && !p.down && blockIdx.x == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_EINVAL));
+        return -1;
+    };
+    if (p.P <= 32) {                           // one warp, no scratch
+        if (tid < 32) {
+            const int e = lane < p.P ? expert_of(lane) : -1;
+            const unsigned same = __match_any_sync(kAll, e);
+            const int c = __popc(same), rank = __popc(same & ((1u << lane) - 1)), m = e >= 0 && rank == 0 ? (c + p.nc - 1) / p.nc : 0;
+            int place = 0, chunk = 0;          // slots and chunks of lower experts
+            for (int t = 0; t < p.P; ++t) {
+                const int et = __shfl_sync(kAll, e, t), mt = __shfl_sync(kAll, m, t);
+                if (et >= 0 && et < e) ++place, chunk += mt;
+            }
+            if (e >= 0) pl.order[place + rank] = (unsigned short)lane;
+            for (int j = 0; j < m; ++j) {
+                pl.expert[chunk + j] = (unsigned short)e;
+                pl.first[chunk + j] = (unsigned short)(place + j * p.nc);
+                pl.n[chunk + j] = (unsigned char)min(p.nc, c - j * p.nc);
+            }
+            const int chunks = __reduce_add_sync(kAll, m);
+            if (lane == 0) pl.chunks = chunks;
         }
-        sc.id[i] = (short)e;
+        __syncthreads();
+        return;
     }
+    for (int e = tid; e < p.E; e += blockDim.x) sc.count[e] = 0;
+    for (int i = tid; i < p.P; i += blockDim.x) sc.id[i] = (short)expert_of(i);
     __syncthreads();
     if (tid < 32) {
         // ranks in the order of the slots
@@ -89,74 +122,99 @@ __device__ __forceinline__ void make_plan(const MoeStream &p, Plan &pl, PlanScra
 }
 
 // ---------------------------------------------------------------- columns
+// What runs once per block is kept small: its instructions come from memory, and
+// that is most of what they cost (columns staged by code with every type and
+// alignment inlined and unrolled: 8 us a product, this 1 us).
+
 template <class T> __device__ __forceinline__ float as_float(T v);
 template <> __device__ __forceinline__ float as_float<float>(float v) { return v; }
 template <> __device__ __forceinline__ float as_float<__half>(__half v) { return __half2float(v); }
 template <> __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Eight values of a row from column c on, 0 past the row.
-template <class T>
-__device__ __forceinline__ void row8(const T *r, int c, int K, float (&v)[8]) {
-    union {
-        uint4 q[sizeof(T) / 2];
-        T e[8];
-    } u;
-    if (c + 8 <= K && (uintptr_t)(r + c) % 16 == 0) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u.q[i] = reinterpret_cast<const uint4 *>(r + c)[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = as_float<T>(u.e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < K ? as_float<T>(r[c + i]) : 0.f;
+// Where a product's columns come from: eight values of a slot's column from c on,
+// 0 from K on, and where they are.  The tokens' rows:
+template <class T> struct TokenRows {
+    static __device__ __forceinline__ const void *at(const MoeStream &p, int slot, int c) {
+        return (const T *)p.x + (long long)p.by_k(slot) * p.ldx + c;
     }
-}
-
-// Eight values of slot `slot`'s column of the product from column c on: of its
-// token's row, or h, or act(gate) * up from the slices' sums.
-__device__ __forceinline__ void column8(const MoeStream &p, int slot, int c, float (&v)[8]) {
-    if (!p.down) {
-        const long long at = (long long)(slot / p.k) * p.ldx;
-        if (p.type == B200Q_T_F32) row8((const float *)p.x + at, c, p.K, v);
-        else if (p.type == B200Q_T_F16) row8((const __half *)p.x + at, c, p.K, v);
-        else row8((const __nv_bfloat16 *)p.x + at, c, p.K, v);
-        return;
-    }
-    if (p.ns_in == 1) {
-        row8(p.in + (long long)slot * p.F, c, p.F, v);
-        return;
-    }
-    float u[8];
+    static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
+        const T *r = (const T *)at(p, slot, c);
+        if (p.aligned && c + 8 <= p.K) {
+            union {
+                uint4 q[sizeof(T) / 2];
+                T e[8];
+            } u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
-    for (int s = 0; s < p.ns_in; ++s) {
-        const float *g = p.in + ((long long)s * p.P + slot) * 2 * p.F;
-        float a[8], b[8];
-        row8(g, c, p.F, a);
-        row8(g + p.F, c, p.F, b);
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) u.q[i] = reinterpret_cast<const uint4 *>(r)[i];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += a[i], u[i] += b[i];
+            for (int i = 0; i < 8; ++i) v[i] = as_float<T>(u.e[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < p.K ? as_float<T>(r[i]) : 0.f;
+        }
     }
+};
+// h, in rows of ldh floats, a multiple of 8:
+struct GatedRows {
+    static __device__ __forceinline__ const void *at(const MoeStream &p, int slot, int c) {
+        return p.in + (long long)slot * p.ldh + c;
+    }
+    static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        if (c < p.K) {
+            const float4 *r = reinterpret_cast<const float4 *>(at(p, slot, c));
+            a = r[0], b = r[1];
+        }
+        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_q8(v[i], p.act) * u[i];
-}
+        for (int i = 0; i < 8; ++i) v[i] = c + i < p.K ? w[i] : 0.f;   // what is behind the row is not h
+    }
+};
+// act(gate) * up of the slices' sums, [ns_in][P][2][ldh]:
+struct SlicedRows {
+    static __device__ __forceinline__ const void *at(const MoeStream &p, int slot, int c) {
+        return p.in + (long long)slot * 2 * p.ldh + c;
+    }
+    static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            float a = 0.f, b = 0.f;
+            if (c + i < p.K)
+                for (int s = 0; s < p.ns_in; ++s) {
+                    const float *g = p.in + ((long long)s * p.P + slot) * 2 * p.ldh + c + i;
+                    a += g[0], b += g[p.ldh];
+                }
+            a = act_q8(a, p.act) * b;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i == j) v[j] = a;
+        }
+    }
+};
 
 // The power of two that brings a column's largest magnitude (its bits) to
 // [2^14, 2^15); at most 2^126, so that the inverse is a normal number.
 __device__ __forceinline__ int exponent_for(unsigned top) { return top ? min(126, 14 + 127 - (int)(top >> 23)) : 0; }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((unsigned)(127 + e) << 23); }
 
+__device__ __forceinline__ unsigned largest(const float (&v)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));     // a NaN shows in the products
+    return __float_as_uint(m);
+}
+
 // Unit u of a column: the eight values whose 16 bytes stand side by side for
 // the instructions, and where they do.  Per 64 bytes of codes a column has KC / 8
 // pieces of 64 bytes, 16 of them for each of the four threads that share a row.
-template <int FMT>
+template <int FMT, class Src>
 __device__ __forceinline__ void unit8(const MoeStream &p, int slot, int k0, int u, float (&v)[8]) {
     if constexpr (FMT == B200Q_I2) {
         // a word is 16 codes: the values that its instructions 2j, 2j+1 take, j = u & 1
         const int c = k0 + 16 * (u >> 1), j = u & 1;
         float lo[8], hi[8];
-        column8(p, slot, c, lo);
-        column8(p, slot, c + 8, hi);
+        Src::load(p, slot, c, lo);
+        Src::load(p, slot, c + 8, hi);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             v[4 * t] = j ? lo[2 + t] : lo[t];
@@ -165,7 +223,7 @@ __device__ __forceinline__ void unit8(const MoeStream &p, int slot, int k0, int 
             v[4 * t + 3] = j ? hi[6 + t] : hi[4 + t];
         }
     } else {
-        column8(p, slot, k0 + 8 * u, v);
+        Src::load(p, slot, k0 + 8 * u, v);
     }
 }
 template <int FMT>
@@ -181,28 +239,30 @@ __device__ __forceinline__ int unit_at(int u) {
 // (odd units of int2), and are divided by 2^b for a field at bit b.
 template <int FMT, int PC, bool RAW>
 __device__ __forceinline__ float split(const float (&v)[8], float scale, int u, uint4 &hi, uint4 &rest) {
-    __half h[8], l[8];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float f = v[i] * scale;
-        h[i] = __float2half_rn(f);
-        l[i] = __float2half_rn(f - __half2float(h[i]));
-        sum += __half2float(h[i]) + (PC == 2 ? __half2float(l[i]) : 0.f);
-    }
     const float d0 = RAW && FMT == B200Q_I2 && (u & 1) ? 1.f / 16.f : 1.f;
     const float d1 = RAW ? d0 / (float)(1 << kShift<FMT>) : 1.f;
-    auto pack = [](__half a, __half b, float by) {
-        const __half2 m = RAW ? __hmul2(__halves2half2(a, b), __float2half2_rn(by)) : __halves2half2(a, b);
-        return *reinterpret_cast<const uint32_t *>(&m);
-    };
-    if constexpr (FMT == B200Q_I4) {           // pairs (0,4) (2,6) (1,5) (3,7)
-        hi = make_uint4(pack(h[0], h[4], d0), pack(h[2], h[6], d0), pack(h[1], h[5], d1), pack(h[3], h[7], d1));
-        rest = make_uint4(pack(l[0], l[4], d0), pack(l[2], l[6], d0), pack(l[1], l[5], d1), pack(l[3], l[7], d1));
-    } else {
-        hi = make_uint4(pack(h[0], h[1], d0), pack(h[2], h[3], d0), pack(h[4], h[5], d1), pack(h[6], h[7], d1));
-        rest = make_uint4(pack(l[0], l[1], d0), pack(l[2], l[3], d0), pack(l[4], l[5], d1), pack(l[6], l[7], d1));
+    constexpr int kOrder[8] = {0, FMT == B200Q_I4 ? 4 : 1, 2, FMT == B200Q_I4 ? 6 : 3,
+                               FMT == B200Q_I4 ? 1 : 4, 5, FMT == B200Q_I4 ? 3 : 6, 7};
+    uint32_t h[4], l[4];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[kOrder[2 * i]] * scale, b = v[kOrder[2 * i + 1]] * scale, d = i < 2 ? d0 : d1;
+        const __half2 t = __floats2half2_rn(a, b);
+        const float2 f = __half22float2(t);
+        sum += f.x + f.y;
+        const __half2 hd = RAW ? __hmul2(t, __float2half2_rn(d)) : t;
+        h[i] = *reinterpret_cast<const uint32_t *>(&hd);
+        if constexpr (PC == 2) {
+            const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+            const float2 rf = __half22float2(r);
+            sum += rf.x + rf.y;
+            const __half2 rd = RAW ? __hmul2(r, __float2half2_rn(d)) : r;
+            l[i] = *reinterpret_cast<const uint32_t *>(&rd);
+        }
     }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    if constexpr (PC == 2) rest = make_uint4(l[0], l[1], l[2], l[3]);
     return sum;
 }
 
@@ -225,10 +285,10 @@ __device__ __forceinline__ void put(const MoeStream &p, int slice, int slot, int
         const int f = tile * 8 + r;
         if (f >= p.rows) return;
         if (p.ns == 1) {
-            p.out[at * p.rows + f] = act_q8(a, p.act) * b;
+            p.out[at * p.ldh + f] = act_q8(a, p.act) * b;
         } else {
-            p.out[at * 2 * p.rows + f] = a;
-            p.out[(at * 2 + 1) * p.rows + f] = b;
+            p.out[at * 2 * p.ldh + f] = a;
+            p.out[(at * 2 + 1) * p.ldh + f] = b;
         }
     }
 }
@@ -296,7 +356,7 @@ __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], int n, F
 
 // ---------------------------------------------------------------- few columns
 // Up to 8 columns of an expert, resident in shared memory.
-constexpr int kFewWarps = 16, kFewColumns = 8;
+constexpr int kFewColumns = 8;
 
 struct FewColumns {
     unsigned top[kFewColumns];                 // the largest magnitude
@@ -304,11 +364,11 @@ struct FewColumns {
     float part[512];                           // sums of 32 units each
 };
 
-// AHEAD: lines in a warp's ring.
-template <int AHEAD> struct FewShape {
-    static constexpr int kRing = kFewWarps * AHEAD * 2048;
+// W: warps of a block; AHEAD: lines in a warp's ring.
+template <int W, int AHEAD> struct FewShape {
+    static constexpr int kRing = W * AHEAD * 2048;
     static constexpr int kRedTile = kFewColumns * kRedPitch;           // floats of a warp's tile
-    static constexpr int kRed = 2 * kFewWarps * kRedTile * 4;          // two sets, used in turn; the plan's scratch before
+    static constexpr int kRed = 2 * W * kRedTile * 4;                  // two sets, used in turn; the plan's scratch before
     static constexpr int kColumnsAt = kRing + kRed;
     static constexpr int kPlanAt = kColumnsAt + (int)sizeof(FewColumns);
     static constexpr int kB = (kPlanAt + (int)sizeof(Plan) + 127) / 128 * 128;
@@ -316,57 +376,58 @@ template <int AHEAD> struct FewShape {
 };
 
 // The columns of a chunk, lines l0 .. l1-1, into shared memory.  A warp takes 32
-// units of a column at a time.  Called by the whole block; ends with a barrier.
-template <int FMT, int PC, bool RAW>
-__device__ __forceinline__ void stage(const MoeStream &p, const unsigned short *order, int n, int l0, int l1, uint8_t *B,
-                                      FewColumns &cl) {
+// units of a column at a time: first for its largest magnitude, then again to
+// scale it.  Called by the whole block; ends with a barrier.
+template <int FMT, int PC, bool RAW, class Src>
+__device__ __forceinline__ void stage_from(const MoeStream &p, const unsigned short *order, int n, int l0, int l1, uint8_t *B,
+                                        FewColumns &cl) {
     constexpr int KC = Fmt<FMT>::KC;
     const int units = (l1 - l0) * KC;          // of a column: KC to a line
-    const int k0 = l0 * 8 * KC;
-    const int blocks = (units + 31) / 32, all = n * blocks;
+    const int k0 = l0 * 8 * KC, width = (units + 31) & ~31;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x < kFewColumns) cl.top[threadIdx.x] = 0u;
-    __syncthreads();
-#pragma unroll 2
-    for (int b = warp; b < all; b += kFewWarps) {
-        const int c = b / blocks, u = (b - c * blocks) * 32 + lane;
-        unsigned m = 0;
-        if (u < units) {
-            float v[8];
-            column8(p, order[c], k0 + 8 * u, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {     // 0: all loads under way at once
+        int b = warp;
+#pragma unroll 1
+        for (int c = 0, u = (int)threadIdx.x; c < n; u += blockDim.x, b += blockDim.x >> 5) {
+#pragma unroll 1
+            while (u >= width && c < n) u -= width, ++c;
+            if (c == n) break;
+            const int slot = order[c];
+            if (pass == 0) {
+                if (k0 + 8 * u < p.K) asm volatile("prefetch.global.L1 [%0];" ::"l"(Src::at(p, slot, k0 + 8 * u)));
+                continue;
+            }
+            float v[8] = {}, sum = 0.f;
+            if (u < units) unit8<FMT, Src>(p, slot, k0, u, v);
+            if (pass == 1) {
+                const unsigned m = __reduce_max_sync(kAll, largest(v));
+                if (lane == 0) atomicMax(&cl.top[c], m);
+                continue;
+            }
+            if (u < units) {
+                uint4 hi, rest;
+                sum = split<FMT, PC, RAW>(v, power(exponent_for(cl.top[c])), u, hi, rest);
+                uint8_t *to = B + c * p.pitch + unit_at<FMT>(u);
+                *reinterpret_cast<uint4 *>(to) = hi;
+                if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + p.nc * p.pitch) = rest;
+            }
+            if constexpr (RAW) {
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+                if (lane == 0) cl.part[b] = sum;
+            }
         }
-        m = __reduce_max_sync(kAll, m);
-        if (lane == 0) atomicMax(&cl.top[c], m);
+        __syncthreads();
     }
-    __syncthreads();
-#pragma unroll 2
-    for (int b = warp; b < all; b += kFewWarps) {
-        const int c = b / blocks, u = (b - c * blocks) * 32 + lane;
-        const float scale = power(exponent_for(cl.top[c]));
-        float sum = 0.f;
-        if (u < units) {
-            float v[8];
-            uint4 hi, rest;
-            unit8<FMT>(p, order[c], k0, u, v);
-            sum = split<FMT, PC, RAW>(v, scale, u, hi, rest);
-            uint8_t *to = B + c * p.pitch + unit_at<FMT>(u);
-            *reinterpret_cast<uint4 *>(to) = hi;
-            if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + p.nc * p.pitch) = rest;
-        }
-        if constexpr (RAW) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            if (lane == 0) cl.part[b] = sum;
-        }
-    }
-    __syncthreads();
     if (warp < n) {
         float sum = 0.f;
         if constexpr (RAW) {
+            const int blocks = width / 32;
+#pragma unroll 1
             for (int b = lane; b < blocks; b += 32) sum += cl.part[warp * blocks + b];
-#pragma unroll
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
         }
         if (lane == 0) {
@@ -377,24 +438,23 @@ __device__ __forceinline__ void stage(const MoeStream &p, const unsigned short *
     __syncthreads();
 }
 
-// Warps that share a tile, of a block that has t tiles of `per` lines: the share
-// of the warps' lines that are used, in rounds of 16 / wk tiles; sharing costs a
-// barrier and an addition per tile.
-__device__ __forceinline__ int warps_per_tile(float t, int per) {
-    int best = 1;
-    float most = 0.f;
-    for (int wk = 1; wk <= kFewWarps && wk <= per; wk *= 2) {
-        const float g = (float)(kFewWarps / wk);
-        const float used = t / (ceilf(t / g) * g) * (float)per / (float)((per + wk - 1) / wk * wk) *
-                           (1.f - 0.02f * (float)(wk > 1 ? wk : 0));
-        if (used > most) most = used, best = wk;
+template <int FMT, int PC, bool RAW>
+__device__ __forceinline__ void stage(const MoeStream &p, const unsigned short *order, int n, int l0, int l1, uint8_t *B,
+                                      FewColumns &cl) {
+    if (p.down) {
+        if (p.ns_in == 1) stage_from<FMT, PC, RAW, GatedRows>(p, order, n, l0, l1, B, cl);
+        else stage_from<FMT, PC, RAW, SlicedRows>(p, order, n, l0, l1, B, cl);
+    } else if constexpr (!RAW) {
+        stage_from<FMT, PC, RAW, TokenRows<float>>(p, order, n, l0, l1, B, cl);
+    } else if constexpr (PC == 1) {            // with two pieces 16-bit rows are only h
+        if (p.type == B200Q_T_F16) stage_from<FMT, PC, RAW, TokenRows<__half>>(p, order, n, l0, l1, B, cl);
+        else stage_from<FMT, PC, RAW, TokenRows<__nv_bfloat16>>(p, order, n, l0, l1, B, cl);
     }
-    return best;
 }
 
-template <int FMT, int PC, bool RAW, int AHEAD>
-__global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid_constant__ MoeStream p) {
-    using Sh = FewShape<AHEAD>;
+template <int FMT, int PC, bool RAW, int W, int AHEAD>
+__global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_constant__ MoeStream p) {
+    using Sh = FewShape<W, AHEAD>;
     constexpr int KC = Fmt<FMT>::KC;
     extern __shared__ __align__(128) uint8_t smem[];
     float *red = reinterpret_cast<float *>(smem + Sh::kRing);
@@ -403,23 +463,30 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid
     uint8_t *B = smem + Sh::kB;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
 
+    // Addresses that the kernel will wait for one after the other, asked for
+    // together: their pages have to be found.
+    if (tid == 0) prefetch(p.ids);
+    if (tid == 32) prefetch(p.table);
+    if (tid == 64) prefetch(p.down ? (const void *)p.in : p.x);
+    if (tid == 96) prefetch(p.out);
     // The ids may come from the kernel before gate and up; down follows them, and
     // they were there when gate and up began.
     if (!p.down) dependency_wait();
     make_plan(p, pl, *reinterpret_cast<PlanScratch *>(red));
-    const long long all = (long long)pl.chunks * p.ns * p.tiles;
-    const long long lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
-    const int wk = warps_per_tile((float)all / (float)gridDim.x, p.lines / p.ns);
-    const int kw = warp % wk, wm = warp / wk, groups = kFewWarps / wk;
+    // an even run of the tiles; their number is below 2^31
+    const int all = pl.chunks * p.ns * p.tiles, each = p.by_grid(all), more = all - each * (int)gridDim.x;
+    const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
+    const int wk = 1 << p.wk, kw = warp & (wk - 1), groups = W >> p.wk, wm = warp >> p.wk;
+    auto first_line = [&](int slice) { return p.ns == 1 ? (slice ? p.lines : 0) : (int)((long long)slice * p.lines / p.ns); };
 
     // the copy cursor: this warp's next line
-    const long long first_end = (lo / p.tiles + 1) * p.tiles;
-    long long fu = lo + wm, fend = hi < first_end ? hi : first_end;         // its tile, the end of its slice's
-    int fcs = (int)(lo / p.tiles), fchunk = -1, fline = 0, fl1 = 0, fslot = 0;
+    int fcs = p.by_tiles(lo), fu = lo + wm, fend = min(hi, (fcs + 1) * p.tiles);     // its slice's number, tile, end of the tiles
+    int fchunk = -1, fline = 0, fl1 = 0, fslot = 0;
     const uint8_t *rows0 = nullptr, *rows1 = nullptr;                       // rows g and g + 8 of tile 0
     const uint8_t *f0 = nullptr, *f1 = nullptr;                             // the next line of the cursor's
     const long long tile_bytes = (p.down ? 16 : 8) * p.ld;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (AHEAD * 2048) + lane * 16;
+    const uint64_t policy = stream_policy();
     const int step = wk * 128;
     auto open = [&]() {                        // the cursor's tile, or a later one that has a line for this warp
         while (true) {
@@ -427,12 +494,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid
                 if (fend >= hi) return;        // none is left
                 ++fcs;
                 fu = fend + wm;
-                fend = hi < fend + p.tiles ? hi : fend + p.tiles;
+                fend = min(hi, fend + p.tiles);
                 continue;
             }
             const int c = p.ns == 1 ? fcs : fcs / p.ns, sl = fcs - c * p.ns;
-            fline = (int)((long long)sl * p.lines / p.ns) + kw;
-            fl1 = (int)((long long)(sl + 1) * p.lines / p.ns);
+            fline = first_line(sl) + kw;
+            fl1 = first_line(sl + 1);
             if (fline >= fl1) {
                 fu += groups;
                 continue;
@@ -443,7 +510,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid
                 rows1 = (p.down ? e.codes[2] + 8 * p.ld : e.codes[1]) + g * p.ld + tig * 16;
                 fchunk = c;
             }
-            const long long off = (fu - (long long)fcs * p.tiles) * tile_bytes + fline * 128;
+            const long long off = (fu - fcs * p.tiles) * tile_bytes + fline * 128;
             f0 = rows0 + off;
             f1 = rows1 + off;
             return;
@@ -452,10 +519,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid
     auto copy_line = [&]() {
         if (fu < fend) {
             const uint32_t to = ring + fslot * 2048;
-            copy16(to, f0);
-            copy16(to + 512, f1);
-            copy16(to + 1024, f0 + 64);
-            copy16(to + 1536, f1 + 64);
+            copy16_stream(to, f0, policy);
+            copy16_stream(to + 512, f1, policy);
+            copy16_stream(to + 1024, f0 + 64, policy);
+            copy16_stream(to + 1536, f1 + 64, policy);
             f0 += step;
             f1 += step;
             if (++fslot == AHEAD) fslot = 0;
@@ -466,33 +533,39 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid
         }
         asm volatile("cp.async.commit_group;" ::: "memory");           // empty at the end: the waits count groups
     };
-    open();
-#pragma unroll 1
-    for (int i = 0; i < AHEAD; ++i) copy_line();
-
-    if (p.down) dependency_wait();
-    let_dependents_start();
 
     const uint8_t *slots = smem + warp * (AHEAD * 2048) + lane * 16;
     const int colat = min(g, p.nc - 1) * p.pitch + tig * 16;           // a column past the chunk's is computed and not stored
-    int slot = 0, set = 0;
-    for (long long u0 = lo; u0 < hi;) {        // the block's tiles of one slice
-        const int cs = (int)(u0 / p.tiles), c = cs / p.ns, slice = cs - c * p.ns;
-        const long long base = (long long)cs * p.tiles, u1 = hi < base + p.tiles ? hi : base + p.tiles;
-        const int l0 = (int)((long long)slice * p.lines / p.ns), l1 = (int)((long long)(slice + 1) * p.lines / p.ns);
+    int slot = 0, set = 0, cs = fcs;
+    // Down fills its ring while gate and up end.  Gate and up ask for their first
+    // columns before the codes, which keep the memory busy for a while.
+    bool filled = p.down;
+    if (p.down) {
+        open();
+#pragma unroll 1
+        for (int i = 0; i < AHEAD; ++i) copy_line();
+        dependency_wait();
+    }
+    let_dependents_start();
+    for (int u0 = lo; u0 < hi; ++cs) {         // the block's tiles of one slice of one chunk
+        const int c = p.ns == 1 ? cs : cs / p.ns, slice = cs - c * p.ns;
+        const int base = cs * p.tiles, u1 = min(hi, base + p.tiles), l0 = first_line(slice), l1 = first_line(slice + 1);
         const unsigned short *order = pl.order + pl.first[c];
         const int n = pl.n[c];
+        __syncthreads();                       // the columns before are read, and the plan's scratch
+        stage<FMT, PC, RAW>(p, order, n, l0, l1, B, cl);
+        if (!filled) {
+            open();
+#pragma unroll 1
+            for (int i = 0; i < AHEAD; ++i) copy_line();
+            filled = true;
+        }
         const Expert &e = p.table[pl.expert[c]];
         const float *s0 = p.down ? e.scales[2] : e.scales[0], *s1 = p.down ? e.scales[2] + 8 : e.scales[1];
-        __syncthreads();                       // the columns before are read
-        stage<FMT, PC, RAW>(p, order, n, l0, l1, B, cl);
         const int r = wk == 1 ? g : tid & 7;
-        auto finish = [&](int tile, int col, float a, float b, float sa, float sb) {
-            const float un = cl.unscale[col], z = cl.zero[col];
-            put(p, slice, order[col], tile, r, product<RAW>(a, z, sa, un), product<RAW>(b, z, sb, un));
-        };
-        for (long long u = u0 + wm; u < u1; u += groups) {
-            const int tile = (int)(u - base);
+#pragma unroll 1
+        for (int u = u0 + wm; u < u1; u += groups) {
+            const int tile = u - base;
             // the scales of rows r and r + 8, fetched now, used at the end; rows past the last have scale 0
             const float sa = s0[tile * (p.down ? 16 : 8) + r], sb = s1[tile * (p.down ? 16 : 8) + r];
             float sum[1][1][4] = {};
@@ -500,36 +573,47 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) moe_few_kernel(const __grid
 #pragma unroll 1
             for (int line = l0 + kw; line < l1; line += wk, xb += wk * (16 * KC)) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
-                uint4 q[2][1][2];              // [64 bytes][tile][row half]
+                const uint8_t *from = slots + slot * 2048;
+                uint4 q[1][2], next[1][2];     // [tile][row half]
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i >> 1][0][i & 1] = *reinterpret_cast<const uint4 *>(slots + slot * 2048 + i * 512);
+                for (int i = 0; i < 2; ++i) {
+                    q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 512);
+                    next[0][i] = *reinterpret_cast<const uint4 *>(from + 1024 + i * 512);
+                }
                 if (++slot == AHEAD) slot = 0;
                 copy_line();                   // into the slot just read: this thread's own
                 float acc[1][1][4] = {}, rest[1][1][4] = {};
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    chunk_products<FMT, 1, 1, PC, RAW>(q[half], n, [&](int) { return xb + half * (8 * KC); }, p.nc * p.pitch, sum, acc,
-                                                       rest);
+                const uint8_t *xh = xb;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half, xh += 8 * KC) {
+                    chunk_products<FMT, 1, 1, PC, RAW>(q, n, [&](int) { return xh; }, p.nc * p.pitch, sum, acc, rest);
+                    q[0][0] = next[0][0], q[0][1] = next[0][1];
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[0][0][i] += PC == 2 ? rest[0][0][i] : acc[0][0][i];
             }
-            const float (&s)[4] = sum[0][0];
-            if (wk == 1) {
-                if (2 * tig < n) finish(tile, 2 * tig, s[0], s[2], sa, sb);
-                if (2 * tig + 1 < n) finish(tile, 2 * tig + 1, s[1], s[3], sa, sb);
-            } else {
+            float a0 = sum[0][0][0], b0 = sum[0][0][2], a1 = sum[0][0][1], b1 = sum[0][0][3];
+            int col = 2 * tig, stride = 1;     // the columns that this thread writes, row r of the tile: at most two if wk = 1
+            const float *part = red + (set * W + wm * wk) * Sh::kRedTile + r;
+            if (wk > 1) {
                 // [column][row] of this warp's part, added over the tile's warps in order; the two sets
                 // take turns, so that one barrier per tile is enough
-                float *to = red + (set * kFewWarps + warp) * Sh::kRedTile + 2 * tig * kRedPitch + g;
-                to[0] = s[0], to[kRedPitch] = s[1], to[8] = s[2], to[kRedPitch + 8] = s[3];
+                float *to = red + (set * W + warp) * Sh::kRedTile + 2 * tig * kRedPitch + g;
+                to[0] = a0, to[kRedPitch] = a1, to[8] = b0, to[kRedPitch + 8] = b1;
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + wm), "r"(wk * 32) : "memory");
-                for (int col = (kw * 32 + lane) >> 3; col < n; col += wk * 4) {
-                    const float *from = red + (set * kFewWarps + wm * wk) * Sh::kRedTile + col * kRedPitch + r;
-                    float a = 0.f, b = 0.f;
-                    for (int w = 0; w < wk; ++w) a += from[w * Sh::kRedTile], b += from[w * Sh::kRedTile + 8];
-                    finish(tile, col, a, b, sa, sb);
-                }
+                col = (kw * 32 + lane) >> 3, stride = wk * 4;
                 set ^= 1;
+            }
+            const int end = wk > 1 ? n : min(n, col + 2);
+#pragma unroll 1
+            for (; col < end; col += stride) {
+                if (wk > 1) {
+                    a0 = b0 = 0.f;
+                    for (int w = 0; w < wk; ++w) a0 += part[col * kRedPitch + w * Sh::kRedTile], b0 += part[col * kRedPitch + w * Sh::kRedTile + 8];
+                }
+                const float un = cl.unscale[col], z = cl.zero[col];
+                put(p, slice, order[col], tile, r, product<RAW>(a0, z, sa, un), product<RAW>(b0, z, sb, un));
+                a0 = a1, b0 = b1;
             }
         }
         u0 = u1;
@@ -555,7 +639,7 @@ template <int FMT, int PC> struct ManyShape {
 
 // A row of the tokens, or of h, per block, as pieces of f16 in the order of the
 // instructions; what the sums need of it to info.
-template <int FMT, int PC, bool RAW>
+template <int FMT, int PC, bool RAW, class Src>
 __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant__ MoeStream p, uint8_t *cols, float2 *info) {
     constexpr int KC = Fmt<FMT>::KC;
     __shared__ unsigned tops[8];
@@ -569,28 +653,31 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
     }
     const int slot = p.down ? row : row * p.k, units = p.lines * KC;
     unsigned m = 0;
-#pragma unroll 2
-    for (int u = threadIdx.x; u < units; u += 256) {
-        float v[8];
-        column8(p, slot, 8 * u, v);
+#pragma unroll 1
+    for (int u0 = threadIdx.x; u0 < units; u0 += 3 * 256) {
+        float v[3][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 3; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+            if (u0 + i * 256 < units) Src::load(p, slot, 8 * (u0 + i * 256), v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) m = max(m, largest(v[i]));
     }
     m = __reduce_max_sync(kAll, m);
     if (lane == 0) tops[warp] = m;
     __syncthreads();
-    m = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, tops[w]);
+    m = __reduce_max_sync(kAll, tops[lane & 7]);
     const int up = exponent_for(m);
     const float scale = power(up);
     uint8_t *to = cols + (long long)row * PC * p.lines * (16 * KC);
     float sum = 0.f;
-#pragma unroll 2
+#pragma unroll 1
     for (int u = threadIdx.x; u < units; u += 256) {
         float v[8];
         uint4 hi, rest;
-        unit8<FMT>(p, slot, 0, u, v);
+        unit8<FMT, Src>(p, slot, 0, u, v);
         sum += split<FMT, PC, RAW>(v, scale, u, hi, rest);
         *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u)) = hi;
         if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * (16 * KC) + unit_at<FMT>(u)) = rest;
@@ -601,6 +688,7 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
     __syncthreads();
     if (threadIdx.x == 0) {
         sum = 0.f;
+#pragma unroll 1
         for (int w = 0; w < 8; ++w) sum += sums[w];
         info[row] = make_float2(power(-up), RAW ? sum * kZeroPoint<FMT> : 0.f);
     }
@@ -620,26 +708,24 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
     dependency_wait();
     let_dependents_start();
     const int units = (p.tiles + 1) / 2;       // pairs of tiles
-    const long long all = (long long)pl.chunks * units;
-    const long long lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+    const int all = pl.chunks * units, each = p.by_grid(all), more = all - each * (int)gridDim.x;
+    const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
 
     // A round: up to 8 units of one chunk, a warp each, over the whole length of
     // the rows.  A chunk's rounds share its units evenly.
     struct Round {
-        long long u, end;                      // the first unit, the end of the block's in this chunk
-        int c, n;                              // chunk; units
+        int u, c, n;                           // the first unit, its chunk, units
     };
-    auto begin = [&](Round &r, long long u) {
+    auto begin = [&](Round &r, int u) {
         r.u = u;
         r.n = 0;
         if (u >= hi) return;
-        r.c = (int)(u / units);
-        const long long last = (long long)(r.c + 1) * units;
-        r.end = hi < last ? hi : last;
-        const int left = (int)(r.end - u), rounds = (left + kManyWarps - 1) / kManyWarps;
+        r.c = u / units;
+        const int left = min(hi, (r.c + 1) * units) - u, rounds = (left + kManyWarps - 1) / kManyWarps;
         r.n = (left + rounds - 1) / rounds;
     };
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    const uint64_t policy = stream_policy();
     const long long tile_bytes = (p.down ? 16 : 8) * p.ld, row_bytes = (long long)PC * p.lines * (16 * KC);
 
     // the copy cursor
@@ -654,7 +740,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         fn = pl.n[f.c];
         if (warp < f.n) {
             const Expert &e = p.table[pl.expert[f.c]];
-            const int tile = (int)(f.u + warp - (long long)f.c * units) * 2;
+            const int tile = (f.u + warp - f.c * units) * 2;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {      // a tile past the last reads the last again
                 const long long off = min(tile + m, p.tiles - 1) * tile_bytes + g * p.ld + tig * 16;
@@ -670,17 +756,17 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const uint32_t t = to + warp * 4096 + m * 2048 + lane * 16;
-                    copy16(t, f0[m]);
-                    copy16(t + 512, f1[m]);
-                    copy16(t + 1024, f0[m] + 64);
-                    copy16(t + 1536, f1[m] + 64);
+                    copy16_stream(t, f0[m], policy);
+                    copy16_stream(t + 512, f1[m], policy);
+                    copy16_stream(t + 1024, f0[m] + 64, policy);
+                    copy16_stream(t + 1536, f1[m] + 64, policy);
                     f0[m] += 128;
                     f1[m] += 128;
                 }
             }
             for (int i = tid; i < fn * PC * KC; i += kManyThreads) {   // 16 bytes each
                 const int c = i / (PC * KC), pc = i / KC % PC, j = i % KC, slot = forder[c];
-                const int row = p.down ? slot : slot / p.k;
+                const int row = p.down ? slot : p.by_k(slot);
                 copy16(to + Sh::kCodes + pc * Sh::kPlane + c * Sh::kPitch + j * 16,
                        p.cols + row * row_bytes + ((long long)pc * p.lines + fline) * (16 * KC) + j * 16);
             }
@@ -706,11 +792,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             turn ^= 1;
             if (tid < pl.n[r.c]) {
                 const int slot = pl.order[pl.first[r.c] + tid];
-                info[turn * 32 + tid] = p.info[p.down ? slot : slot / p.k];
+                info[turn * 32 + tid] = p.info[p.down ? slot : p.by_k(slot)];
             }
             chunk = r.c;
         }
-        const int n = pl.n[r.c], tile = (int)(r.u + warp - (long long)r.c * units) * 2;
+        const int n = pl.n[r.c], tile = (r.u + warp - r.c * units) * 2;
         const bool mine = warp < r.n;
         float sum[2][NT][4] = {}, sa[2] = {}, sb[2] = {};
         if (mine) {
@@ -773,27 +859,28 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 
 // ---------------------------------------------------------------- launches
 template <int FMT, int PC, bool RAW>
-cudaError_t moe_start(const MoeStream &p, const MoeWay &w, int grid, cudaStream_t st) {
-    auto go = [&](auto kernel, int warps) {
+cudaError_t moe_start(const MoeStream &p, const MoeWay &w, int n_sms, cudaStream_t st) {
+    auto go = [&](auto kernel) {
         cudaError_t e = allow_dynamic_smem((const void *)kernel, 227 * 1024);
-        return e != cudaSuccess ? e : launch_dependent(kernel, dim3(grid), 32 * warps, w.smem, st, p);
+        return e != cudaSuccess ? e : launch_dependent(kernel, dim3(n_sms * w.blocks), 32 * w.warps, w.smem, st, p);
     };
-    if (w.kind == 2) return go(moe_many_kernel<FMT, PC, RAW>, kManyWarps);
-    if (w.kind == 1) return go(moe_few_kernel<FMT, PC, RAW, 5>, kFewWarps);
-    return go(moe_few_kernel<FMT, PC, RAW, 3>, kFewWarps);
+    if (w.kind == 2) return go(moe_many_kernel<FMT, PC, RAW>);
+    if (w.kind == 1) return go(moe_few_kernel<FMT, PC, RAW, 8, 4>);
+    return go(moe_few_kernel<FMT, PC, RAW, 16, 3>);
 }
 
 template <int FMT>
-cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int grid, cudaStream_t st) {
-    if (p.type == B200Q_T_F32) return moe_start<FMT, 2, false>(p, w, grid, st);
-    return moe_pieces(p.type, p.down) == 2 ? moe_start<FMT, 2, true>(p, w, grid, st) : moe_start<FMT, 1, true>(p, w, grid, st);
+cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int n_sms, cudaStream_t st) {
+    if (p.type == B200Q_T_F32) return moe_start<FMT, 2, false>(p, w, n_sms, st);
+    return moe_pieces(p.type, p.down) == 2 ? moe_start<FMT, 2, true>(p, w, n_sms, st) : moe_start<FMT, 1, true>(p, w, n_sms, st);
 }
 
 template <int FMT>
 cudaError_t moe_launch_prepare(const MoeStream &p, int rows, uint8_t *cols, float2 *info, cudaStream_t st) {
-    if (p.type == B200Q_T_F32) return launch_dependent(moe_prepare_kernel<FMT, 2, false>, dim3(rows), 256, 0, st, p, cols, info);
-    return moe_pieces(p.type, p.down) == 2 ? launch_dependent(moe_prepare_kernel<FMT, 2, true>, dim3(rows), 256, 0, st, p, cols, info)
-                                           : launch_dependent(moe_prepare_kernel<FMT, 1, true>, dim3(rows), 256, 0, st, p, cols, info);
+    auto go = [&](auto kernel) { return launch_dependent(kernel, dim3(rows), 256, 0, st, p, cols, info); };
+    if (p.type == B200Q_T_F32) return p.down ? go(moe_prepare_kernel<FMT, 2, false, GatedRows>) : go(moe_prepare_kernel<FMT, 2, false, TokenRows<float>>);
+    if (p.type == B200Q_T_F16) return p.down ? go(moe_prepare_kernel<FMT, 2, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, TokenRows<__half>>);
+    return p.down ? go(moe_prepare_kernel<FMT, 1, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, TokenRows<__nv_bfloat16>>);
 }
 
 // kind 0 and 1: as many columns as there are tokens, at most 8, and slices that
@@ -804,6 +891,8 @@ MoeWay moe_way_of(int kind, int pieces, int S, int lines) {
     MoeWay w{};
     w.kind = kind;
     w.ns = 1;
+    w.warps = kind == 0 ? 16 : 8;
+    w.blocks = kind == 1 ? 2 : 1;
     if (kind == 2) {
         w.nc = pieces == 2 ? kManyColumns<FMT, 2> : kManyColumns<FMT, 1>;
         w.smem = pieces == 2 ? ManyShape<FMT, 2>::kBytes : ManyShape<FMT, 1>::kBytes;
@@ -811,7 +900,7 @@ MoeWay moe_way_of(int kind, int pieces, int S, int lines) {
         return w;
     }
     w.nc = S < kFewColumns ? S : kFewColumns;
-    const size_t fixed = kind ? FewShape<5>::kB : FewShape<3>::kB, room = 227 * 1024 - fixed;
+    const size_t fixed = kind ? FewShape<8, 4>::kB : FewShape<16, 3>::kB, room = (kind ? 113 * 1024 : 227 * 1024) - fixed;
     // a column is 64 bytes off a 128-byte multiple: no bank conflicts; 512 blocks of 32 units have their sums' places
     auto fits = [&](int ns) {
         const long long per = (lines + ns - 1) / ns;

@@ -182,7 +182,7 @@ struct Experts {
     long long ld_in, ld_out;   // row strides of gate / up and of down, bytes
     Expert *table;             // device, [E]
 };
-constexpr int kMoeMaxExperts = 1024, kMoeMaxK = 32;
+constexpr int kMoeMaxExperts = 1024, kMoeMaxK = 32, kMoeMaxSize = 1 << 24;
 
 // y = res + sum_j w_j down_e(act(gate_e x) * (up_e x)), e = ids[s, j].
 struct Moe {
