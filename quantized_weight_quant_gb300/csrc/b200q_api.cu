@@ -253,7 +253,7 @@ int b200q_device_status(void) {
     if (e != cudaSuccess) return cuda_fail(e, "b200q_device_status");
     if (d == (unsigned)(-B200Q_ECUDA))
         return fail(B200Q_ECUDA, "b200q_device_status: an 8-bit product found its tensor memory at another base than 0");
-    if (a || b || c || d || m == (unsigned)(-B200Q_ETIMEOUT))
+    if (a || b || c || d || m == (unsigned)(-B200Q_ETIMEOUT) || x == (unsigned)(-B200Q_ETIMEOUT))
         return fail(B200Q_ETIMEOUT, "b200q_device_status: a kernel gave up on a bounded wait");
     if (m) return fail(B200Q_EINVAL, "b200q_device_status: an MLA call met a NULL or unaligned cache page");
     if (x) return fail(B200Q_EINVAL, "b200q_device_status: an experts' call met an expert number outside the layer");
@@ -995,6 +995,9 @@ b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q
             else if (t.fmt != ex->fmt || t.O != (m == 2 ? ex->D : ex->F) || t.I != (m == 2 ? ex->F : ex->D))
                 rc = fail(B200Q_EINVAL, "%s: %s %d is not [%d, %d] in the first tensor's format", who,
                           m == 0 ? "gate" : m == 1 ? "up" : "down", e, m == 2 ? ex->D : ex->F, m == 2 ? ex->F : ex->D);
+            if (rc == B200Q_OK && !tmap_encode_2d(&host[e].map[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, t.codes, (uint64_t)t.ld,
+                                                  (uint64_t)t.o_pad, (uint64_t)t.ld, 128, 8, CU_TENSOR_MAP_SWIZZLE_128B))
+                rc = fail(B200Q_ECUDA, "%s: encoding a tensor map failed", who);
             host[e].codes[m] = t.codes;
             host[e].scales[m] = t.scales;
         }

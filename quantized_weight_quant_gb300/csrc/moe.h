@@ -32,7 +32,7 @@ struct MoeStream {
     int lines, ns, ns_in;                     // 128-byte lines of a row, slices of them
     int tiles, wk;                            // of the rows; 2^wk warps share one (few columns)
     Quotient by_tiles, by_grid, by_k;
-    int nc, pitch;                            // columns of a chunk, bytes of one in shared memory
+    int nc, held, pitch;                      // columns of a chunk, of those staged together, bytes of one in shared memory
     bool down, aligned;                       // aligned: the tokens' rows start on 16 bytes
     // many columns: rows in f16 as prepared, their scales and sums
     const uint8_t *cols;                      // [rows][pieces][lines][16 KC]
@@ -42,7 +42,8 @@ struct MoeStream {
 // How a product is launched: its kernel, columns of a chunk, slices, shared memory.
 struct MoeWay {
     int kind;                                 // 0 few columns, 1 few and short ones (two blocks on an SM), 2 many columns
-    int nc, ns, pitch, warps, blocks;         // columns of a chunk, slices, bytes of a column; warps of a block, blocks on an SM
+    int nc, held, ns, pitch;                  // columns of a chunk, of those staged together, slices, bytes of a column
+    int warps, blocks;                        // warps of a block, blocks on an SM
     size_t smem;
 };
 template <int FMT> MoeWay moe_way(int kind, int pieces, int S, int lines);

@@ -134,6 +134,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.wk = shared_by(w.warps, chosen(n, a.k, ex.E) * w.ns * p.tiles / (n_sms * w.blocks), p.lines / w.ns);
         p.ns = w.ns;
         p.nc = w.nc;
+        p.held = w.held;
         p.pitch = w.pitch;
     };
     void *err = nullptr;

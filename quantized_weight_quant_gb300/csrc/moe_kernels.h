@@ -355,27 +355,63 @@ __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], int n, F
 }
 
 // ---------------------------------------------------------------- few columns
-// Up to 8 columns of an expert, resident in shared memory.
-constexpr int kFewColumns = 8;
+// Up to 8 columns of an expert, those of a few chunks at a time in shared memory.
+constexpr int kFewColumns = 8, kFewHeld = 16;  // of a chunk; of the chunks that are staged together
 
 struct FewColumns {
-    unsigned top[kFewColumns];                 // the largest magnitude
-    float unscale[kFewColumns], zero[kFewColumns];     // the inverse scale; the zero point times the sum
+    unsigned top[kFewHeld];                    // the largest magnitude
+    float unscale[kFewHeld], zero[kFewHeld];   // the inverse scale; the zero point times the sum
+    const float *scales[kFewHeld][2];          // of a staged chunk: its rows' scales, gate and up, or down twice
     float part[512];                           // sums of 32 units each
 };
 
 // W: warps of a block; AHEAD: lines in a warp's ring.
 template <int W, int AHEAD> struct FewShape {
     static constexpr int kRing = W * AHEAD * 2048;
+    static constexpr int kBarsAt = kRing;
+    static constexpr int kRedAt = kBarsAt + W * AHEAD * 8;
     static constexpr int kRedTile = kFewColumns * kRedPitch;           // floats of a warp's tile
     static constexpr int kRed = 2 * W * kRedTile * 4;                  // two sets, used in turn; the plan's scratch before
-    static constexpr int kColumnsAt = kRing + kRed;
+    static constexpr int kColumnsAt = kRedAt + kRed;
     static constexpr int kPlanAt = kColumnsAt + (int)sizeof(FewColumns);
     static constexpr int kB = (kPlanAt + (int)sizeof(Plan) + 127) / 128 * 128;
     static_assert(sizeof(PlanScratch) <= kRed, "the plan's scratch lies where the sums will");
 };
 
-// The columns of a chunk, lines l0 .. l1-1, into shared memory.  A warp takes 32
+__device__ __forceinline__ unsigned long long global_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Whether the barrier's phase ended within the limit.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    unsigned long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+        uint32_t done;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(done)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if (it == 0) t0 = global_ns();
+        if ((it & 255) == 255 && global_ns() - t0 > limit_ns) return false;
+    }
+}
+
+constexpr unsigned long long kMoeWaitNs = 2000000000ull;               // 2 s bound on any wait
+
+// A box of 8 rows x 128 bytes of codes to shared memory, swizzled.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], "
+        "%5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// The columns of n slots, lines l0 .. l1-1, into shared memory.  A warp takes 32
 // units of a column at a time: first for its largest magnitude, then again to
 // scale it.  Called by the whole block; ends with a barrier.
 template <int FMT, int PC, bool RAW, class Src>
@@ -385,7 +421,7 @@ __device__ __forceinline__ void stage_from(const MoeStream &p, const unsigned sh
     const int units = (l1 - l0) * KC;          // of a column: KC to a line
     const int k0 = l0 * 8 * KC, width = (units + 31) & ~31;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < kFewColumns) cl.top[threadIdx.x] = 0u;
+    if (threadIdx.x < kFewHeld) cl.top[threadIdx.x] = 0u;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {     // 0: all loads under way at once
         int b = warp;
@@ -411,7 +447,7 @@ __device__ __forceinline__ void stage_from(const MoeStream &p, const unsigned sh
                 sum = split<FMT, PC, RAW>(v, power(exponent_for(cl.top[c])), u, hi, rest);
                 uint8_t *to = B + c * p.pitch + unit_at<FMT>(u);
                 *reinterpret_cast<uint4 *>(to) = hi;
-                if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + p.nc * p.pitch) = rest;
+                if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + p.held * p.pitch) = rest;
             }
             if constexpr (RAW) {
 #pragma unroll 1
@@ -421,18 +457,19 @@ __device__ __forceinline__ void stage_from(const MoeStream &p, const unsigned sh
         }
         __syncthreads();
     }
-    if (warp < n) {
+#pragma unroll 1
+    for (int c = warp; c < n; c += (int)blockDim.x >> 5) {
         float sum = 0.f;
         if constexpr (RAW) {
             const int blocks = width / 32;
 #pragma unroll 1
-            for (int b = lane; b < blocks; b += 32) sum += cl.part[warp * blocks + b];
+            for (int b = lane; b < blocks; b += 32) sum += cl.part[c * blocks + b];
 #pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
         }
         if (lane == 0) {
-            cl.unscale[warp] = power(-exponent_for(cl.top[warp]));
-            cl.zero[warp] = sum * kZeroPoint<FMT>;
+            cl.unscale[c] = power(-exponent_for(cl.top[c]));
+            cl.zero[c] = sum * kZeroPoint<FMT>;
         }
     }
     __syncthreads();
@@ -456,12 +493,17 @@ template <int FMT, int PC, bool RAW, int W, int AHEAD>
 __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_constant__ MoeStream p) {
     using Sh = FewShape<W, AHEAD>;
     constexpr int KC = Fmt<FMT>::KC;
-    extern __shared__ __align__(128) uint8_t smem[];
-    float *red = reinterpret_cast<float *>(smem + Sh::kRing);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *red = reinterpret_cast<float *>(smem + Sh::kRedAt);
     FewColumns &cl = *reinterpret_cast<FewColumns *>(smem + Sh::kColumnsAt);
     Plan &pl = *reinterpret_cast<Plan *>(smem + Sh::kPlanAt);
     uint8_t *B = smem + Sh::kB;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (AHEAD * 2048);
+    const uint32_t bars = (uint32_t)__cvta_generic_to_shared(smem + Sh::kBarsAt) + warp * (AHEAD * 8);
+    // The lanes' rows of a box are not in order: two rows that a quarter of a warp
+    // reads together have their 16 bytes in different banks.
+    const int row = (g & 1) << 2 | g >> 1;
 
     // Addresses that the kernel will wait for one after the other, asked for
     // together: their pages have to be found.
@@ -469,6 +511,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
     if (tid == 32) prefetch(p.table);
     if (tid == 64) prefetch(p.down ? (const void *)p.in : p.x);
     if (tid == 96) prefetch(p.out);
+    if (lane == 0) {                           // the warp's own barriers
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * i) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
     // The ids may come from the kernel before gate and up; down follows them, and
     // they were there when gate and up began.
     if (!p.down) dependency_wait();
@@ -480,143 +528,127 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
     auto first_line = [&](int slice) { return p.ns == 1 ? (slice ? p.lines : 0) : (int)((long long)slice * p.lines / p.ns); };
 
     // the copy cursor: this warp's next line
-    int fcs = p.by_tiles(lo), fu = lo + wm, fend = min(hi, (fcs + 1) * p.tiles);     // its slice's number, tile, end of the tiles
-    int fchunk = -1, fline = 0, fl1 = 0, fslot = 0;
-    const uint8_t *rows0 = nullptr, *rows1 = nullptr;                       // rows g and g + 8 of tile 0
-    const uint8_t *f0 = nullptr, *f1 = nullptr;                             // the next line of the cursor's
-    const long long tile_bytes = (p.down ? 16 : 8) * p.ld;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (AHEAD * 2048) + lane * 16;
+    int fu = lo + wm, fline = 0, fl1 = 0, fy = 0, fslot = 0;
+    const CUtensorMap *map = nullptr;          // of gate or down; the one of up is the next
     const uint64_t policy = stream_policy();
-    const int step = wk * 128;
     auto open = [&]() {                        // the cursor's tile, or a later one that has a line for this warp
-        while (true) {
-            if (fu >= fend) {
-                if (fend >= hi) return;        // none is left
-                ++fcs;
-                fu = fend + wm;
-                fend = min(hi, fend + p.tiles);
-                continue;
-            }
-            const int c = p.ns == 1 ? fcs : fcs / p.ns, sl = fcs - c * p.ns;
+#pragma unroll 1
+        for (; fu < hi; fu += groups) {
+            const int cs = p.by_tiles(fu), c = p.ns == 1 ? cs : cs / p.ns, sl = cs - c * p.ns;
             fline = first_line(sl) + kw;
             fl1 = first_line(sl + 1);
-            if (fline >= fl1) {
-                fu += groups;
-                continue;
-            }
-            if (c != fchunk) {
-                const Expert &e = p.table[pl.expert[c]];
-                rows0 = (p.down ? e.codes[2] : e.codes[0]) + g * p.ld + tig * 16;
-                rows1 = (p.down ? e.codes[2] + 8 * p.ld : e.codes[1]) + g * p.ld + tig * 16;
-                fchunk = c;
-            }
-            const long long off = (fu - fcs * p.tiles) * tile_bytes + fline * 128;
-            f0 = rows0 + off;
-            f1 = rows1 + off;
+            if (fline >= fl1) continue;
+            map = p.table[pl.expert[c]].map + (p.down ? 2 : 0);
+            fy = (fu - cs * p.tiles) * (p.down ? 16 : 8);
             return;
         }
     };
     auto copy_line = [&]() {
-        if (fu < fend) {
-            const uint32_t to = ring + fslot * 2048;
-            copy16_stream(to, f0, policy);
-            copy16_stream(to + 512, f1, policy);
-            copy16_stream(to + 1024, f0 + 64, policy);
-            copy16_stream(to + 1536, f1 + 64, policy);
-            f0 += step;
-            f1 += step;
+        if (fu < hi) {
+            if (lane == 0) {
+                const uint32_t to = ring + fslot * 2048, bar = bars + 8 * fslot;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 2048;" ::"r"(bar) : "memory");
+                copy_box(to, map, fline * 128, fy, bar, policy);
+                copy_box(to + 1024, p.down ? map : map + 1, fline * 128, p.down ? fy + 8 : fy, bar, policy);
+            }
             if (++fslot == AHEAD) fslot = 0;
             if ((fline += wk) >= fl1) {
                 fu += groups;
                 open();
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");           // empty at the end: the waits count groups
     };
-
-    const uint8_t *slots = smem + warp * (AHEAD * 2048) + lane * 16;
-    const int colat = min(g, p.nc - 1) * p.pitch + tig * 16;           // a column past the chunk's is computed and not stored
-    int slot = 0, set = 0, cs = fcs;
-    // Down fills its ring while gate and up end.  Gate and up ask for their first
-    // columns before the codes, which keep the memory busy for a while.
-    bool filled = p.down;
-    if (p.down) {
-        open();
+    open();
 #pragma unroll 1
-        for (int i = 0; i < AHEAD; ++i) copy_line();
-        dependency_wait();
-    }
+    for (int i = 0; i < AHEAD; ++i) copy_line();
+    if (p.down) dependency_wait();
     let_dependents_start();
-    for (int u0 = lo; u0 < hi; ++cs) {         // the block's tiles of one slice of one chunk
-        const int c = p.ns == 1 ? cs : cs / p.ns, slice = cs - c * p.ns;
-        const int base = cs * p.tiles, u1 = min(hi, base + p.tiles), l0 = first_line(slice), l1 = first_line(slice + 1);
-        const unsigned short *order = pl.order + pl.first[c];
-        const int n = pl.n[c];
-        __syncthreads();                       // the columns before are read, and the plan's scratch
-        stage<FMT, PC, RAW>(p, order, n, l0, l1, B, cl);
-        if (!filled) {
-            open();
+
+    const uint8_t *mine = smem + warp * (AHEAD * 2048) + row * 128 + ((tig ^ row) << 4);
+    int slot = 0, set = 0, u = lo + wm;        // the warp's tiles follow each other as the cursor's do
+    uint32_t parity = 0;
+    bool ok = true;                            // false: a copy did not come, the rest is not waited for
 #pragma unroll 1
-            for (int i = 0; i < AHEAD; ++i) copy_line();
-            filled = true;
+    for (int u0 = lo; u0 < hi;) {              // the block's tiles whose columns are staged together
+        const int cs0 = p.by_tiles(u0), c0 = p.ns == 1 ? cs0 : cs0 / p.ns, slice = cs0 - c0 * p.ns;
+        const int l0 = first_line(slice), l1 = first_line(slice + 1);
+        const unsigned short *order = pl.order + pl.first[c0];
+        int held = pl.n[c0], chunks = 1, u1 = (cs0 + 1) * p.tiles;
+        if (p.ns == 1) {
+#pragma unroll 1
+            for (; u1 < hi && held + pl.n[c0 + chunks] <= p.held; u1 += p.tiles) held += pl.n[c0 + chunks], ++chunks;
         }
-        const Expert &e = p.table[pl.expert[c]];
-        const float *s0 = p.down ? e.scales[2] : e.scales[0], *s1 = p.down ? e.scales[2] + 8 : e.scales[1];
-        const int r = wk == 1 ? g : tid & 7;
+        u1 = min(u1, hi);
+        __syncthreads();                       // the columns before are read, and the plan's scratch
+        if (tid < chunks) {
+            const Expert &e = p.table[pl.expert[c0 + tid]];
+            cl.scales[tid][0] = e.scales[p.down ? 2 : 0];
+            cl.scales[tid][1] = p.down ? e.scales[2] + 8 : e.scales[1];
+        }
+        stage<FMT, PC, RAW>(p, order, held, l0, l1, B, cl);
 #pragma unroll 1
-        for (int u = u0 + wm; u < u1; u += groups) {
-            const int tile = u - base;
+        for (; u < u1; u += groups) {
+            const int cs = p.by_tiles(u), at = p.ns == 1 ? cs - c0 : 0, tile = u - cs * p.tiles;
+            const int n = pl.n[c0 + at], column = pl.first[c0 + at] - pl.first[c0];
             // the scales of rows r and r + 8, fetched now, used at the end; rows past the last have scale 0
-            const float sa = s0[tile * (p.down ? 16 : 8) + r], sb = s1[tile * (p.down ? 16 : 8) + r];
+            const int r = wk == 1 ? row : tid & 7, o = tile * (p.down ? 16 : 8) + r;
+            const float sa = cl.scales[at][0][o], sb = cl.scales[at][1][o];
             float sum[1][1][4] = {};
-            const uint8_t *xb = B + kw * (16 * KC) + colat;
+            // a column past the chunk's is computed and not stored
+            const uint8_t *xb = B + (column + min(g, n - 1)) * p.pitch + tig * 16 + kw * (16 * KC);
 #pragma unroll 1
             for (int line = l0 + kw; line < l1; line += wk, xb += wk * (16 * KC)) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
-                const uint8_t *from = slots + slot * 2048;
+                if (ok) ok = mbar_wait(bars + 8 * slot, parity, kMoeWaitNs);
+                const uint8_t *from = mine + slot * 2048, *from2 = reinterpret_cast<const uint8_t *>((uintptr_t)from ^ 64);
                 uint4 q[1][2], next[1][2];     // [tile][row half]
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 512);
-                    next[0][i] = *reinterpret_cast<const uint4 *>(from + 1024 + i * 512);
+                    q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 1024);
+                    next[0][i] = *reinterpret_cast<const uint4 *>(from2 + i * 1024);
                 }
-                if (++slot == AHEAD) slot = 0;
-                copy_line();                   // into the slot just read: this thread's own
+                if (++slot == AHEAD) slot = 0, parity ^= 1;
+                __syncwarp();                  // the slot is read
+                if (ok) copy_line();
                 float acc[1][1][4] = {}, rest[1][1][4] = {};
                 const uint8_t *xh = xb;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, xh += 8 * KC) {
-                    chunk_products<FMT, 1, 1, PC, RAW>(q, n, [&](int) { return xh; }, p.nc * p.pitch, sum, acc, rest);
+                    chunk_products<FMT, 1, 1, PC, RAW>(q, n, [&](int) { return xh; }, p.held * p.pitch, sum, acc, rest);
                     q[0][0] = next[0][0], q[0][1] = next[0][1];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[0][0][i] += PC == 2 ? rest[0][0][i] : acc[0][0][i];
             }
             float a0 = sum[0][0][0], b0 = sum[0][0][2], a1 = sum[0][0][1], b1 = sum[0][0][3];
-            int col = 2 * tig, stride = 1;     // the columns that this thread writes, row r of the tile: at most two if wk = 1
+            int col = 2 * tig, stride = 1, end = min(n, col + 2);      // the columns that this thread writes, row r of the tile
             const float *part = red + (set * W + wm * wk) * Sh::kRedTile + r;
             if (wk > 1) {
                 // [column][row] of this warp's part, added over the tile's warps in order; the two sets
                 // take turns, so that one barrier per tile is enough
-                float *to = red + (set * W + warp) * Sh::kRedTile + 2 * tig * kRedPitch + g;
+                float *to = red + (set * W + warp) * Sh::kRedTile + 2 * tig * kRedPitch + row;
                 to[0] = a0, to[kRedPitch] = a1, to[8] = b0, to[kRedPitch + 8] = b1;
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + wm), "r"(wk * 32) : "memory");
-                col = (kw * 32 + lane) >> 3, stride = wk * 4;
+                col = (kw * 32 + lane) >> 3, stride = wk * 4, end = n;
                 set ^= 1;
             }
-            const int end = wk > 1 ? n : min(n, col + 2);
 #pragma unroll 1
             for (; col < end; col += stride) {
                 if (wk > 1) {
                     a0 = b0 = 0.f;
                     for (int w = 0; w < wk; ++w) a0 += part[col * kRedPitch + w * Sh::kRedTile], b0 += part[col * kRedPitch + w * Sh::kRedTile + 8];
                 }
-                const float un = cl.unscale[col], z = cl.zero[col];
-                put(p, slice, order[col], tile, r, product<RAW>(a0, z, sa, un), product<RAW>(b0, z, sb, un));
+                const float un = cl.unscale[column + col], z = cl.zero[column + col];
+                put(p, slice, order[column + col], tile, r, product<RAW>(a0, z, sa, un), product<RAW>(b0, z, sb, un));
                 a0 = a1, b0 = b1;
             }
         }
         u0 = u1;
+    }
+    if (!ok) {
+        // gave up: say so, and let the copies in flight land
+        if (lane == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_ETIMEOUT));
+#pragma unroll 1
+        for (int i = 0; i < AHEAD; ++i) mbar_wait(bars + 8 * i, i < slot ? parity ^ 1 : parity, kMoeWaitNs / 8);
     }
 }
 
@@ -902,13 +934,15 @@ MoeWay moe_way_of(int kind, int pieces, int S, int lines) {
     w.nc = S < kFewColumns ? S : kFewColumns;
     const size_t fixed = kind ? FewShape<8, 4>::kB : FewShape<16, 3>::kB, room = (kind ? 113 * 1024 : 227 * 1024) - fixed;
     // a column is 64 bytes off a 128-byte multiple: no bank conflicts; 512 blocks of 32 units have their sums' places
-    auto fits = [&](int ns) {
-        const long long per = (lines + ns - 1) / ns;
-        return (per * 16 * KC + 64) * w.nc * pieces <= (long long)room && (per * KC + 31) / 32 * w.nc <= 512;
+    auto most = [&](int ns) {
+        const long long per = (lines + ns - 1) / ns, bytes = (long long)room / ((per * 16 * KC + 64) * pieces), sums = 512 / ((per * KC + 31) / 32);
+        const long long n = bytes < sums ? bytes : sums;
+        return (int)(n < kFewHeld ? n : kFewHeld);
     };
-    while (!fits(w.ns)) ++w.ns;
+    while (most(w.ns) < w.nc) ++w.ns;
+    w.held = most(w.ns);
     w.pitch = (lines + w.ns - 1) / w.ns * 16 * KC + 64;
-    w.smem = fixed + (size_t)w.pitch * w.nc * pieces;
+    w.smem = fixed + (size_t)w.pitch * w.held * pieces;
     return w;
 }
 
