@@ -27,14 +27,14 @@ struct MoeStream {
     float *out;                               // gate and up: what down reads; down: [ns][P][D]
     unsigned int *err;                        // where a wrong id is recorded
     long long ldx, ld;                        // values; bytes of a row of codes
-    int P, k, E, type, act;                   // P = S * k
+    int S, P, k, E, type, act;                // P = S * k
     int K, rows, ldh;                         // columns of the product's rows; its rows; F rounded up to 8
     int lines, ns, ns_in;                     // 128-byte lines of a row, slices of them
     int tiles, wk;                            // of the rows; 2^wk warps share one (few columns)
     Quotient by_tiles, by_grid, by_k;
     int nc, held, pitch;                      // columns of a chunk, of those staged together, bytes of one in shared memory
-    bool down, aligned;                       // aligned: the tokens' rows start on 16 bytes
-    // many columns: rows in f16 as prepared, their scales and sums
+    bool down, aligned, prepared;             // aligned: the tokens' rows start on 16 bytes
+    // prepared: rows in f16 pieces, their scales and sums
     const uint8_t *cols;                      // [rows][pieces][lines][16 KC]
     const float2 *info;                       // inverse scale, zero point times sum
 };

@@ -144,8 +144,11 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
     // h, the down sums, and for many columns the prepared rows
     auto up16 = [](size_t n) { return (n + 15) / 16 * 16; };
     const size_t n_h = up16((size_t)wi.ns * P * (wi.ns == 1 ? 1 : 2) * ldh * 4), n_part = up16((size_t)wo.ns * P * ex.D * 4);
-    const size_t n_x = kind == 2 ? (size_t)S * pc_in * in_lines * 16 * KC : 0, n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * 16 * KC : 0;
-    const size_t n_info = kind == 2 ? up16((size_t)P * 8) : 0;
+    // Tokens' rows are prepared by a launch of their own where there are more than
+    // two (every block would convert them all), h where there are many columns.
+    const bool prepare = kind != 1 && S > 2;
+    const size_t n_x = prepare ? (size_t)S * pc_in * in_lines * 16 * KC : 0, n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * 16 * KC : 0;
+    const size_t n_info = prepare ? up16((size_t)P * 8) : 0;
     uint8_t *ws = nullptr;
     e = workspace_alloc((void **)&ws, n_h + n_part + (n_x > n_hc ? n_x : n_hc) + n_info, st);
     if (e != cudaSuccess) return e;
@@ -163,6 +166,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.err = (unsigned int *)err;
         p.ldx = a.ldx;
         p.ld = ex.ld_in;
+        p.S = n;
         p.P = n * a.k;
         p.k = a.k;
         p.E = ex.E;
@@ -178,7 +182,8 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         place(p, wi, n);
         p.cols = cols;
         p.info = info;
-        if (kind == 2) e = moe_launch_prepare<FMT>(p, n, cols, info, st);
+        p.prepared = prepare;
+        if (prepare) e = moe_launch_prepare<FMT>(p, n, cols, info, st);
         if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wi, n_sms, st);
         if (e != cudaSuccess) break;
         p.down = true;
@@ -189,7 +194,8 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.lines = out_lines;
         p.tiles = (int)((ex.D + 15ll) / 16);
         place(p, wo, n);
-        if (kind == 2) e = moe_launch_prepare<FMT>(p, p.P, cols, info, st);
+        p.prepared = kind == 2;
+        if (p.prepared) e = moe_launch_prepare<FMT>(p, p.P, cols, info, st);
         if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wo, n_sms, st);
         if (e != cudaSuccess) break;
         Sum q{sums, p.ids, a.wts + (long long)s0 * a.k, a.res ? (const char *)a.res + s0 * a.ldr * b : nullptr,

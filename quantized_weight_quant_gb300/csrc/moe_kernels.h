@@ -131,14 +131,13 @@ template <> __device__ __forceinline__ float as_float<float>(float v) { return v
 template <> __device__ __forceinline__ float as_float<__half>(__half v) { return __half2float(v); }
 template <> __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Where a product's columns come from: eight values of a slot's column from c on,
-// 0 from K on, and where they are.  The tokens' rows:
+// Where a product's columns come from: eight values of row `row` from c on, 0
+// from K on.  kExact: f16 holds them, scaled.  The tokens' rows:
 template <class T> struct TokenRows {
-    static __device__ __forceinline__ const void *at(const MoeStream &p, int slot, int c) {
-        return (const T *)p.x + (long long)p.by_k(slot) * p.ldx + c;
-    }
-    static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
-        const T *r = (const T *)at(p, slot, c);
+    static constexpr bool kExact = sizeof(T) == 2;
+    static __device__ __forceinline__ const T *at(const MoeStream &p, int row, int c) { return (const T *)p.x + row * p.ldx + c; }
+    static __device__ __forceinline__ void load(const MoeStream &p, int row, int c, float (&v)[8]) {
+        const T *r = at(p, row, c);
         if (p.aligned && c + 8 <= p.K) {
             union {
                 uint4 q[sizeof(T) / 2];
@@ -154,15 +153,13 @@ template <class T> struct TokenRows {
         }
     }
 };
-// h, in rows of ldh floats, a multiple of 8:
+// h of the slots, in rows of ldh floats, a multiple of 8:
 struct GatedRows {
-    static __device__ __forceinline__ const void *at(const MoeStream &p, int slot, int c) {
-        return p.in + (long long)slot * p.ldh + c;
-    }
+    static constexpr bool kExact = false;
     static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
         if (c < p.K) {
-            const float4 *r = reinterpret_cast<const float4 *>(at(p, slot, c));
+            const float4 *r = reinterpret_cast<const float4 *>(p.in + (long long)slot * p.ldh + c);
             a = r[0], b = r[1];
         }
         const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -172,9 +169,7 @@ struct GatedRows {
 };
 // act(gate) * up of the slices' sums, [ns_in][P][2][ldh]:
 struct SlicedRows {
-    static __device__ __forceinline__ const void *at(const MoeStream &p, int slot, int c) {
-        return p.in + (long long)slot * 2 * p.ldh + c;
-    }
+    static constexpr bool kExact = false;
     static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
@@ -208,13 +203,13 @@ __device__ __forceinline__ unsigned largest(const float (&v)[8]) {
 // the instructions, and where they do.  Per 64 bytes of codes a column has KC / 8
 // pieces of 64 bytes, 16 of them for each of the four threads that share a row.
 template <int FMT, class Src>
-__device__ __forceinline__ void unit8(const MoeStream &p, int slot, int k0, int u, float (&v)[8]) {
+__device__ __forceinline__ void unit8(const MoeStream &p, int row, int k0, int u, float (&v)[8]) {
     if constexpr (FMT == B200Q_I2) {
         // a word is 16 codes: the values that its instructions 2j, 2j+1 take, j = u & 1
         const int c = k0 + 16 * (u >> 1), j = u & 1;
         float lo[8], hi[8];
-        Src::load(p, slot, c, lo);
-        Src::load(p, slot, c + 8, hi);
+        Src::load(p, row, c, lo);
+        Src::load(p, row, c + 8, hi);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             v[4 * t] = j ? lo[2 + t] : lo[t];
@@ -223,7 +218,7 @@ __device__ __forceinline__ void unit8(const MoeStream &p, int slot, int k0, int 
             v[4 * t + 3] = j ? hi[6 + t] : hi[4 + t];
         }
     } else {
-        Src::load(p, slot, k0 + 8 * u, v);
+        Src::load(p, row, k0 + 8 * u, v);
     }
 }
 template <int FMT>
@@ -237,7 +232,7 @@ __device__ __forceinline__ int unit_at(int u) {
 // takes a word of codes apart, and what is left of them to `rest`; their sum as
 // they are then.  RAW: two by two they meet fields 0 0 1 1 of a word, or 2 2 3 3
 // (odd units of int2), and are divided by 2^b for a field at bit b.
-template <int FMT, int PC, bool RAW>
+template <int FMT, int PC, bool RAW, bool EXACT>
 __device__ __forceinline__ float split(const float (&v)[8], float scale, int u, uint4 &hi, uint4 &rest) {
     const float d0 = RAW && FMT == B200Q_I2 && (u & 1) ? 1.f / 16.f : 1.f;
     const float d1 = RAW ? d0 / (float)(1 << kShift<FMT>) : 1.f;
@@ -247,18 +242,23 @@ __device__ __forceinline__ float split(const float (&v)[8], float scale, int u, 
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = v[kOrder[2 * i]] * scale, b = v[kOrder[2 * i + 1]] * scale, d = i < 2 ? d0 : d1;
-        const __half2 t = __floats2half2_rn(a, b);
-        const float2 f = __half22float2(t);
-        sum += f.x + f.y;
-        const __half2 hd = RAW ? __hmul2(t, __float2half2_rn(d)) : t;
-        h[i] = *reinterpret_cast<const uint32_t *>(&hd);
-        if constexpr (PC == 2) {
-            const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
-            const float2 rf = __half22float2(r);
-            sum += rf.x + rf.y;
-            const __half2 rd = RAW ? __hmul2(r, __float2half2_rn(d)) : r;
-            l[i] = *reinterpret_cast<const uint32_t *>(&rd);
+        const float d = i < 2 ? d0 : d1;
+        float a = v[kOrder[2 * i]] * scale, b = v[kOrder[2 * i + 1]] * scale;
+        if constexpr (PC == 1 && EXACT) {      // rounds only what is 2^-38 of the column's largest or less
+            sum += a + b;
+            const __half2 t = __floats2half2_rn(a * d, b * d);
+            h[i] = *reinterpret_cast<const uint32_t *>(&t);
+        } else {
+            const __half2 t = __floats2half2_rn(a, b), td = RAW ? __hmul2(t, __float2half2_rn(d)) : t;
+            const float2 f = __half22float2(t);
+            sum += f.x + f.y;
+            h[i] = *reinterpret_cast<const uint32_t *>(&td);
+            if constexpr (PC == 2) {
+                const __half2 r = __floats2half2_rn(a - f.x, b - f.y), rd = RAW ? __hmul2(r, __float2half2_rn(d)) : r;
+                const float2 rf = __half22float2(r);
+                sum += rf.x + rf.y;
+                l[i] = *reinterpret_cast<const uint32_t *>(&rd);
+            }
         }
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
@@ -296,14 +296,19 @@ __device__ __forceinline__ void put(const MoeStream &p, int slice, int slot, int
 // The products of a thread's 16 bytes of codes (of MT tiles, rows g and g + 8)
 // with NT x 8 columns, of which the first n are wanted; `from(nt)` is where this
 // thread's column of tile nt has its values, its second pieces `plane` bytes
-// further.  Two pieces: the first ones' sums are taken out of the accumulator
-// after every word of codes, the second ones are in `rest`.
-template <int FMT, int NT, int MT, int PC, bool RAW, class From>
+// further.  The words take NA accumulators in turn: an instruction waits for the
+// one before it on the same accumulator.  Two pieces: the first ones' sums are
+// taken out of the accumulator after every word of codes, the second ones are in
+// `rest`.
+template <int FMT, int NT, int MT, int PC, bool RAW, int NA, class From>
 __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], int n, From from, int plane, float (&sum)[MT][NT][4],
-                                               float (&acc)[MT][NT][4], float (&rest)[PC == 2 ? MT : 1][PC == 2 ? NT : 1][4]) {
+                                               float (&accs)[NA][MT][NT][4],
+                                               float (&rests)[PC == 2 ? NA : 1][PC == 2 ? MT : 1][PC == 2 ? NT : 1][4]) {
     constexpr int MMAS = Fmt<FMT>::MMAS;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
+        float (&acc)[MT][NT][4] = accs[w % NA];
+        auto &rest = rests[PC == 2 ? w % NA : 0];
         uint32_t a[MT][MMAS][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -361,15 +366,15 @@ constexpr int kFewColumns = 8, kFewHeld = 16;  // of a chunk; of the chunks that
 struct FewColumns {
     unsigned top[kFewHeld];                    // the largest magnitude
     float unscale[kFewHeld], zero[kFewHeld];   // the inverse scale; the zero point times the sum
-    const float *scales[kFewHeld][2];          // of a staged chunk: its rows' scales, gate and up, or down twice
-    float part[512];                           // sums of 32 units each
+    const float *scales[kFewHeld][2];          // of a chunk: its rows' scales, gate and up, or down twice
+    float part[kFewHeld][16];                  // the warps' sums
 };
 
 // W: warps of a block; AHEAD: lines in a warp's ring.
 template <int W, int AHEAD> struct FewShape {
     static constexpr int kRing = W * AHEAD * 2048;
     static constexpr int kBarsAt = kRing;
-    static constexpr int kRedAt = kBarsAt + W * AHEAD * 8;
+    static constexpr int kRedAt = kBarsAt + W * AHEAD * 8 + 16;        // and the columns' barrier
     static constexpr int kRedTile = kFewColumns * kRedPitch;           // floats of a warp's tile
     static constexpr int kRed = 2 * W * kRedTile * 4;                  // two sets, used in turn; the plan's scratch before
     static constexpr int kColumnsAt = kRedAt + kRed;
@@ -411,81 +416,83 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// The columns of n slots, lines l0 .. l1-1, into shared memory.  A warp takes 32
-// units of a column at a time: first for its largest magnitude, then again to
-// scale it.  Called by the whole block; ends with a barrier.
-template <int FMT, int PC, bool RAW, class Src>
-__device__ __forceinline__ void stage_from(const MoeStream &p, const unsigned short *order, int n, int l0, int l1, uint8_t *B,
-                                        FewColumns &cl) {
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, int bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+
+// n rows, lines l0 .. l1-1 of them, into shared memory as columns; row_of(c) is
+// column c's.  First their largest magnitudes, then once more to scale them.
+// Called by the whole block; ends with a barrier.
+template <int FMT, int PC, bool RAW, class Src, class RowOf>
+__device__ __forceinline__ void stage_from(const MoeStream &p, RowOf row_of, int n, int l0, int l1, uint8_t *B, FewColumns &cl) {
     constexpr int KC = Fmt<FMT>::KC;
     const int units = (l1 - l0) * KC;          // of a column: KC to a line
-    const int k0 = l0 * 8 * KC, width = (units + 31) & ~31;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < kFewHeld) cl.top[threadIdx.x] = 0u;
+    const int k0 = l0 * 8 * KC, tid = threadIdx.x, lane = tid & 31;
+    int lg = 5;                                // 2^lg threads take a column
+    while (1 << lg < units && 1 << lg < (int)blockDim.x) ++lg;
+    const int sub = tid & ((1 << lg) - 1), c0 = tid >> lg, step = (int)blockDim.x >> lg;
+    if (tid < kFewHeld) cl.top[tid] = 0u;
+    __syncthreads();
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {     // 0: all loads under way at once
-        int b = warp;
+    for (int c = c0; c < n; c += step) {
+        const int row = row_of(c);
+        unsigned m = 0;
 #pragma unroll 1
-        for (int c = 0, u = (int)threadIdx.x; c < n; u += blockDim.x, b += blockDim.x >> 5) {
-#pragma unroll 1
-            while (u >= width && c < n) u -= width, ++c;
-            if (c == n) break;
-            const int slot = order[c];
-            if (pass == 0) {
-                if (k0 + 8 * u < p.K) asm volatile("prefetch.global.L1 [%0];" ::"l"(Src::at(p, slot, k0 + 8 * u)));
-                continue;
-            }
-            float v[8] = {}, sum = 0.f;
-            if (u < units) unit8<FMT, Src>(p, slot, k0, u, v);
-            if (pass == 1) {
-                const unsigned m = __reduce_max_sync(kAll, largest(v));
-                if (lane == 0) atomicMax(&cl.top[c], m);
-                continue;
-            }
-            if (u < units) {
-                uint4 hi, rest;
-                sum = split<FMT, PC, RAW>(v, power(exponent_for(cl.top[c])), u, hi, rest);
-                uint8_t *to = B + c * p.pitch + unit_at<FMT>(u);
-                *reinterpret_cast<uint4 *>(to) = hi;
-                if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + p.held * p.pitch) = rest;
-            }
-            if constexpr (RAW) {
-#pragma unroll 1
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-                if (lane == 0) cl.part[b] = sum;
-            }
+        for (int u = sub; u < units; u += 1 << lg) {
+            float v[8];
+            Src::load(p, row, k0 + 8 * u, v);
+            m = max(m, largest(v));
         }
-        __syncthreads();
+        m = __reduce_max_sync(kAll, m);
+        if (lane == 0) atomicMax(&cl.top[c], m);
     }
+    __syncthreads();
 #pragma unroll 1
-    for (int c = warp; c < n; c += (int)blockDim.x >> 5) {
+    for (int c = c0; c < n; c += step) {
+        const int row = row_of(c), up = exponent_for(cl.top[c]);
+        const float scale = power(up);
+        float sum = 0.f;
+        uint8_t *to = B + c * p.pitch;
+#pragma unroll 1
+        for (int u = sub; u < units; u += 1 << lg) {
+            float v[8];
+            uint4 hi, rest;
+            unit8<FMT, Src>(p, row, k0, u, v);
+            sum += split<FMT, PC, RAW, Src::kExact>(v, scale, u, hi, rest);
+            *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u)) = hi;
+            if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u) + p.held * p.pitch) = rest;
+        }
+        if constexpr (RAW) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            if (lane == 0) cl.part[c][sub >> 5] = sum;
+        }
+        if (sub == 0) cl.unscale[c] = power(-up);
+    }
+    __syncthreads();
+    if (tid < n) {
         float sum = 0.f;
         if constexpr (RAW) {
-            const int blocks = width / 32;
 #pragma unroll 1
-            for (int b = lane; b < blocks; b += 32) sum += cl.part[c * blocks + b];
-#pragma unroll 1
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            for (int w = 0; w < 1 << (lg - 5); ++w) sum += cl.part[tid][w];
         }
-        if (lane == 0) {
-            cl.unscale[c] = power(-exponent_for(cl.top[c]));
-            cl.zero[c] = sum * kZeroPoint<FMT>;
-        }
+        cl.zero[tid] = sum * kZeroPoint<FMT>;
     }
     __syncthreads();
 }
 
-template <int FMT, int PC, bool RAW>
-__device__ __forceinline__ void stage(const MoeStream &p, const unsigned short *order, int n, int l0, int l1, uint8_t *B,
-                                      FewColumns &cl) {
+template <int FMT, int PC, bool RAW, class RowOf>
+__device__ __forceinline__ void stage(const MoeStream &p, RowOf row_of, int n, int l0, int l1, uint8_t *B, FewColumns &cl) {
     if (p.down) {
-        if (p.ns_in == 1) stage_from<FMT, PC, RAW, GatedRows>(p, order, n, l0, l1, B, cl);
-        else stage_from<FMT, PC, RAW, SlicedRows>(p, order, n, l0, l1, B, cl);
+        if (p.ns_in == 1) stage_from<FMT, PC, RAW, GatedRows>(p, row_of, n, l0, l1, B, cl);
+        else stage_from<FMT, PC, RAW, SlicedRows>(p, row_of, n, l0, l1, B, cl);
     } else if constexpr (!RAW) {
-        stage_from<FMT, PC, RAW, TokenRows<float>>(p, order, n, l0, l1, B, cl);
+        stage_from<FMT, PC, RAW, TokenRows<float>>(p, row_of, n, l0, l1, B, cl);
     } else if constexpr (PC == 1) {            // with two pieces 16-bit rows are only h
-        if (p.type == B200Q_T_F16) stage_from<FMT, PC, RAW, TokenRows<__half>>(p, order, n, l0, l1, B, cl);
-        else stage_from<FMT, PC, RAW, TokenRows<__nv_bfloat16>>(p, order, n, l0, l1, B, cl);
+        if (p.type == B200Q_T_F16) stage_from<FMT, PC, RAW, TokenRows<__half>>(p, row_of, n, l0, l1, B, cl);
+        else stage_from<FMT, PC, RAW, TokenRows<__nv_bfloat16>>(p, row_of, n, l0, l1, B, cl);
     }
 }
 
@@ -511,16 +518,21 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
     if (tid == 32) prefetch(p.table);
     if (tid == 64) prefetch(p.down ? (const void *)p.in : p.x);
     if (tid == 96) prefetch(p.out);
+    const uint32_t colbar = (uint32_t)__cvta_generic_to_shared(smem + Sh::kBarsAt + W * AHEAD * 8);
     if (lane == 0) {                           // the warp's own barriers
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * i) : "memory");
+        if (warp == 0) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(colbar) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
-    // The ids may come from the kernel before gate and up; down follows them, and
-    // they were there when gate and up began.
-    if (!p.down) dependency_wait();
+    // The ids may come from the kernel before the call's first; the others follow
+    // it, and the ids were there when it began.
+    const bool first_kernel = !p.down && !p.prepared;
+    if (first_kernel) dependency_wait();
     make_plan(p, pl, *reinterpret_cast<PlanScratch *>(red));
+    // the tokens' rows are the columns where all of them have room
+    const bool tokens = !p.down && p.ns == 1 && p.S <= p.held;
     // an even run of the tiles; their number is below 2^31
     const int all = pl.chunks * p.ns * p.tiles, each = p.by_grid(all), more = all - each * (int)gridDim.x;
     const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
@@ -561,12 +573,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
     open();
 #pragma unroll 1
     for (int i = 0; i < AHEAD; ++i) copy_line();
-    if (p.down) dependency_wait();
+    if (!first_kernel) dependency_wait();
     let_dependents_start();
 
     const uint8_t *mine = smem + warp * (AHEAD * 2048) + row * 128 + ((tig ^ row) << 4);
     int slot = 0, set = 0, u = lo + wm;        // the warp's tiles follow each other as the cursor's do
-    uint32_t parity = 0;
+    uint32_t parity = 0, colparity = 0;
     bool ok = true;                            // false: a copy did not come, the rest is not waited for
 #pragma unroll 1
     for (int u0 = lo; u0 < hi;) {              // the block's tiles whose columns are staged together
@@ -576,7 +588,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
         int held = pl.n[c0], chunks = 1, u1 = (cs0 + 1) * p.tiles;
         if (p.ns == 1) {
 #pragma unroll 1
-            for (; u1 < hi && held + pl.n[c0 + chunks] <= p.held; u1 += p.tiles) held += pl.n[c0 + chunks], ++chunks;
+            for (; u1 < hi && chunks < kFewHeld && (tokens || held + pl.n[c0 + chunks] <= p.held); u1 += p.tiles)
+                held += pl.n[c0 + chunks], ++chunks;
         }
         u1 = min(u1, hi);
         __syncthreads();                       // the columns before are read, and the plan's scratch
@@ -585,17 +598,43 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
             cl.scales[tid][0] = e.scales[p.down ? 2 : 0];
             cl.scales[tid][1] = p.down ? e.scales[2] + 8 : e.scales[1];
         }
-        stage<FMT, PC, RAW>(p, order, held, l0, l1, B, cl);
+        auto row_of = [&](int c) { return tokens ? c : p.down ? order[c] : p.by_k(order[c]); };
+        const int columns = tokens ? p.S : held;
+        if (tokens && u0 != lo) {
+            __syncthreads();
+        } else if (p.prepared) {
+            const int bytes = (l1 - l0) * (16 * KC);
+            if (tid == 0) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(colbar), "r"(columns * PC * bytes) : "memory");
+#pragma unroll 1
+                for (int c = 0; c < columns * PC; ++c) {               // first pieces, then second ones
+                    const int col = c < columns ? c : c - columns;
+                    const uint8_t *from = p.cols + ((long long)(row_of(col) * PC + (c < columns ? 0 : 1)) * p.lines + l0) * (16 * KC);
+                    copy_bulk((uint32_t)__cvta_generic_to_shared(B) + (col + (c < columns ? 0 : p.held)) * p.pitch, from, bytes, colbar);
+                }
+            }
+            if (tid < columns) {
+                const float2 i = p.info[row_of(tid)];
+                cl.unscale[tid] = i.x;
+                cl.zero[tid] = slice == 0 ? i.y : 0.f;                 // of the whole row: taken off once
+            }
+            if (ok) ok = mbar_wait(colbar, colparity, kMoeWaitNs);
+            colparity ^= 1;
+            __syncthreads();
+        } else {
+            stage<FMT, PC, RAW>(p, row_of, columns, l0, l1, B, cl);
+        }
 #pragma unroll 1
         for (; u < u1; u += groups) {
             const int cs = p.by_tiles(u), at = p.ns == 1 ? cs - c0 : 0, tile = u - cs * p.tiles;
-            const int n = pl.n[c0 + at], column = pl.first[c0 + at] - pl.first[c0];
+            const int n = pl.n[c0 + at], first = pl.first[c0 + at] - pl.first[c0];
+            auto column = [&](int c) { return tokens ? p.by_k(order[first + c]) : first + c; };
             // the scales of rows r and r + 8, fetched now, used at the end; rows past the last have scale 0
             const int r = wk == 1 ? row : tid & 7, o = tile * (p.down ? 16 : 8) + r;
             const float sa = cl.scales[at][0][o], sb = cl.scales[at][1][o];
             float sum[1][1][4] = {};
             // a column past the chunk's is computed and not stored
-            const uint8_t *xb = B + (column + min(g, n - 1)) * p.pitch + tig * 16 + kw * (16 * KC);
+            const uint8_t *xb = B + column(min(g, n - 1)) * p.pitch + tig * 16 + kw * (16 * KC);
 #pragma unroll 1
             for (int line = l0 + kw; line < l1; line += wk, xb += wk * (16 * KC)) {
                 if (ok) ok = mbar_wait(bars + 8 * slot, parity, kMoeWaitNs);
@@ -609,15 +648,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                 if (++slot == AHEAD) slot = 0, parity ^= 1;
                 __syncwarp();                  // the slot is read
                 if (ok) copy_line();
-                float acc[1][1][4] = {}, rest[1][1][4] = {};
-                const uint8_t *xh = xb;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half, xh += 8 * KC) {
-                    chunk_products<FMT, 1, 1, PC, RAW>(q, n, [&](int) { return xh; }, p.held * p.pitch, sum, acc, rest);
-                    q[0][0] = next[0][0], q[0][1] = next[0][1];
-                }
+                constexpr int NA = PC == 2 ? 2 : 4;
+                float acc[NA][1][1][4] = {}, rest[PC == 2 ? NA : 1][1][1][4] = {};
+                chunk_products<FMT, 1, 1, PC, RAW, NA>(q, n, [&](int) { return xb; }, p.held * p.pitch, sum, acc, rest);
+                chunk_products<FMT, 1, 1, PC, RAW, NA>(next, n, [&](int) { return xb + 8 * KC; }, p.held * p.pitch, sum, acc, rest);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[0][0][i] += PC == 2 ? rest[0][0][i] : acc[0][0][i];
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (PC == 2) sum[0][0][i] += rest[0][0][0][i] + rest[1][0][0][i];
+                    else sum[0][0][i] += (acc[0][0][0][i] + acc[1][0][0][i]) + (acc[2][0][0][i] + acc[3][0][0][i]);
+                }
             }
             float a0 = sum[0][0][0], b0 = sum[0][0][2], a1 = sum[0][0][1], b1 = sum[0][0][3];
             int col = 2 * tig, stride = 1, end = min(n, col + 2);      // the columns that this thread writes, row r of the tile
@@ -637,8 +676,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                     a0 = b0 = 0.f;
                     for (int w = 0; w < wk; ++w) a0 += part[col * kRedPitch + w * Sh::kRedTile], b0 += part[col * kRedPitch + w * Sh::kRedTile + 8];
                 }
-                const float un = cl.unscale[column + col], z = cl.zero[column + col];
-                put(p, slice, order[column + col], tile, r, product<RAW>(a0, z, sa, un), product<RAW>(b0, z, sb, un));
+                const int b = column(col);
+                const float un = cl.unscale[b], z = cl.zero[b];
+                put(p, slice, order[first + col], tile, r, product<RAW>(a0, z, sa, un), product<RAW>(b0, z, sb, un));
                 a0 = a1, b0 = b1;
             }
         }
@@ -683,7 +723,7 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
         const int e = p.ids[row];
         if (e < 0 || e >= p.E) return;         // an empty slot has no h
     }
-    const int slot = p.down ? row : row * p.k, units = p.lines * KC;
+    const int units = p.lines * KC;
     unsigned m = 0;
 #pragma unroll 1
     for (int u0 = threadIdx.x; u0 < units; u0 += 3 * 256) {
@@ -692,7 +732,7 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
         for (int i = 0; i < 3; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-            if (u0 + i * 256 < units) Src::load(p, slot, 8 * (u0 + i * 256), v[i]);
+            if (u0 + i * 256 < units) Src::load(p, row, 8 * (u0 + i * 256), v[i]);
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) m = max(m, largest(v[i]));
@@ -709,8 +749,8 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
     for (int u = threadIdx.x; u < units; u += 256) {
         float v[8];
         uint4 hi, rest;
-        unit8<FMT, Src>(p, slot, 0, u, v);
-        sum += split<FMT, PC, RAW>(v, scale, u, hi, rest);
+        unit8<FMT, Src>(p, row, 0, u, v);
+        sum += split<FMT, PC, RAW, Src::kExact>(v, scale, u, hi, rest);
         *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u)) = hi;
         if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * (16 * KC) + unit_at<FMT>(u)) = rest;
     }
@@ -848,7 +888,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             const uint8_t *at = smem + stage * Sh::kStage;
             if (++stage == STAGES) stage = 0;
             if (!mine) continue;
-            float acc[2][NT][4] = {}, rest[PC == 2 ? 2 : 1][PC == 2 ? NT : 1][4] = {};
+            float acc[1][2][NT][4] = {}, rest[1][PC == 2 ? 2 : 1][PC == 2 ? NT : 1][4] = {};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint4 q[2][2];
@@ -858,14 +898,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
                     for (int i = 0; i < 2; ++i)
                         q[m][i] = *reinterpret_cast<const uint4 *>(at + warp * 4096 + m * 2048 + half * 1024 + i * 512 + lane * 16);
                 const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
-                chunk_products<FMT, NT, 2, PC, RAW>(q, n, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
+                chunk_products<FMT, NT, 2, PC, RAW, 1>(q, n, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[m][nt][i] += PC == 2 ? rest[PC == 2 ? m : 0][PC == 2 ? nt : 0][i] : acc[m][nt][i];
+                    for (int i = 0; i < 4; ++i) sum[m][nt][i] += PC == 2 ? rest[0][PC == 2 ? m : 0][PC == 2 ? nt : 0][i] : acc[0][m][nt][i];
         }
         if (mine) {
             const unsigned short *order = pl.order + pl.first[r.c];
@@ -933,10 +973,9 @@ MoeWay moe_way_of(int kind, int pieces, int S, int lines) {
     }
     w.nc = S < kFewColumns ? S : kFewColumns;
     const size_t fixed = kind ? FewShape<8, 4>::kB : FewShape<16, 3>::kB, room = (kind ? 113 * 1024 : 227 * 1024) - fixed;
-    // a column is 64 bytes off a 128-byte multiple: no bank conflicts; 512 blocks of 32 units have their sums' places
+    // a column is 64 bytes off a 128-byte multiple: no bank conflicts
     auto most = [&](int ns) {
-        const long long per = (lines + ns - 1) / ns, bytes = (long long)room / ((per * 16 * KC + 64) * pieces), sums = 512 / ((per * KC + 31) / 32);
-        const long long n = bytes < sums ? bytes : sums;
+        const long long n = (long long)room / (((lines + ns - 1ll) / ns * 16 * KC + 64) * pieces);
         return (int)(n < kFewHeld ? n : kFewHeld);
     };
     while (most(w.ns) < w.nc) ++w.ns;
