@@ -1,6 +1,7 @@
 // Shared by the files of the experts' layer.
 #pragma once
 
+#include "launch.h"
 #include "qwq_internal.h"
 
 namespace qwq {
@@ -65,22 +66,5 @@ MOE_FORMAT(B200Q_I2);
 // f16 pieces of a column: f32 needs two for its 24 bits; h of f16 rows two, so
 // that its rounding is below y's; f16 and bf16 are exact in one.
 inline int moe_pieces(int type, bool down) { return type == B200Q_T_F32 || (down && type == B200Q_T_F16) ? 2 : 1; }
-
-template <class K, class... P>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const P &...p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p...);
-    count_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
 
 }  // namespace qwq

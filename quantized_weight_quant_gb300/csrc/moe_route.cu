@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "launch.h"
 #include "qwq_internal.h"
 
 namespace qwq {
@@ -265,19 +266,8 @@ cudaError_t start(const Route &a, cudaStream_t st) {
     const int warps = a.S > 2 * sm_count(dev) ? kWarps : 1;
     // a row's logits, and where there are groups their c as f64
     const int row_bytes = ((a.E + (a.E & 1)) * 4 + (a.n_group > 1 ? a.E * 8 : 0) + 15) & ~15;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.S + (long long)warps - 1) / warps));
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = (size_t)warps * row_bytes;            // at most 4 * 12 KB
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, moe_route_kernel<T, NV>, a, row_bytes);
-    count_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(moe_route_kernel<T, NV>, dim3((unsigned)((a.S + (long long)warps - 1) / warps)), 32 * warps,
+                            (size_t)warps * row_bytes, st, a, row_bytes);          // at most 4 * 12 KB
 }
 
 template <class T>
