@@ -9,16 +9,6 @@ namespace qwq {
 constexpr int kMoePairs = 1024;               // slots of a launch at most
 constexpr int kMoeTokens = 64;                // tokens of a launch at most
 
-// Division of a number below 2^31 by a fixed one, without the instructions of a
-// division.
-struct Quotient {
-    unsigned long long by;                    // 2^64 / d + 1; 0: d = 1
-    explicit Quotient(unsigned d = 1) : by(d > 1 ? ~0ull / d + 1 : 0) {}
-#ifdef __CUDACC__
-    __device__ __forceinline__ int operator()(int v) const { return by ? (int)__umul64hi((unsigned long long)v, by) : v; }
-#endif
-};
-
 // One of the two products: gate and up of the tokens' rows, or down of h.
 struct MoeStream {
     const Expert *table;

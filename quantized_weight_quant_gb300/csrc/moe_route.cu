@@ -28,8 +28,11 @@ __device__ __forceinline__ float load(const float *p) { return *p; }
 __device__ __forceinline__ float load(const __half *p) { return __half2float(*p); }
 __device__ __forceinline__ float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+// What decides first: within 1e-6 of the scores is enough (keys_of's distances).
+__device__ __forceinline__ float exp_of(float v) { return __expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float ratio(float a, float b) { return __fdividef(a, b); }
+__device__ __forceinline__ double ratio(double a, double b) { return a / b; }
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
 
@@ -69,13 +72,91 @@ __device__ __forceinline__ float exp_diff(float a, float b) {
     return err == err ? expf(d) * (1.f + err) : expf(d);
 }
 
-// One token's row: the logits in this warp's registers and its shared memory.
+// One token's row: in this warp's registers, the logits in its shared memory too.
 template <int NV> struct Row {
-    float l[NV];                             // logit of expert lane + 32 i, -infinity past E
+    float l[NV], bias[NV];                   // logit and bias of expert lane + 32 i, -infinity and 0 past E
     float *sm;                               // the same, by expert
     float top, sum;                          // softmax: the largest finite logit, sum exp(l - top) of those
     bool nan;
 };
+
+__device__ __forceinline__ unsigned first_lane(bool is) { return __ffs(__ballot_sync(kAll, is)) - 1; }
+
+// The values of the groups, lane g that of group g, from c's keys: of groups of
+// 32 m neighbours the m registers' two largest over the warp; of 2, 4, 8 or 16 neighbours
+// over as many lanes; of another number by a walk over c in shared memory.
+template <int NV>
+__device__ __forceinline__ float group_values(const Route &p, int lane, int n, const unsigned (&kc)[NV], float *by) {
+    unsigned a = 0, b = 0;                   // of this lane's group: the two largest keys
+    if (n % 32 == 0) {
+        unsigned ga = 0, gb = 0;
+        int g = 0, left = n / 32;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const unsigned x = __reduce_max_sync(kAll, kc[i]), at = first_lane(kc[i] == x);
+            const unsigned y = p.group_top > 1 ? __reduce_max_sync(kAll, lane == (int)at ? 0u : kc[i]) : 0u;
+            gb = max(min(ga, x), max(gb, y));
+            ga = max(ga, x);
+            if (--left == 0) {
+                if (lane == g) a = ga, b = gb;
+                ga = gb = 0;
+                ++g;
+                left = n / 32;
+            }
+        }
+    } else if (n < 32 && (n & (n - 1)) == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unsigned x = kc[i], y = 0;
+            for (int o = 1; o < n; o <<= 1) {
+                const unsigned ox = __shfl_xor_sync(kAll, x, o), oy = __shfl_xor_sync(kAll, y, o);
+                y = max(min(x, ox), max(y, oy));
+                x = max(x, ox);
+            }
+            // group g is in register i = g n / 32, from lane g n % 32 on
+            const int from = lane * n;
+            const unsigned gx = __shfl_sync(kAll, x, from & 31), gy = __shfl_sync(kAll, y, from & 31);
+            if (from >> 5 == i) a = gx, b = gy;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + 32 * i < p.E) by[lane + 32 * i] = __uint_as_float(kc[i]);
+        __syncwarp();
+        if (lane < p.n_group) {
+            int j = lane % n;                // lanes begin at different places: no bank conflicts
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                const unsigned v = __float_as_uint(by[lane * n + j]);
+                b = max(min(a, v), b);
+                a = max(a, v);
+                if (++j == n) j = 0;
+            }
+        }
+        __syncwarp();
+    }
+    if (a == 0) return -INFINITY;
+    return value_of(a) + (p.group_top > 1 && b ? value_of(b) : 0.f);
+}
+template <int NV>
+__device__ __forceinline__ double group_values(const Route &p, int lane, int n, const unsigned long long (&kc)[NV], double *by) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (lane + 32 * i < p.E) by[lane + 32 * i] = __longlong_as_double((long long)kc[i]);
+    __syncwarp();
+    unsigned long long a = 0, b = 0;
+    if (lane < p.n_group) {
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            const unsigned long long v = (unsigned long long)__double_as_longlong(by[lane * n + t]);
+            b = max(min(a, v), b);
+            a = max(a, v);
+        }
+    }
+    __syncwarp();
+    if (a == 0) return -INFINITY;
+    return value_of(a) + (p.group_top > 1 && b ? value_of(b) : 0.);
+}
 
 // Keys of c in the arithmetic of V; the groups that do not stay have key 0.
 // *near: a decision was nearer than V's errors (f32 only).
@@ -90,49 +171,28 @@ __device__ __forceinline__ void keys_of(const Route &p, const Row<NV> &r, int la
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     }
-    auto score = [&](float l) {
-        if (p.score == B200Q_SCORE_SOFTMAX) return finite(l) ? exp_of((V)l - (V)r.top) / sum : (V)0;
-        return (V)1 / ((V)1 + exp_of(-(V)l));
-    };
     // c, or where nothing but its order counts, the logit
     const bool scored = p.bias || (p.n_group > 1 && p.group_top > 1);
-    V c[NV];
+    typename Key<V>::T kc[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        c[i] = (V)r.l[i];
-        if (r.l[i] != r.l[i]) c[i] = -INFINITY;
-        if (scored && c[i] > -INFINITY) {
-            c[i] = score(r.l[i]);
-            if (p.bias) c[i] += (V)p.bias[e];
+        const float l = r.l[i];
+        V c = (V)l;
+        if (scored) {
+            if (p.score == B200Q_SCORE_SOFTMAX) c = finite(l) ? ratio(exp_of((V)l - (V)r.top), sum) : (V)0;
+            else c = ratio((V)1, (V)1 + exp_of(-(V)l));
+            c += (V)r.bias[i];
         }
-        key[i] = key_of(c[i]);
-        if (!p.bias) key[i] = (typename Key<V>::T)(e < p.E ? key_of((V)(r.l[i])) : key_of((V)-INFINITY));
+        kc[i] = l > -INFINITY ? key_of(c) : (typename Key<V>::T)0;
+        key[i] = p.bias ? kc[i] : key_of((V)l);
     }
     if (p.n_group == 1) return;
-    // a lane per group; c by expert, in the arithmetic of V
-    V *by = reinterpret_cast<V *>(r.sm + p.E + (p.E & 1));
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (lane + 32 * i < p.E) by[lane + 32 * i] = key_of(c[i]) ? c[i] : (V)-INFINITY;
-    __syncwarp();
     const int n = p.E / p.n_group;
-    V a = -INFINITY, b = -INFINITY;          // the group's two largest
-    if (lane < p.n_group) {
-        int j = lane % n;                    // lanes begin at different places: no bank conflicts
-        for (int t = 0; t < n; ++t) {
-            const V v = by[lane * n + j];
-            b = v > a ? a : v > b ? v : b;
-            a = v > a ? v : a;
-            if (++j == n) j = 0;
-        }
-    }
-    V value = a;
-    if (p.group_top > 1 && b > -INFINITY) value += b;
-    __syncwarp();
+    const V value = group_values<NV>(p, lane, n, kc, reinterpret_cast<V *>(r.sm + p.E + (p.E & 1)));
     // place: how many groups have a larger value, or the same and a lower index
     int place = 0;
     V least = INFINITY;                      // to the next lower or equal value
+#pragma unroll 1
     for (int g = 0; g < p.n_group; ++g) {
         const V o = __shfl_sync(kAll, value, g);
         if (o > value || (o == value && g < lane)) ++place;
@@ -142,25 +202,28 @@ __device__ __forceinline__ void keys_of(const Route &p, const Row<NV> &r, int la
     if (near && scored) {
         // only the last group that stays has to be told from the next.  A value that is infinite or NaN is left to f64.
         const bool last = lane < p.n_group && place == p.topk_group - 1 && p.topk_group < p.n_group && value > -INFINITY;
-        const float eps = (p.score == B200Q_SCORE_SOFTMAX ? 1.2e-5f : 4e-6f) + 5e-7f * fabsf((float)value);
+        const float eps = (p.score == B200Q_SCORE_SOFTMAX ? 1.2e-5f : 1.8e-6f) + 3e-7f * fabsf((float)value);
         if (__any_sync(kAll, last && !((float)least > eps))) *near = true;
     }
+    const Quotient &by_n = p.by_group;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = lane + 32 * i;
-        if (e < p.E && !(stays >> (e / n) & 1u)) key[i] = 0;
+        if (e < p.E && !(stays >> by_n(e) & 1u)) key[i] = 0;
     }
 }
 
 // The k largest keys, descending, equal ones by index: lane j gets the j-th
-// expert, or -1.  near: as above, of neighbouring choices.
+// expert, or -1.  near: as above, of neighbouring choices, the last and the one after
+// it (lane k's) among them; *least is then the least value of those.
 template <class V, int NV>
-__device__ __forceinline__ int select(const Route &p, int lane, typename Key<V>::T (&key)[NV], bool *near) {
+__device__ __forceinline__ int select(const Route &p, int lane, typename Key<V>::T (&key)[NV], bool *near, float *least) {
     using K = typename Key<V>::T;
     int mine = -1;
-    const float eps = p.score == B200Q_SCORE_SOFTMAX ? 6e-6f : 2e-6f;
+    const float eps = p.score == B200Q_SCORE_SOFTMAX ? 6e-6f : 9e-7f;
     float before = INFINITY;
-    const int rounds = near && p.bias ? p.k + 1 : p.k;       // one more: what the last choice was told from
+    const int rounds = near && p.bias ? p.k + 1 : p.k;
+#pragma unroll 1
     for (int j = 0; j < rounds; ++j) {
         K best = 0;
         int at = 0;
@@ -172,15 +235,53 @@ __device__ __forceinline__ int select(const Route &p, int lane, typename Key<V>:
         const unsigned e = __reduce_min_sync(kAll, best == top ? (unsigned)(lane + 32 * at) : kAll);
         if (near && p.bias) {
             const float v = (float)value_of(top);
-            if (j > 0 && !(before - v > eps + 2.5e-7f * fabsf(v))) *near = true;
+            if (j > 0 && !(before - v > eps + 1.5e-7f * fabsf(v))) *near = true;
             before = v;
         }
-        if (j < p.k && lane == j) mine = (int)e;
+        if (lane == j) mine = (int)e;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if ((unsigned)(lane + 32 * i) == e) key[i] = 0;
     }
+    if (least) *least = before;
     return mine;
+}
+
+// Where f32 left the order of neighbouring choices open: those that it looked at
+// (id), and what is no further below the last of them than its errors, are ranked
+// in 64 bits, a lane each.  key: what is left of the row's, f32.  false: more than
+// 32 of them, or a softmax, which needs the whole row.
+template <int NV>
+__device__ __forceinline__ bool rank_again(const Route &p, const Row<NV> &r, int lane, const unsigned (&key)[NV], float least, int &id) {
+    const float floor_ = least - 9e-7f - 1.5e-7f * fabsf(least);
+    if (!finite(floor_) || p.score == B200Q_SCORE_SOFTMAX || p.k == 32) return false;
+    int have = __popc(__ballot_sync(kAll, id >= 0)), mine = id;
+    const unsigned low = key_of(floor_);
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i) {
+        unsigned k = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j == i) k = key[j];
+        unsigned in = __ballot_sync(kAll, k != 0 && k >= low);
+        if (have + __popc(in) > 32) return false;
+#pragma unroll 1
+        for (; in; in &= in - 1, ++have)
+            if (lane == have) mine = 32 * i + __ffs(in) - 1;
+    }
+    unsigned long long k64 = 0;
+    if (lane < have) k64 = key_of(1.0 / (1.0 + exp(-(double)r.sm[mine])) + (double)p.bias[mine]);
+    int got = -1;
+#pragma unroll 1
+    for (int j = 0; j < p.k; ++j) {
+        const unsigned long long top = warp_max(k64);
+        if (top == 0) break;
+        const unsigned e = __reduce_min_sync(kAll, k64 == top ? (unsigned)mine : kAll);
+        if (lane == j) got = (int)e;
+        if (k64 == top && mine == (int)e) k64 = 0;
+    }
+    id = got;
+    return true;
 }
 
 template <class T, int NV>
@@ -200,11 +301,13 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const Route p, i
 #pragma unroll
     for (int i = 0; i < NV; ++i) r.l[i] = lane + 32 * i < p.E ? load(src + lane + 32 * i) : -INFINITY;
 #pragma unroll
+    for (int i = 0; i < NV; ++i) r.bias[i] = p.bias && lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.f;
+#pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = lane + 32 * i;
         if (e < p.E) {
             r.sm[e] = r.l[i];
-            r.nan |= r.l[i] != r.l[i] || (p.bias && p.bias[e] != p.bias[e]);
+            r.nan |= r.l[i] != r.l[i] || r.bias[i] != r.bias[i];
         }
         if (finite(r.l[i])) r.top = fmaxf(r.top, r.l[i]);
         else r.nan |= p.score == B200Q_SCORE_SOFTMAX && r.l[i] > 0.f;      // infinity / infinity
@@ -214,19 +317,22 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const Route p, i
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) r.top = fmaxf(r.top, __shfl_xor_sync(kAll, r.top, o));
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r.sum += finite(r.l[i]) ? expf(r.l[i] - r.top) : 0.f;
+        for (int i = 0; i < NV; ++i) r.sum += finite(r.l[i]) ? __expf(r.l[i] - r.top) : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) r.sum += __shfl_xor_sync(kAll, r.sum, o);
     }
-    bool near = false;
+    bool near = false, near_groups = false;
     unsigned key[NV];
-    keys_of<float>(p, r, lane, key, &near);
-    int id = select<float>(p, lane, key, &near);
-    if (near) {
+    float least;
+    __syncwarp();                            // the logits in shared memory
+    keys_of<float>(p, r, lane, key, &near_groups);
+    int id = select<float>(p, lane, key, &near, &least);
+    if (near_groups || (near && !rank_again(p, r, lane, key, least, id))) {
         unsigned long long k64[NV];
         keys_of<double>(p, r, lane, k64, nullptr);
-        id = select<double>(p, lane, k64, nullptr);
+        id = select<double>(p, lane, k64, nullptr, nullptr);
     }
+    if (lane >= p.k) id = -1;
     __syncwarp();
     // weights: lane j its own.  With norm only the ratios count: they are taken
     // relative to the largest logit chosen (capped at 0 for the sigmoid), so that
@@ -265,9 +371,11 @@ cudaError_t start(const Route &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int warps = a.S > 2 * sm_count(dev) ? kWarps : 1;
     // a row's logits, and where there are groups their c as f64
+    Route p = a;
+    p.by_group = Quotient(a.E / a.n_group);
     const int row_bytes = ((a.E + (a.E & 1)) * 4 + (a.n_group > 1 ? a.E * 8 : 0) + 15) & ~15;
     return launch_dependent(moe_route_kernel<T, NV>, dim3((unsigned)((a.S + (long long)warps - 1) / warps)), 32 * warps,
-                            (size_t)warps * row_bytes, st, a, row_bytes);          // at most 4 * 12 KB
+                            (size_t)warps * row_bytes, st, p, row_bytes);          // at most 4 * 12 KB
 }
 
 template <class T>

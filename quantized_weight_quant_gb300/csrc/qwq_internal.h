@@ -157,6 +157,16 @@ cudaError_t launch_gemm_q8(const MatQ8 &a, cudaStream_t st);
 
 // ---- the mixture-of-experts block
 
+// Division of a number below 2^31 by a fixed one, without the instructions of a
+// division.
+struct Quotient {
+    unsigned long long by;                    // 2^64 / d + 1; 0: d = 1
+    explicit Quotient(unsigned d = 1) : by(d > 1 ? ~0ull / d + 1 : 0) {}
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int v) const { return by ? (int)__umul64hi((unsigned long long)v, by) : v; }
+#endif
+};
+
 // Scores, grouped top-k and weights of S tokens over E experts.
 struct Route {
     const void *logits;
@@ -168,6 +178,7 @@ struct Route {
     float scale;
     int *ids;
     float *wts;
+    Quotient by_group;         // an expert's group: set by the launch
 };
 constexpr int kRouteMaxE = 1024, kRouteMaxK = 32, kRouteMaxGroups = 32;
 cudaError_t launch_moe_route(const Route &a, cudaStream_t st);
