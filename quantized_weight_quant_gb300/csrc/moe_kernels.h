@@ -294,14 +294,14 @@ __device__ __forceinline__ void put(const MoeStream &p, int slice, int slot, int
 }
 
 // The products of a thread's 16 bytes of codes (of MT tiles, rows g and g + 8)
-// with NT x 8 columns, of which the first n are wanted; `from(nt)` is where this
+// with N x 8 columns of the NT x 8 that have sums; `from(nt)` is where this
 // thread's column of tile nt has its values, its second pieces `plane` bytes
 // further.  The words take NA accumulators in turn: an instruction waits for the
 // one before it on the same accumulator.  Two pieces: the first ones' sums are
 // taken out of the accumulator after every word of codes, the second ones are in
 // `rest`.
-template <int FMT, int NT, int MT, int PC, bool RAW, int NA, class From>
-__device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], int n, From from, int plane, float (&sum)[MT][NT][4],
+template <int FMT, int N, int NT, int MT, int PC, bool RAW, int NA, class From>
+__device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], From from, int plane, float (&sum)[MT][NT][4],
                                                float (&accs)[NA][MT][NT][4],
                                                float (&rests)[PC == 2 ? NA : 1][PC == 2 ? MT : 1][PC == 2 ? NT : 1][4]) {
     constexpr int MMAS = Fmt<FMT>::MMAS;
@@ -327,8 +327,7 @@ __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], int n, F
             }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && nt * 8 >= n) break;
+        for (int nt = 0; nt < N; ++nt) {
 #pragma unroll
             for (int pc = 0; pc < PC; ++pc) {
                 const uint8_t *at = from(nt) + pc * plane;
@@ -650,8 +649,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                 if (ok) copy_line();
                 constexpr int NA = PC == 2 ? 2 : 4;
                 float acc[NA][1][1][4] = {}, rest[PC == 2 ? NA : 1][1][1][4] = {};
-                chunk_products<FMT, 1, 1, PC, RAW, NA>(q, n, [&](int) { return xb; }, p.held * p.pitch, sum, acc, rest);
-                chunk_products<FMT, 1, 1, PC, RAW, NA>(next, n, [&](int) { return xb + 8 * KC; }, p.held * p.pitch, sum, acc, rest);
+                chunk_products<FMT, 1, 1, 1, PC, RAW, NA>(q, [&](int) { return xb; }, p.held * p.pitch, sum, acc, rest);
+                chunk_products<FMT, 1, 1, 1, PC, RAW, NA>(next, [&](int) { return xb + 8 * KC; }, p.held * p.pitch, sum, acc, rest);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if constexpr (PC == 2) sum[0][0][i] += rest[0][0][0][i] + rest[1][0][0][i];
@@ -695,18 +694,22 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
 // ---------------------------------------------------------------- many columns
 // Up to 32 columns of an expert, prepared in memory once and copied line by line
 // beside the codes, in stages that the whole block shares: a warp keeps the sums
-// of 32 rows with all columns over the rows' whole length.
-constexpr int kManyWarps = 8, kManyThreads = 32 * kManyWarps;
+// of 16 rows with all columns over the rows' whole length.
+template <int N> struct Count {
+    static constexpr int value = N;
+};
+constexpr int kManyWarps = 16, kManyThreads = 32 * kManyWarps;
 template <int FMT, int PC> constexpr int kManyColumns = FMT == B200Q_I2 && PC == 2 ? 16 : 32;
 template <int FMT, int PC> constexpr int kManyStages = FMT == B200Q_I8 || (FMT == B200Q_I4 && PC == 1) ? 4 : 3;
 template <int FMT, int PC> struct ManyShape {
     static constexpr int kPitch = 16 * Fmt<FMT>::KC + 64;              // of a column's line: no bank conflicts
     static constexpr int kPlane = kManyColumns<FMT, PC> * kPitch;
-    static constexpr int kCodes = kManyWarps * 4096;
+    static constexpr int kCodes = kManyWarps * 2048;
     static constexpr int kStage = kCodes + PC * kPlane;
-    static constexpr int kPlanAt = kManyStages<FMT, PC> * kStage;      // the plan's scratch lies in the stages before
-    static constexpr int kInfoAt = (kPlanAt + (int)sizeof(Plan) + 15) / 16 * 16;
-    static constexpr int kBytes = kInfoAt + 2 * 32 * 8;
+    static_assert(kStage % 1024 == 0, "a box of codes is swizzled by its address");
+    static constexpr int kBarsAt = kManyStages<FMT, PC> * kStage;      // the plan's scratch lies in the stages before
+    static constexpr int kPlanAt = kBarsAt + 2 * 8 * kManyStages<FMT, PC>;
+    static constexpr int kBytes = kPlanAt + (int)sizeof(Plan);
 };
 
 // A row of the tokens, or of h, per block, as pieces of f16 in the order of the
@@ -770,160 +773,154 @@ template <int FMT, int PC, bool RAW>
 __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_constant__ MoeStream p) {
     using Sh = ManyShape<FMT, PC>;
     constexpr int KC = Fmt<FMT>::KC, NT = kManyColumns<FMT, PC> / 8, STAGES = kManyStages<FMT, PC>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     Plan &pl = *reinterpret_cast<Plan *>(smem + Sh::kPlanAt);
-    float2 *info = reinterpret_cast<float2 *>(smem + Sh::kInfoAt);     // [2][32], of two chunks in turn
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+    const int row = (g & 1) << 2 | g >> 1;     // of a box: as in the kernel for few columns
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), full = base + Sh::kBarsAt, empty = full + 8 * STAGES;
 
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * STAGES; ++i)   // every warp brings its part of a stage, and lets go of it
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(full + 8 * i), "r"(kManyWarps) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     // the ids were there when the kernel that prepares the rows began
     make_plan(p, pl, *reinterpret_cast<PlanScratch *>(smem));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");       // the scratch was written here, the stages are by copies
+    __syncthreads();
     dependency_wait();
     let_dependents_start();
-    const int units = (p.tiles + 1) / 2;       // pairs of tiles
-    const int all = pl.chunks * units, each = p.by_grid(all), more = all - each * (int)gridDim.x;
+    const int all = pl.chunks * p.tiles, each = p.by_grid(all), more = all - each * (int)gridDim.x;
     const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
 
-    // A round: up to 8 units of one chunk, a warp each, over the whole length of
-    // the rows.  A chunk's rounds share its units evenly.
+    // A round: up to 16 tiles of one chunk, a warp each, over the whole length of the
+    // rows.  A chunk's rounds share its tiles evenly.
     struct Round {
-        int u, c, n;                           // the first unit, its chunk, units
+        int u, c, n;                           // the first tile, its chunk, tiles
     };
     auto begin = [&](Round &r, int u) {
         r.u = u;
         r.n = 0;
         if (u >= hi) return;
-        r.c = u / units;
-        const int left = min(hi, (r.c + 1) * units) - u, rounds = (left + kManyWarps - 1) / kManyWarps;
+        r.c = p.by_tiles(u);
+        const int left = min(hi, (r.c + 1) * p.tiles) - u, rounds = (left + kManyWarps - 1) / kManyWarps;
         r.n = (left + rounds - 1) / rounds;
     };
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-    const uint64_t policy = stream_policy();
-    const long long tile_bytes = (p.down ? 16 : 8) * p.ld, row_bytes = (long long)PC * p.lines * (16 * KC);
 
-    // the copy cursor
+    // this warp's copies of the next stage: its tile's line, and every 16th column's
     Round f = {};
-    int fline = 0, fstage = 0, fn = 0;
-    const uint8_t *f0[2] = {}, *f1[2] = {};
-    const unsigned short *forder = nullptr;
-    auto open = [&]() {
-        if (f.n == 0) return;
-        fline = 0;
-        forder = pl.order + pl.first[f.c];
-        fn = pl.n[f.c];
+    int fline = 0, fstage = 0;
+    const uint64_t policy = stream_policy();
+    auto copy_stage = [&]() {                  // lane 0
+        if (!f.n) return;
+        const uint32_t to = base + fstage * Sh::kStage, bar = full + 8 * fstage;
+        const int n = pl.n[f.c], columns = (n - warp + kManyWarps - 1) / kManyWarps;        // of this warp
+        const int bytes = (warp < f.n ? 2048 : 0) + (columns > 0 ? columns : 0) * PC * (16 * KC);
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
         if (warp < f.n) {
-            const Expert &e = p.table[pl.expert[f.c]];
-            const int tile = (f.u + warp - f.c * units) * 2;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {      // a tile past the last reads the last again
-                const long long off = min(tile + m, p.tiles - 1) * tile_bytes + g * p.ld + tig * 16;
-                f0[m] = (p.down ? e.codes[2] : e.codes[0]) + off;
-                f1[m] = (p.down ? e.codes[2] + 8 * p.ld : e.codes[1]) + off;
-            }
+            const CUtensorMap *map = p.table[pl.expert[f.c]].map + (p.down ? 2 : 0);
+            const int y = (f.u + warp - f.c * p.tiles) * (p.down ? 16 : 8);
+            copy_box(to + warp * 2048, map, fline * 128, y, bar, policy);
+            copy_box(to + warp * 2048 + 1024, p.down ? map : map + 1, fline * 128, p.down ? y + 8 : y, bar, policy);
         }
-    };
-    auto copy_line = [&]() {
-        if (f.n) {
-            const uint32_t to = base + fstage * Sh::kStage;
-            if (warp < f.n) {
+#pragma unroll 1
+        for (int c = warp; c < n; c += kManyWarps) {
+            const int slot = pl.order[pl.first[f.c] + c];
+            const uint8_t *from = p.cols + ((long long)(p.down ? slot : p.by_k(slot)) * PC * p.lines + fline) * (16 * KC);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t t = to + warp * 4096 + m * 2048 + lane * 16;
-                    copy16_stream(t, f0[m], policy);
-                    copy16_stream(t + 512, f1[m], policy);
-                    copy16_stream(t + 1024, f0[m] + 64, policy);
-                    copy16_stream(t + 1536, f1[m] + 64, policy);
-                    f0[m] += 128;
-                    f1[m] += 128;
-                }
-            }
-            for (int i = tid; i < fn * PC * KC; i += kManyThreads) {   // 16 bytes each
-                const int c = i / (PC * KC), pc = i / KC % PC, j = i % KC, slot = forder[c];
-                const int row = p.down ? slot : p.by_k(slot);
-                copy16(to + Sh::kCodes + pc * Sh::kPlane + c * Sh::kPitch + j * 16,
-                       p.cols + row * row_bytes + ((long long)pc * p.lines + fline) * (16 * KC) + j * 16);
-            }
-            if (++fstage == STAGES) fstage = 0;
-            if (++fline == p.lines) {
-                begin(f, f.u + f.n);
-                open();
-            }
+            for (int pc = 0; pc < PC; ++pc)
+                copy_bulk(to + Sh::kCodes + pc * Sh::kPlane + c * Sh::kPitch, from + (long long)pc * p.lines * (16 * KC), 16 * KC, bar);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++fstage == STAGES) fstage = 0;
+        if (++fline == p.lines) {
+            fline = 0;
+            begin(f, f.u + f.n);
+        }
     };
     begin(f, lo);
-    open();
-    __syncthreads();                           // the plan's scratch is read
+    if (lane == 0) {
 #pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) copy_line();
-
-    int stage = 0, turn = 0, chunk = -1;
+        for (int i = 0; i < STAGES; ++i) copy_stage();
+    }
+    int stage = 0, before = 0;                 // the stage that is read, the one that was
+    uint32_t parity = 0, parity_before = 0;
+    bool ok = true;                            // false: a copy did not come, or a warp did not let go: nothing more is waited for
     Round r = {};
     begin(r, lo);
+#pragma unroll 1
     while (r.n) {
-        if (r.c != chunk) {                    // read after this round's first barrier at the earliest
-            turn ^= 1;
-            if (tid < pl.n[r.c]) {
-                const int slot = pl.order[pl.first[r.c] + tid];
-                info[turn * 32 + tid] = p.info[p.down ? slot : p.by_k(slot)];
-            }
-            chunk = r.c;
-        }
-        const int n = pl.n[r.c], tile = (r.u + warp - r.c * units) * 2;
+        const int n = pl.n[r.c], tile = r.u + warp - r.c * p.tiles;
         const bool mine = warp < r.n;
-        float sum[2][NT][4] = {}, sa[2] = {}, sb[2] = {};
+        float sum[1][NT][4] = {}, sa = 0.f, sb = 0.f;
         if (mine) {
             const Expert &e = p.table[pl.expert[r.c]];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int t = min(tile + m, p.tiles - 1) * (p.down ? 16 : 8) + g;
-                sa[m] = (p.down ? e.scales[2] : e.scales[0])[t];
-                sb[m] = (p.down ? e.scales[2] + 8 : e.scales[1])[t];
-            }
+            const int o = tile * (p.down ? 16 : 8) + row;
+            sa = (p.down ? e.scales[2] : e.scales[0])[o];
+            sb = (p.down ? e.scales[2] + 8 : e.scales[1])[o];
         }
 #pragma unroll 1
         for (int line = 0; line < p.lines; ++line) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-            __syncthreads();                   // this stage is there for all, the one before is read by all
-            copy_line();
+            if (ok) ok = mbar_wait(full + 8 * stage, parity, kMoeWaitNs);
             const uint8_t *at = smem + stage * Sh::kStage;
-            if (++stage == STAGES) stage = 0;
-            if (!mine) continue;
-            float acc[1][2][NT][4] = {}, rest[1][PC == 2 ? 2 : 1][PC == 2 ? NT : 1][4] = {};
+            // N: the tiles of columns that the chunk has; without a branch between their instructions
+            auto products = [&](auto tiles) {
+                constexpr int N = decltype(tiles)::value;
+                float acc[1][1][NT][4] = {}, rest[1][1][PC == 2 ? NT : 1][4] = {};
+                const uint8_t *codes = at + warp * 2048 + row * 128 + ((tig ^ row) << 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint4 q[2][2];
+                for (int half = 0; half < 2; ++half) {
+                    const uint8_t *from = reinterpret_cast<const uint8_t *>((uintptr_t)codes ^ (half * 64));
+                    uint4 q[1][2];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                    for (int i = 0; i < 2; ++i) q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 1024);
+                    const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
+                    chunk_products<FMT, N, NT, 1, PC, RAW, 1>(q, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
+                }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        q[m][i] = *reinterpret_cast<const uint4 *>(at + warp * 4096 + m * 2048 + half * 1024 + i * 512 + lane * 16);
-                const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
-                chunk_products<FMT, NT, 2, PC, RAW, 1>(q, n, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
+                for (int nt = 0; nt < N; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[0][nt][i] += PC == 2 ? rest[0][0][PC == 2 ? nt : 0][i] : acc[0][0][nt][i];
+            };
+            if (mine) {
+                if (n <= 8) products(Count<1>{});
+                else if (n <= 16) products(Count<2>{});
+                else if (NT > 2 && n <= 24) products(Count<NT < 3 ? NT : 3>{});
+                else products(Count<NT>{});
             }
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[m][nt][i] += PC == 2 ? rest[0][PC == 2 ? m : 0][PC == 2 ? nt : 0][i] : acc[0][m][nt][i];
+            __syncwarp();
+            if (lane == 0) {
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty + 8 * stage) : "memory");
+                // the stage before this one is let go by all, or soon: filled again
+                if (r.u != lo || line) {
+                    if (f.n && ok) ok = mbar_wait(empty + 8 * before, parity_before, kMoeWaitNs);
+                    if (ok) copy_stage();
+                }
+            }
+            before = stage, parity_before = parity;
+            if (++stage == STAGES) stage = 0, parity ^= 1;
         }
         if (mine) {
             const unsigned short *order = pl.order + pl.first[r.c];
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int c = nt * 8 + 2 * tig + j;
-                        if (c < n && tile + m < p.tiles) {
-                            const float2 i = info[turn * 32 + c];
-                            put(p, 0, order[c], tile + m, g, product<RAW>(sum[m][nt][j], i.y, sa[m], i.x),
-                                product<RAW>(sum[m][nt][2 + j], i.y, sb[m], i.x));
-                        }
+                for (int j = 0; j < 2; ++j) {
+                    const int c = nt * 8 + 2 * tig + j;
+                    if (c < n) {
+                        const int slot = order[c];
+                        const float2 i = p.info[p.down ? slot : p.by_k(slot)];
+                        put(p, 0, slot, tile, row, product<RAW>(sum[0][nt][j], i.y, sa, i.x), product<RAW>(sum[0][nt][2 + j], i.y, sb, i.x));
                     }
+                }
         }
         begin(r, r.u + r.n);
+    }
+    if (!ok) {
+        // gave up: say so, and let the copies in flight land
+        if (lane == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_ETIMEOUT));
+#pragma unroll 1
+        for (int i = 0; i < STAGES; ++i) mbar_wait(full + 8 * i, i < stage ? parity ^ 1 : parity, kMoeWaitNs / 8);
     }
 }
 
@@ -963,7 +960,7 @@ MoeWay moe_way_of(int kind, int pieces, int S, int lines) {
     MoeWay w{};
     w.kind = kind;
     w.ns = 1;
-    w.warps = kind == 0 ? 16 : 8;
+    w.warps = kind == 1 ? 8 : 16;
     w.blocks = kind == 1 ? 2 : 1;
     if (kind == 2) {
         w.nc = pieces == 2 ? kManyColumns<FMT, 2> : kManyColumns<FMT, 1>;
