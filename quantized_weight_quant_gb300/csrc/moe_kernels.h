@@ -852,7 +852,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
     while (r.n) {
         const int n = pl.n[r.c], tile = r.u + warp - r.c * p.tiles;
         const bool mine = warp < r.n;
-        float sum[1][NT][4] = {}, sa = 0.f, sb = 0.f;
+        // One piece: the sums stay in the accumulators (16-bit rows; what those drop of a row of 6144 is below 1e-4
+        // of a unit of the types' last places).  Two: they are taken out after every word of codes.
+        constexpr int NA = PC == 2 ? 1 : 2;
+        float sum[1][NT][4] = {}, acc[NA][1][NT][4] = {}, sa = 0.f, sb = 0.f;
         if (mine) {
             const Expert &e = p.table[pl.expert[r.c]];
             const int o = tile * (p.down ? 16 : 8) + row;
@@ -866,7 +869,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             // N: the tiles of columns that the chunk has; without a branch between their instructions
             auto products = [&](auto tiles) {
                 constexpr int N = decltype(tiles)::value;
-                float acc[1][1][NT][4] = {}, rest[1][1][PC == 2 ? NT : 1][4] = {};
+                float rest[1][1][PC == 2 ? NT : 1][4] = {};
                 const uint8_t *codes = at + warp * 2048 + row * 128 + ((tig ^ row) << 4);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -875,12 +878,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 #pragma unroll
                     for (int i = 0; i < 2; ++i) q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 1024);
                     const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
-                    chunk_products<FMT, N, NT, 1, PC, RAW, 1>(q, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
+                    chunk_products<FMT, N, NT, 1, PC, RAW, NA>(q, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
                 }
+                if constexpr (PC == 2) {
 #pragma unroll
-                for (int nt = 0; nt < N; ++nt)
+                    for (int nt = 0; nt < N; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[0][nt][i] += PC == 2 ? rest[0][0][PC == 2 ? nt : 0][i] : acc[0][0][nt][i];
+                        for (int i = 0; i < 4; ++i) sum[0][nt][i] += rest[0][0][nt][i];
+                }
             };
             if (mine) {
                 if (n <= 8) products(Count<1>{});
@@ -902,6 +907,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         }
         if (mine) {
             const unsigned short *order = pl.order + pl.first[r.c];
+            if constexpr (PC == 1) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[0][nt][i] = acc[0][0][nt][i] + acc[1][0][nt][i];
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
