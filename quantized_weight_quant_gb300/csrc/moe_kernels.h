@@ -791,73 +791,85 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
     __syncthreads();
     dependency_wait();
     let_dependents_start();
-    const int all = pl.chunks * p.tiles, each = p.by_grid(all), more = all - each * (int)gridDim.x;
-    const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
-
     // A round: up to 16 tiles of one chunk, a warp each, over the whole length of the
-    // rows.  A chunk's rounds share its tiles evenly.
-    struct Round {
-        int u, c, n;                           // the first tile, its chunk, tiles
-    };
-    auto begin = [&](Round &r, int u) {
-        r.u = u;
-        r.n = 0;
-        if (u >= hi) return;
-        r.c = p.by_tiles(u);
-        const int left = min(hi, (r.c + 1) * p.tiles) - u, rounds = (left + kManyWarps - 1) / kManyWarps;
-        r.n = (left + rounds - 1) / rounds;
+    // rows.  A chunk's rounds share its tiles evenly, a block takes an even run of rounds.
+    const int rounds = (p.tiles + kManyWarps - 1) / kManyWarps;        // of a chunk
+    const int all = pl.chunks * rounds, each = p.by_grid(all), more = all - each * (int)gridDim.x;
+    const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
+    auto tiles_of = [&](int u, int &c, int &from) {                    // round u's chunk, first tile and tiles
+        c = u / rounds;
+        from = (int)((long long)(u - c * rounds) * p.tiles / rounds);
+        return (int)((long long)(u - c * rounds + 1) * p.tiles / rounds) - from;
     };
 
     // this warp's copies of the next stage: its tile's line, and every 16th column's
-    Round f = {};
-    int fline = 0, fstage = 0;
+    int fu = lo, fline = 0, fstage = 0, fbytes = 0, fy = 0;
+    const CUtensorMap *map = nullptr;          // of the tile; none: the round has fewer tiles
+    const uint8_t *from[2] = {};               // of the columns (32 at most)
     const uint64_t policy = stream_policy();
-    auto copy_stage = [&]() {                  // lane 0
-        if (!f.n) return;
-        const uint32_t to = base + fstage * Sh::kStage, bar = full + 8 * fstage;
-        const int n = pl.n[f.c], columns = (n - warp + kManyWarps - 1) / kManyWarps;        // of this warp
-        const int bytes = (warp < f.n ? 2048 : 0) + (columns > 0 ? columns : 0) * PC * (16 * KC);
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-        if (warp < f.n) {
-            const CUtensorMap *map = p.table[pl.expert[f.c]].map + (p.down ? 2 : 0);
-            const int y = (f.u + warp - f.c * p.tiles) * (p.down ? 16 : 8);
-            copy_box(to + warp * 2048, map, fline * 128, y, bar, policy);
-            copy_box(to + warp * 2048 + 1024, p.down ? map : map + 1, fline * 128, p.down ? y + 8 : y, bar, policy);
+    const long long plane = (long long)p.lines * (16 * KC);
+    auto open = [&]() {
+        if (fu >= hi) return;
+        int c, first;
+        const int tiles = tiles_of(fu, c, first), n = pl.n[c];
+        fline = fbytes = 0;
+        map = nullptr;
+        if (warp < tiles) {
+            map = p.table[pl.expert[c]].map + (p.down ? 2 : 0);
+            fy = (first + warp) * (p.down ? 16 : 8);
+            fbytes = 2048;
         }
-#pragma unroll 1
-        for (int c = warp; c < n; c += kManyWarps) {
-            const int slot = pl.order[pl.first[f.c] + c];
-            const uint8_t *from = p.cols + ((long long)(p.down ? slot : p.by_k(slot)) * PC * p.lines + fline) * (16 * KC);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            from[i] = nullptr;
+            if (warp + i * kManyWarps < n) {
+                const int slot = pl.order[pl.first[c] + warp + i * kManyWarps];
+                from[i] = p.cols + (p.down ? slot : p.by_k(slot)) * (PC * plane);
+                fbytes += PC * (16 * KC);
+            }
+        }
+    };
+    auto copy_stage = [&]() {                  // lane 0
+        if (fu >= hi) return;
+        const uint32_t to = base + fstage * Sh::kStage, bar = full + 8 * fstage;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(fbytes) : "memory");
+        if (map) {
+            copy_box(to + warp * 2048, map, fline * 128, fy, bar, policy);
+            copy_box(to + warp * 2048 + 1024, p.down ? map : map + 1, fline * 128, p.down ? fy + 8 : fy, bar, policy);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!from[i]) break;
 #pragma unroll
             for (int pc = 0; pc < PC; ++pc)
-                copy_bulk(to + Sh::kCodes + pc * Sh::kPlane + c * Sh::kPitch, from + (long long)pc * p.lines * (16 * KC), 16 * KC, bar);
+                copy_bulk(to + Sh::kCodes + pc * Sh::kPlane + (warp + i * kManyWarps) * Sh::kPitch, from[i] + pc * plane, 16 * KC, bar);
+            from[i] += 16 * KC;
         }
         if (++fstage == STAGES) fstage = 0;
         if (++fline == p.lines) {
-            fline = 0;
-            begin(f, f.u + f.n);
+            ++fu;
+            open();
         }
     };
-    begin(f, lo);
     if (lane == 0) {
+        open();
 #pragma unroll 1
         for (int i = 0; i < STAGES; ++i) copy_stage();
     }
     int stage = 0, before = 0;                 // the stage that is read, the one that was
     uint32_t parity = 0, parity_before = 0;
     bool ok = true;                            // false: a copy did not come, or a warp did not let go: nothing more is waited for
-    Round r = {};
-    begin(r, lo);
 #pragma unroll 1
-    while (r.n) {
-        const int n = pl.n[r.c], tile = r.u + warp - r.c * p.tiles;
-        const bool mine = warp < r.n;
+    for (int u = lo; u < hi; ++u) {
+        int chunk, first;
+        const bool mine = warp < tiles_of(u, chunk, first);
+        const int n = pl.n[chunk], tile = first + warp;
         // One piece: the sums stay in the accumulators (16-bit rows; what those drop of a row of 6144 is below 1e-4
         // of a unit of the types' last places).  Two: they are taken out after every word of codes.
         constexpr int NA = PC == 2 ? 1 : 2;
         float sum[1][NT][4] = {}, acc[NA][1][NT][4] = {}, sa = 0.f, sb = 0.f;
         if (mine) {
-            const Expert &e = p.table[pl.expert[r.c]];
+            const Expert &e = p.table[pl.expert[chunk]];
             const int o = tile * (p.down ? 16 : 8) + row;
             sa = (p.down ? e.scales[2] : e.scales[0])[o];
             sb = (p.down ? e.scales[2] + 8 : e.scales[1])[o];
@@ -897,8 +909,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             if (lane == 0) {
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty + 8 * stage) : "memory");
                 // the stage before this one is let go by all, or soon: filled again
-                if (r.u != lo || line) {
-                    if (f.n && ok) ok = mbar_wait(empty + 8 * before, parity_before, kMoeWaitNs);
+                if (u != lo || line) {
+                    if (fu < hi && ok) ok = mbar_wait(empty + 8 * before, parity_before, kMoeWaitNs);
                     if (ok) copy_stage();
                 }
             }
@@ -906,7 +918,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             if (++stage == STAGES) stage = 0, parity ^= 1;
         }
         if (mine) {
-            const unsigned short *order = pl.order + pl.first[r.c];
+            const unsigned short *order = pl.order + pl.first[chunk];
             if constexpr (PC == 1) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -925,7 +937,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
                     }
                 }
         }
-        begin(r, r.u + r.n);
     }
     if (!ok) {
         // gave up: say so, and let the copies in flight land
