@@ -995,8 +995,11 @@ b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q
             else if (t.fmt != ex->fmt || t.O != (m == 2 ? ex->D : ex->F) || t.I != (m == 2 ? ex->F : ex->D))
                 rc = fail(B200Q_EINVAL, "%s: %s %d is not [%d, %d] in the first tensor's format", who,
                           m == 0 ? "gate" : m == 1 ? "up" : "down", e, m == 2 ? ex->D : ex->F, m == 2 ? ex->F : ex->D);
-            if (rc == B200Q_OK && !tmap_encode_2d(&host[e].map[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, t.codes, (uint64_t)t.ld,
-                                                  (uint64_t)t.o_pad, (uint64_t)t.ld, 128, 8, CU_TENSOR_MAP_SWIZZLE_128B))
+            auto encode = [&](CUtensorMap *map, int rows) {
+                return tmap_encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.codes, (uint64_t)t.ld, (uint64_t)t.o_pad,
+                                      (uint64_t)t.ld, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+            };
+            if (rc == B200Q_OK && !(encode(&host[e].map[m], 8) && encode(&host[e].wide[m], 64)))
                 rc = fail(B200Q_ECUDA, "%s: encoding a tensor map failed", who);
             host[e].codes[m] = t.codes;
             host[e].scales[m] = t.scales;

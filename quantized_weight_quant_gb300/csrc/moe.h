@@ -26,7 +26,7 @@ struct MoeStream {
     int nc, held, pitch;                      // columns of a chunk, of those staged together, bytes of one in shared memory
     bool down, aligned, prepared;             // aligned: the tokens' rows start on 16 bytes
     // prepared: rows in f16 pieces, their scales and sums
-    const uint8_t *cols;                      // [rows][pieces][lines][16 KC]
+    const uint8_t *cols;                      // as moe_prepare_kernel lays them out
     const float2 *info;                       // inverse scale, zero point times sum
 };
 
@@ -41,13 +41,13 @@ template <int FMT> MoeWay moe_way(int kind, int pieces, int S, int lines);
 
 template <int FMT> cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int n_sms, cudaStream_t st);
 // rows of the tokens, or of h, prepared for many columns
-template <int FMT> cudaError_t moe_launch_prepare(const MoeStream &p, int rows, uint8_t *cols, float2 *info, cudaStream_t st);
+template <int FMT> cudaError_t moe_launch_prepare(const MoeStream &p, int rows, bool ordered, uint8_t *cols, float2 *info, cudaStream_t st);
 
 // One translation unit per format has these.
 #define MOE_FORMAT(F)                                                                                          \
     template <> MoeWay moe_way<F>(int kind, int pieces, int S, int lines);                                     \
     extern template cudaError_t moe_launch_stream<F>(const MoeStream &, const MoeWay &, int, cudaStream_t);    \
-    extern template cudaError_t moe_launch_prepare<F>(const MoeStream &, int, uint8_t *, float2 *, cudaStream_t)
+    extern template cudaError_t moe_launch_prepare<F>(const MoeStream &, int, bool, uint8_t *, float2 *, cudaStream_t)
 MOE_FORMAT(B200Q_I8);
 MOE_FORMAT(B200Q_I4);
 MOE_FORMAT(B200Q_I2);

@@ -147,7 +147,8 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
     // Tokens' rows are prepared by a launch of their own where there are more than
     // two (every block would convert them all), h where there are many columns.
     const bool prepare = kind != 1 && S > 2;
-    const size_t n_x = prepare ? (size_t)S * pc_in * in_lines * 16 * KC : 0, n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * 16 * KC : 0;
+    const size_t n_x = kind == 2 ? (size_t)P * pc_in * in_lines * (16 * KC + 64) : prepare ? (size_t)S * pc_in * in_lines * 16 * KC : 0;
+    const size_t n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * (16 * KC + 64) : 0;
     const size_t n_info = prepare ? up16((size_t)P * 8) : 0;
     uint8_t *ws = nullptr;
     e = workspace_alloc((void **)&ws, n_h + n_part + (n_x > n_hc ? n_x : n_hc) + n_info, st);
@@ -183,7 +184,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.cols = cols;
         p.info = info;
         p.prepared = prepare;
-        if (prepare) e = moe_launch_prepare<FMT>(p, n, cols, info, st);
+        if (prepare) e = moe_launch_prepare<FMT>(p, n, kind == 2, cols, info, st);
         if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wi, n_sms, st);
         if (e != cudaSuccess) break;
         p.down = true;
@@ -195,7 +196,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.tiles = (int)((ex.D + 15ll) / 16);
         place(p, wo, n);
         p.prepared = kind == 2;
-        if (p.prepared) e = moe_launch_prepare<FMT>(p, p.P, cols, info, st);
+        if (p.prepared) e = moe_launch_prepare<FMT>(p, p.P, true, cols, info, st);
         if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wo, n_sms, st);
         if (e != cudaSuccess) break;
         Sum q{sums, p.ids, a.wts + (long long)s0 * a.k, a.res ? (const char *)a.res + s0 * a.ldr * b : nullptr,

@@ -713,20 +713,39 @@ template <int FMT, int PC> struct ManyShape {
 };
 
 // A row of the tokens, or of h, per block, as pieces of f16 in the order of the
-// instructions; what the sums need of it to info.
-template <int FMT, int PC, bool RAW, class Src>
+// instructions; what the sums need of it to info.  Few columns read rows: [row]
+// [piece][line][16 KC].  ORDERED, for many: where the plan has the row's slots, a
+// line of all of them side by side, [piece][line][place][kPitch], so that one copy
+// brings a chunk's.
+template <int FMT, int PC, bool RAW, bool ORDERED, class Src>
 __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant__ MoeStream p, uint8_t *cols, float2 *info) {
-    constexpr int KC = Fmt<FMT>::KC;
+    constexpr int KC = Fmt<FMT>::KC, kPitch = ManyShape<FMT, PC>::kPitch;
     __shared__ unsigned tops[8];
     __shared__ float sums[8];
+    __shared__ int places[kMoeMaxK];
     dependency_wait();
     let_dependents_start();
-    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, units = p.lines * KC;
+    const int slots = ORDERED && !p.down ? p.k : 1;                     // of this row
     if (p.down) {
         const int e = p.ids[row];
         if (e < 0 || e >= p.E) return;         // an empty slot has no h
     }
-    const int units = p.lines * KC;
+    if constexpr (ORDERED) {
+        // a slot's place: the slots of lower experts, and of its own before it
+#pragma unroll 1
+        for (int j = warp; j < slots; j += 8) {
+            const int slot = row * slots + j, e = p.ids[slot];
+            int place = 0;
+#pragma unroll 1
+            for (int i = lane; i < p.P; i += 32) {
+                const int o = p.ids[i];
+                place += o >= 0 && o < p.E && (o < e || (o == e && i < slot)) ? 1 : 0;
+            }
+            place = __reduce_add_sync(kAll, place);
+            if (lane == 0) places[j] = e >= 0 && e < p.E ? place : -1;
+        }
+    }
     unsigned m = 0;
 #pragma unroll 1
     for (int u0 = threadIdx.x; u0 < units; u0 += 3 * 256) {
@@ -746,7 +765,6 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
     m = __reduce_max_sync(kAll, tops[lane & 7]);
     const int up = exponent_for(m);
     const float scale = power(up);
-    uint8_t *to = cols + (long long)row * PC * p.lines * (16 * KC);
     float sum = 0.f;
 #pragma unroll 1
     for (int u = threadIdx.x; u < units; u += 256) {
@@ -754,18 +772,31 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
         uint4 hi, rest;
         unit8<FMT, Src>(p, row, 0, u, v);
         sum += split<FMT, PC, RAW, Src::kExact>(v, scale, u, hi, rest);
-        *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u)) = hi;
-        if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * (16 * KC) + unit_at<FMT>(u)) = rest;
+        if constexpr (ORDERED) {
+            const int line = unit_at<FMT>(u) / (16 * KC), in = unit_at<FMT>(u) - line * (16 * KC);
+#pragma unroll 1
+            for (int j = 0; j < slots; ++j) {
+                if (places[j] < 0) continue;
+                uint8_t *to = cols + ((long long)line * p.P + places[j]) * kPitch + in;
+                *reinterpret_cast<uint4 *>(to) = hi;
+                if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * p.P * kPitch) = rest;
+            }
+        } else {
+            uint8_t *to = cols + (long long)row * PC * p.lines * (16 * KC) + unit_at<FMT>(u);
+            *reinterpret_cast<uint4 *>(to) = hi;
+            if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * (16 * KC)) = rest;
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if (lane == 0) sums[warp] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < slots) {
         sum = 0.f;
 #pragma unroll 1
         for (int w = 0; w < 8; ++w) sum += sums[w];
-        info[row] = make_float2(power(-up), RAW ? sum * kZeroPoint<FMT> : 0.f);
+        const int at = ORDERED ? places[threadIdx.x] : row;
+        if (at >= 0) info[at] = make_float2(power(-up), RAW ? sum * kZeroPoint<FMT> : 0.f);
     }
 }
 
@@ -781,8 +812,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 
     if (tid == 0) {
 #pragma unroll
-        for (int i = 0; i < 2 * STAGES; ++i)   // every warp brings its part of a stage, and lets go of it
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(full + 8 * i), "r"(kManyWarps) : "memory");
+        for (int i = 0; i < 2 * STAGES; ++i)   // five warps bring a stage, all let go of it
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(full + 8 * i), "r"(i < STAGES ? 5 : kManyWarps) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // the ids were there when the kernel that prepares the rows began
@@ -802,48 +833,39 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         return (int)((long long)(u - c * rounds + 1) * p.tiles / rounds) - from;
     };
 
-    // this warp's copies of the next stage: its tile's line, and every 16th column's
+    // A stage's copies: the codes in four boxes of 64 rows (8 tiles of gate or of up,
+    // or 4 of down; a round's last box may bring rows that it does not want), one by
+    // each of the first four warps, and the columns by the fifth.
     int fu = lo, fline = 0, fstage = 0, fbytes = 0, fy = 0;
-    const CUtensorMap *map = nullptr;          // of the tile; none: the round has fewer tiles
-    const uint8_t *from[2] = {};               // of the columns (32 at most)
+    const CUtensorMap *map = nullptr;
+    const uint8_t *from = nullptr;
     const uint64_t policy = stream_policy();
-    const long long plane = (long long)p.lines * (16 * KC);
+    const long long line_bytes = (long long)p.P * Sh::kPitch;
     auto open = [&]() {
         if (fu >= hi) return;
         int c, first;
-        const int tiles = tiles_of(fu, c, first), n = pl.n[c];
-        fline = fbytes = 0;
-        map = nullptr;
-        if (warp < tiles) {
-            map = p.table[pl.expert[c]].map + (p.down ? 2 : 0);
-            fy = (first + warp) * (p.down ? 16 : 8);
-            fbytes = 2048;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            from[i] = nullptr;
-            if (warp + i * kManyWarps < n) {
-                const int slot = pl.order[pl.first[c] + warp + i * kManyWarps];
-                from[i] = p.cols + (p.down ? slot : p.by_k(slot)) * (PC * plane);
-                fbytes += PC * (16 * KC);
-            }
+        const int tiles = tiles_of(fu, c, first);
+        fline = 0;
+        if (warp < 4) {
+            const int box = p.down ? 4 : 8, at = p.down ? warp : warp & 1;          // tiles of a box, this one
+            map = p.table[pl.expert[c]].wide + (p.down ? 2 : warp >> 1);
+            fy = (first + at * box) * (p.down ? 16 : 8);
+            fbytes = at * box < tiles ? 8192 : 0;
+        } else {
+            from = p.cols + pl.first[c] * Sh::kPitch;
+            fbytes = pl.n[c] * Sh::kPitch;
         }
     };
-    auto copy_stage = [&]() {                  // lane 0
+    auto copy_stage = [&]() {                  // lane 0 of the first five warps
         if (fu >= hi) return;
         const uint32_t to = base + fstage * Sh::kStage, bar = full + 8 * fstage;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(fbytes) : "memory");
-        if (map) {
-            copy_box(to + warp * 2048, map, fline * 128, fy, bar, policy);
-            copy_box(to + warp * 2048 + 1024, p.down ? map : map + 1, fline * 128, p.down ? fy + 8 : fy, bar, policy);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!from[i]) break;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(warp < 4 ? fbytes : PC * fbytes) : "memory");
+        if (warp < 4) {
+            if (fbytes) copy_box(to + warp * 8192, map, fline * 128, fy, bar, policy);
+        } else {
 #pragma unroll
             for (int pc = 0; pc < PC; ++pc)
-                copy_bulk(to + Sh::kCodes + pc * Sh::kPlane + (warp + i * kManyWarps) * Sh::kPitch, from[i] + pc * plane, 16 * KC, bar);
-            from[i] += 16 * KC;
+                copy_bulk(to + Sh::kCodes + pc * Sh::kPlane, from + (pc * p.lines + fline) * line_bytes, fbytes, bar);
         }
         if (++fstage == STAGES) fstage = 0;
         if (++fline == p.lines) {
@@ -851,7 +873,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             open();
         }
     };
-    if (lane == 0) {
+    if (warp < 5 && lane == 0) {
         open();
 #pragma unroll 1
         for (int i = 0; i < STAGES; ++i) copy_stage();
@@ -882,13 +904,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             auto products = [&](auto tiles) {
                 constexpr int N = decltype(tiles)::value;
                 float rest[1][1][PC == 2 ? NT : 1][4] = {};
-                const uint8_t *codes = at + warp * 2048 + row * 128 + ((tig ^ row) << 4);
+                // rows 8-15 of a tile lie behind rows 0-7, or are up's, in the third and fourth box
+                const uint8_t *codes = at + warp * (p.down ? 2048 : 1024) + row * 128 + ((tig ^ row) << 4);
+                const int second = p.down ? 1024 : 16384;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const uint8_t *from = reinterpret_cast<const uint8_t *>((uintptr_t)codes ^ (half * 64));
                     uint4 q[1][2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 1024);
+                    for (int i = 0; i < 2; ++i) q[0][i] = *reinterpret_cast<const uint4 *>(from + i * second);
                     const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
                     chunk_products<FMT, N, NT, 1, PC, RAW, NA>(q, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
                 }
@@ -909,7 +933,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             if (lane == 0) {
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty + 8 * stage) : "memory");
                 // the stage before this one is let go by all, or soon: filled again
-                if (u != lo || line) {
+                if (warp < 5 && (u != lo || line)) {
                     if (fu < hi && ok) ok = mbar_wait(empty + 8 * before, parity_before, kMoeWaitNs);
                     if (ok) copy_stage();
                 }
@@ -931,9 +955,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
                 for (int j = 0; j < 2; ++j) {
                     const int c = nt * 8 + 2 * tig + j;
                     if (c < n) {
-                        const int slot = order[c];
-                        const float2 i = p.info[p.down ? slot : p.by_k(slot)];
-                        put(p, 0, slot, tile, row, product<RAW>(sum[0][nt][j], i.y, sa, i.x), product<RAW>(sum[0][nt][2 + j], i.y, sb, i.x));
+                        const float2 i = p.info[pl.first[chunk] + c];
+                        put(p, 0, order[c], tile, row, product<RAW>(sum[0][nt][j], i.y, sa, i.x), product<RAW>(sum[0][nt][2 + j], i.y, sb, i.x));
                     }
                 }
         }
@@ -967,11 +990,16 @@ cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int n_sms, cu
 }
 
 template <int FMT>
-cudaError_t moe_launch_prepare(const MoeStream &p, int rows, uint8_t *cols, float2 *info, cudaStream_t st) {
+cudaError_t moe_launch_prepare(const MoeStream &p, int rows, bool ordered, uint8_t *cols, float2 *info, cudaStream_t st) {
     auto go = [&](auto kernel) { return launch_dependent(kernel, dim3(rows), 256, 0, st, p, cols, info); };
-    if (p.type == B200Q_T_F32) return p.down ? go(moe_prepare_kernel<FMT, 2, false, GatedRows>) : go(moe_prepare_kernel<FMT, 2, false, TokenRows<float>>);
-    if (p.type == B200Q_T_F16) return p.down ? go(moe_prepare_kernel<FMT, 2, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, TokenRows<__half>>);
-    return p.down ? go(moe_prepare_kernel<FMT, 1, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, TokenRows<__nv_bfloat16>>);
+    if (!ordered) {                            // few columns: the tokens' rows
+        if (p.type == B200Q_T_F32) return go(moe_prepare_kernel<FMT, 2, false, false, TokenRows<float>>);
+        if (p.type == B200Q_T_F16) return go(moe_prepare_kernel<FMT, 1, true, false, TokenRows<__half>>);
+        return go(moe_prepare_kernel<FMT, 1, true, false, TokenRows<__nv_bfloat16>>);
+    }
+    if (p.type == B200Q_T_F32) return p.down ? go(moe_prepare_kernel<FMT, 2, false, true, GatedRows>) : go(moe_prepare_kernel<FMT, 2, false, true, TokenRows<float>>);
+    if (p.type == B200Q_T_F16) return p.down ? go(moe_prepare_kernel<FMT, 2, true, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, true, TokenRows<__half>>);
+    return p.down ? go(moe_prepare_kernel<FMT, 1, true, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, true, TokenRows<__nv_bfloat16>>);
 }
 
 // kind 0 and 1: as many columns as there are tokens, at most 8, and slices that
