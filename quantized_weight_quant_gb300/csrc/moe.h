@@ -22,7 +22,7 @@ struct MoeStream {
     int K, rows, ldh;                         // columns of the product's rows; its rows; F rounded up to 8
     int lines, ns, ns_in;                     // 128-byte lines of a row, slices of them
     int tiles, wk;                            // of the rows; 2^wk warps share one (few columns)
-    Quotient by_tiles, by_grid, by_k;
+    Quotient by_tiles, by_grid, by_k, by_rounds;   // by_rounds: 16 tiles of a chunk each (many columns)
     int nc, held, pitch;                      // columns of a chunk, of those staged together, bytes of one in shared memory
     bool down, aligned, prepared;             // aligned: the tokens' rows start on 16 bytes
     // prepared: rows in f16 pieces, their scales and sums

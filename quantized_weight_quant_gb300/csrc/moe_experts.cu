@@ -131,6 +131,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.by_tiles = Quotient(p.tiles);
         p.by_grid = Quotient(n_sms * w.blocks);
         p.by_k = Quotient(a.k);
+        p.by_rounds = Quotient((p.tiles + 15) / 16);
         p.wk = shared_by(w.warps, chosen(n, a.k, ex.E) * w.ns * p.tiles / (n_sms * w.blocks), p.lines / w.ns);
         p.ns = w.ns;
         p.nc = w.nc;

@@ -823,14 +823,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
     dependency_wait();
     let_dependents_start();
     // A round: up to 16 tiles of one chunk, a warp each, over the whole length of the
-    // rows.  A chunk's rounds share its tiles evenly, a block takes an even run of rounds.
+    // rows; a block takes an even run of rounds.  (More and shorter rounds, so that no
+    // block has one more than others: no gain, since the boxes then bring rows twice.)
     const int rounds = (p.tiles + kManyWarps - 1) / kManyWarps;        // of a chunk
     const int all = pl.chunks * rounds, each = p.by_grid(all), more = all - each * (int)gridDim.x;
     const int lo = (int)blockIdx.x * each + min((int)blockIdx.x, more), hi = lo + each + ((int)blockIdx.x < more ? 1 : 0);
     auto tiles_of = [&](int u, int &c, int &from) {                    // round u's chunk, first tile and tiles
-        c = u / rounds;
-        from = (int)((long long)(u - c * rounds) * p.tiles / rounds);
-        return (int)((long long)(u - c * rounds + 1) * p.tiles / rounds) - from;
+        c = p.by_rounds(u);
+        from = (u - c * rounds) * kManyWarps;
+        return min(p.tiles - from, kManyWarps);
     };
 
     // A stage's copies: the codes in four boxes of 64 rows (8 tiles of gate or of up,
