@@ -17,7 +17,7 @@ struct MoeStream {
     const float *in;                          // down: h [P][ldh], or the slices' sums of gate and up [ns_in][P][2][ldh]
     float *out;                               // gate and up: what down reads; down: [ns][P][D]
     unsigned int *err;                        // where a wrong id is recorded
-    long long ldx, ld;                        // values; bytes of a row of codes
+    long long ldx;                            // values
     int S, P, k, E, type, act;                // P = S * k
     int K, rows, ldh;                         // columns of the product's rows; its rows; F rounded up to 8
     int lines, ns, ns_in;                     // 128-byte lines of a row, slices of them

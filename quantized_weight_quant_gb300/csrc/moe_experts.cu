@@ -13,7 +13,7 @@
 //     thread.  A column is scaled by a power of two into f16's range, in two
 //     pieces (22 bits) where its type needs them.  Sums are f32, taken out of the
 //     tensor instruction's accumulator, which truncates, every 128 bytes of a row
-//     (every 4 of codes where there are two pieces).
+//     (1024 where there are many columns, every 4 where there are two pieces).
 //   * Codes meet f16 and bf16 rows as unsigned f16 subnormals, one AND for two of
 //     them, and the zero point times the column's sum is taken off at the end: the
 //     instruction aligns its products by their operands' exponents, so that the
@@ -21,9 +21,9 @@
 //     rounding).  f32 rows meet signed codes, exact in f16, one AND and one packed
 //     f16 FMA for two of them.
 //   * Few columns (moe_few_kernel, up to 8 per expert): the columns stay in shared
-//     memory.  A thread copies its own 16 bytes of codes into its own slots of a
-//     ring (cp.async), several lines ahead and across the tiles of the run: no
-//     barrier orders them.  A warp takes whole tiles where the block has many;
+//     memory.  A warp has its own ring of codes, brought by its own TMA boxes of 8
+//     rows x 128 bytes several lines ahead and across the tiles of the run: no
+//     barrier of the block orders them.  A warp takes whole tiles where the block has many;
 //     otherwise wk warps take the 128-byte lines of a tile in turn and add their
 //     sums in warp order.  Three launches: gate and up, down, the weighted sum.
 //   * Many columns (moe_many_kernel): the rows are prepared once, in a launch before
@@ -167,7 +167,6 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.out = h;
         p.err = (unsigned int *)err;
         p.ldx = a.ldx;
-        p.ld = ex.ld_in;
         p.S = n;
         p.P = n * a.k;
         p.k = a.k;
@@ -190,7 +189,6 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         if (e != cudaSuccess) break;
         p.down = true;
         p.out = sums;
-        p.ld = ex.ld_out;
         p.K = ex.F;
         p.rows = ex.D;
         p.lines = out_lines;

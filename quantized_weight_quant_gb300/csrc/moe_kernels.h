@@ -26,9 +26,6 @@ __device__ __forceinline__ uint64_t stream_policy() {
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
     return r;
 }
-__device__ __forceinline__ void copy16_stream(uint32_t dst, const void *src, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
-}
 __device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- plan
@@ -698,7 +695,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
 template <int N> struct Count {
     static constexpr int value = N;
 };
-constexpr int kManyWarps = 16, kManyThreads = 32 * kManyWarps;
+constexpr int kManyWarps = 16, kManyThreads = 32 * kManyWarps, kManyHeld = 8;
 template <int FMT, int PC> constexpr int kManyColumns = FMT == B200Q_I2 && PC == 2 ? 16 : 32;
 template <int FMT, int PC> constexpr int kManyStages = FMT == B200Q_I8 || (FMT == B200Q_I4 && PC == 1) ? 4 : 3;
 template <int FMT, int PC> struct ManyShape {
@@ -887,8 +884,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         int chunk, first;
         const bool mine = warp < tiles_of(u, chunk, first);
         const int n = pl.n[chunk], tile = first + warp;
-        // One piece: the sums stay in the accumulators (16-bit rows; what those drop of a row of 6144 is below 1e-4
-        // of a unit of the types' last places).  Two: they are taken out after every word of codes.
+        // One piece: the sums are taken out of the accumulators after every kManyHeld lines.  An instruction drops up to
+        // an accumulator's last place, so that what is lost of a sum grows with the instructions between (64 of int4:
+        // 4e-6 of sum |x w| at most); over the whole row it would grow with the row.  Two: after every word of codes.
         constexpr int NA = PC == 2 ? 1 : 2;
         float sum[1][NT][4] = {}, acc[NA][1][NT][4] = {}, sa = 0.f, sb = 0.f;
         if (mine) {
@@ -941,15 +939,20 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
             }
             before = stage, parity_before = parity;
             if (++stage == STAGES) stage = 0, parity ^= 1;
+            if constexpr (PC == 1) {
+                if ((line + 1) % kManyHeld == 0 || line + 1 == p.lines) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            sum[0][nt][i] += acc[0][0][nt][i] + acc[1][0][nt][i];
+                            acc[0][0][nt][i] = acc[1][0][nt][i] = 0.f;
+                        }
+                }
+            }
         }
         if (mine) {
             const unsigned short *order = pl.order + pl.first[chunk];
-            if constexpr (PC == 1) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[0][nt][i] = acc[0][0][nt][i] + acc[1][0][nt][i];
-            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -310,6 +310,20 @@ def test_experts_long_rows(q, fmt, D, F):
     layer.free()
 
 
+@pytest.mark.parametrize("fmt,D", [("i2", 65536), ("i4", 65536), ("i8", 32768)])
+@pytest.mark.parametrize("S", [1, 6, 20])
+def test_experts_long_rows_of_one_sign(q, S, fmt, D):
+    """The sums grow all along the row, and with them what a truncating accumulator drops.  f16 out and one h: its rounding,
+    2^-11 of y, is below the products' 1e-5 of sum |x w|, over 100 times a sum of random signs at these lengths."""
+    layer = Layer(q, fmt, 2, D, 1, seed=8)
+    x = _dev(0.25 + np.abs(synth.normal_f32((S, D), S, 1)), "f16")
+    ids, wts = _pick(S, 1, 2, S)
+    y = _moe(q, layer, x, ids, wts, "f16", "none")
+    want, tol = layer.ref(_np64(x), ids, wts.astype(np.float64), "none", None, "f16")
+    _near(y, want, tol, "f16", "S=%d" % S)
+    layer.free()
+
+
 def test_experts_many_tokens_and_slots(q):
     """More tokens than one launch plans at once, 32 slots a token, one expert for all of them."""
     layer = Layer(q, "i4", 5, 96, 80, seed=2)
