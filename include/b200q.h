@@ -651,7 +651,11 @@ void b200q_experts_free(b200q_experts *ex);
  *           whole; a row whose slots are all empty is res, or 0
  * y must not overlap x, ids or wts; ids and wts may be what b200q_moe_route has
  * just written on the stream.  Rows do not depend on each other, and the same
- * call gives the same bits.
+ * call gives the same bits.  Each product is within 1e-5 of scale * sum |deq x| (down:
+ * of h), sums are f32, h is rounded to 11 bits where the rows are bf16, and y once.
+ * Asynchronous, with a stream-ordered workspace of the library's pool; for decode steps:
+ * more than 64 tokens (or 1024 slots) run in turns of that many, each of which
+ * reads its experts again.
  */
 int b200q_moe_experts(const b200q_experts *ex, const void *x, int type, long long ldx, const int *ids,
                       const float *wts, int k, int act, const void *res, long long ldr, void *y, long long ldy, int S,

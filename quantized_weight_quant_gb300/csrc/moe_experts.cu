@@ -25,7 +25,8 @@
 //     rows x 128 bytes several lines ahead and across the tiles of the run: no
 //     barrier of the block orders them.  A warp takes whole tiles where the block has many;
 //     otherwise wk warps take the 128-byte lines of a tile in turn and add their
-//     sums in warp order.  Three launches: gate and up, down, the weighted sum.
+//     sums in warp order.  Three launches: gate and up, down, the weighted sum; from
+//     three tokens on their rows are prepared by one before.
 //   * Many columns (moe_many_kernel): the rows are prepared once, in a launch before
 //     each product, and come line by line beside the codes.
 // No sum depends on the order in which blocks run.
