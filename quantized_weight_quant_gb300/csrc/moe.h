@@ -8,6 +8,7 @@ namespace qwq {
 
 constexpr int kMoePairs = 1024;               // slots of a launch at most
 constexpr int kMoeTokens = 64;                // tokens of a launch at most
+constexpr int kMoeFewColumns = 8;             // of a chunk, few columns
 
 // One of the two products: gate and up of the tokens' rows, or down of h.
 struct MoeStream {

@@ -27,7 +27,7 @@
 //     otherwise wk warps take the 128-byte lines of a tile in turn and add their
 //     sums in warp order.  Three launches: gate and up, down, the weighted sum; from
 //     three tokens on their rows are prepared by one before.
-//   * Many columns (moe_many_kernel): the rows are prepared once, in a launch before
+//   * Many columns (moe_many_kernel), where there are tiles for all SMs: the rows are prepared once, in a launch before
 //     each product, and come line by line beside the codes.
 // No sum depends on the order in which blocks run.
 #include "moe.h"
@@ -107,6 +107,19 @@ double chosen(int S, int k, int E) {
     return E * (1. - none);
 }
 
+// Steps of a warp, a line of a tile each, that the two kernels need for a product.
+// Many columns: a block takes 16 tiles together, so that a few tiles leave SMs
+// idle however long their rows are; few columns: warps take tiles, or share them.
+struct Steps {
+    double few, many;
+};
+Steps steps_of(int S, int k, int E, int tiles, int lines, int nc, int n_sms) {
+    const double touched = chosen(S, k, E), avg = S * (double)k / touched;
+    const double chunks8 = touched * (avg / kMoeFewColumns + 0.5), chunks = touched * (avg <= 0.75 * nc ? 1. : avg / nc + 0.5);
+    const double rounds = chunks * ((tiles + 15) / 16);
+    return {chunks8 * tiles * lines / (16. * n_sms), (double)((long long)(rounds / n_sms + 0.999)) * lines};
+}
+
 template <int FMT>
 cudaError_t run(const Moe &a, cudaStream_t st) {
     constexpr int KC = FMT == B200Q_I8 ? 16 : FMT == B200Q_I4 ? 32 : 64;
@@ -115,11 +128,24 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
     int part = kMoePairs / a.k < kMoeTokens ? kMoePairs / a.k : kMoeTokens;            // tokens per launch
     const int in_lines = (int)(ex.ld_in / 128), out_lines = (int)(ex.ld_out / 128);
     const int pc_in = moe_pieces(a.type, false), pc_out = moe_pieces(a.type, true);
+    const int n_sms = sm_count(ex.device);
     int S = 0, P = 0, kind = 0;
     MoeWay wi, wo;
     for (;; part /= 2) {
         S = a.S < part ? a.S : part, P = S * a.k, kind = kind_of(S, a.k, ex.E);
         wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
+        if (kind == 2) {
+            // What staging costs the kernel for few columns is about three steps; two pieces cost the other a quarter more.
+            // int8 6144 / 256, 8 experts, f32, 64 tokens of 2: 51 us with few, 100 with many (19 and 52 steps); int8
+            // 2048 / 1024, 4 experts, f32, 64 tokens of 2: 44 and 59 (23 and 24); int4 2048 / 1024, 32 experts, bf16, 64
+            // tokens of 4: 57 and 47 (30 and 24); int4 1024 / 512, 16 experts, bf16, 32 tokens of 4: 22 and 20 (4 and 6).
+            const Steps i = steps_of(S, a.k, ex.E, (int)((ex.F + 7ll) / 8), in_lines, wi.nc, n_sms);
+            const Steps o = steps_of(S, a.k, ex.E, (int)((ex.D + 15ll) / 16), out_lines, wo.nc, n_sms);
+            if (i.few + o.few + 3. < (pc_in == 2 ? 1.25 : 1.) * i.many + (pc_out == 2 ? 1.25 : 1.) * o.many) {
+                kind = 0;
+                wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
+            }
+        }
         if (kind == 1 && (wi.ns > 1 || wo.ns > 1)) {       // two blocks on an SM are not worth slices
             kind = 0;
             wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
@@ -127,7 +153,6 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         // tiles of all chunks are numbered in 31 bits; at kMoeMaxSize rows and columns one token's are
         if (part == 1 || ((long long)P * wi.ns * (ex.F / 8 + 1) < 1 << 30 && (long long)P * wo.ns * (ex.D / 16 + 1) < 1 << 30)) break;
     }
-    const int n_sms = sm_count(ex.device);
     auto place = [&](MoeStream &p, const MoeWay &w, int n) {
         p.by_tiles = Quotient(p.tiles);
         p.by_grid = Quotient(n_sms * w.blocks);

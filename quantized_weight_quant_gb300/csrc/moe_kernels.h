@@ -357,7 +357,7 @@ __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], From fro
 
 // ---------------------------------------------------------------- few columns
 // Up to 8 columns of an expert, those of a few chunks at a time in shared memory.
-constexpr int kFewColumns = 8, kFewHeld = 16;  // of a chunk; of the chunks that are staged together
+constexpr int kFewColumns = kMoeFewColumns, kFewHeld = 16;  // of a chunk; of the chunks that are staged together
 
 struct FewColumns {
     unsigned top[kFewHeld];                    // the largest magnitude

@@ -324,6 +324,40 @@ def test_experts_long_rows_of_one_sign(q, S, fmt, D):
     layer.free()
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_experts_long_rows_of_one_sign_many_tiles(q, kind):
+    """As above where there are enough rows for every SM; down takes h[0] alone, so that the other rows' errors do not hide its."""
+    import torch
+    S, D, F = 64, 8192, 2432
+    codes = np.random.default_rng(9).integers(0, 256, (2, F, D)).astype(np.uint8)
+    down = np.zeros((D, F), np.uint8)
+    down[:, 0] = 64
+    one = np.ones(F, np.float32)
+    ts = [[q.tensor_upload(FMTS["i8"], *c.shape, c, v)] for c, v in
+          [(codes[0], one / 4096), (codes[1], one / 4096), (down, np.full(D, 1 / 64, np.float32))]]
+    ex = q.Experts(*ts)
+    x = _dev(0.25 + np.abs(synth.normal_f32((S, D), 9, 1)), kind)
+    y = torch.empty_like(x)
+    q.moe_experts(ex, x, torch.zeros(S, 1, dtype=torch.int32, device="cuda"), torch.ones(S, 1, device="cuda"), y, S, 1, act=q.ACTS["none"])
+    x = _np64(x)
+    wg, wu = (_values(c[:1], "i8", D)[0] / 4096 for c in codes)
+    g, u, dg, du = x @ wg, x @ wu, 1e-5 * (x @ np.abs(wg)), 1e-5 * (x @ np.abs(wu))
+    h, dh = g * u, dg * (np.abs(u) + du) + np.abs(g) * du
+    tol = dh + (1e-5 + (2.0 ** -11 if kind == "bf16" else 0.0)) * (np.abs(h) + dh) + 1e-6 * np.abs(h)
+    _near(y, np.repeat(h[:, None], D, 1), np.repeat(tol[:, None], D, 1), kind)
+    ex.free()
+    for t in ts:
+        t[0].free()
+
+
+@pytest.mark.parametrize("fmt,E,D,F", [("i8", 2, 2048, 64), ("i8", 3, 9001, 40), ("i4", 2, 4097, 77), ("i2", 1, 100, 9001)])
+def test_experts_many_tokens_of_few_tiles(q, fmt, E, D, F):
+    layer = Layer(q, fmt, E, D, F, seed=D)
+    for S, k, kind in [(24, 1, "f32"), (64, E, "bf16"), (33, E, "f16"), (40, E, "f32")]:
+        _check(q, layer, S, k, kind, empty=0.1, seed=S)
+    layer.free()
+
+
 def test_experts_many_tokens_and_slots(q):
     """More tokens than one launch plans at once, 32 slots a token, one expert for all of them."""
     layer = Layer(q, "i4", 5, 96, 80, seed=2)
