@@ -403,6 +403,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
 
 constexpr unsigned long long kMoeWaitNs = 2000000000ull;               // 2 s bound on any wait
 
+// The tensor maps lie in memory that a copy wrote (cudaMemcpyAsync, when the handle
+// was made), not in a kernel's parameters: a thread acquires a map before its first
+// copy by it, or a map that lay at this address before, of a freed layer, may serve.
+__device__ __forceinline__ void acquire_map(const CUtensorMap *map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.sys [%0], 128;" ::"l"(map) : "memory");
+}
+
 // A box of 8 rows x 128 bytes of codes to shared memory, swizzled.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy) {
     asm volatile(
@@ -546,7 +553,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
             fline = first_line(sl) + kw;
             fl1 = first_line(sl + 1);
             if (fline >= fl1) continue;
+            const CUtensorMap *was = map;
             map = p.table[pl.expert[c]].map + (p.down ? 2 : 0);
+            if (lane == 0 && map != was) {
+                acquire_map(map);
+                if (!p.down) acquire_map(map + 1);
+            }
             fy = (fu - cs * p.tiles) * (p.down ? 16 : 8);
             return;
         }
@@ -846,7 +858,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         fline = 0;
         if (warp < 4) {
             const int box = p.down ? 4 : 8, at = p.down ? warp : warp & 1;          // tiles of a box, this one
+            const CUtensorMap *was = map;
             map = p.table[pl.expert[c]].wide + (p.down ? 2 : warp >> 1);
+            if (map != was) acquire_map(map);
             fy = (first + at * box) * (p.down ? 16 : 8);
             fbytes = at * box < tiles ? 8192 : 0;
         } else {

@@ -711,3 +711,24 @@ def test_two_streams_at_once(q):
     for a, (_, _, _, y) in zip(alone, args):
         assert torch.equal(a, y)
     layer.free()
+
+
+def test_layers_made_where_freed_ones_were(q):
+    """A layer's table often lies where a freed layer's did: its tensor maps are those of the new one, of another shape and
+    other codes, for few and for many columns, eager and when a graph of the new layer is replayed."""
+    import torch
+    for n in range(12):
+        D, F = ((1024, 640), (256, 520), (640, 1024))[n % 3]
+        layer = Layer(q, list(FMTS)[n // 2 % 3], 8, D, F, seed=n)
+        for S, k in ((1, 3), (6, 2), (64, 4)):
+            x, r, ids, wts, y = _check(q, layer, S, k, TYPES[n % 3], seed=n)
+            if n % 4 == 0:
+                args = torch.from_numpy(ids).cuda(), torch.from_numpy(wts).cuda(), torch.zeros_like(y)
+                torch.cuda.synchronize()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    q.moe_experts(layer.ex, x, *args, S, k, res=r)
+                g.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(args[2], y)
+        layer.free()
