@@ -690,6 +690,16 @@ int b200q_block_norm(const void *m, int type, long long ldm, const void *h, long
                      void *stream);
 
 /*
+ * Self test of how the experts' layer gives up: sets the limit of the waits of
+ * b200q_moe_experts' later calls to wait_ns nanoseconds, 0 .. 2 * 10^9 (-1: back to
+ * the 2 s they start with).  withhold (the limit is then at most 10^8): its kernels
+ * wait for 16 bytes of prepared rows that nothing copies, give up after the
+ * limit, wait for the copies in flight and return; y is not whole then, and the
+ * status is B200Q_ETIMEOUT.
+ */
+int b200q_selftest_moe(long long wait_ns, int withhold);
+
+/*
  * Self test of the bounded waits: one kernel waits, at most wait_us
  * microseconds (1 .. 10^6), on an mbarrier that nothing arrives on, gives up
  * and records B200Q_ETIMEOUT the way a kernel whose copies never land does.

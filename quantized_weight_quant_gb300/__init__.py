@@ -92,6 +92,8 @@ def _load():
     L.b200q_block_norm.restype = ci
     L.b200q_selftest_q8_plan.argtypes = [ci, ci, ci, ci, ci, ci, vp]
     L.b200q_selftest_q8_plan.restype = ci
+    L.b200q_selftest_moe.argtypes = [cll, ci]
+    L.b200q_selftest_moe.restype = ci
     L.b200q_selftest_q8.argtypes = [cll, ci]
     L.b200q_selftest_q8.restype = ci
     L.b200q_selftest_timeout.argtypes = [ci, vp]
@@ -488,6 +490,12 @@ def selftest_q8(wait_ns: int = -1, status: int = OK) -> None:
     """The limit of the 8-bit tensor-core kernel's waits (-1: its own 2 s), and a
     status for device_status() to report (b200q_selftest_q8)."""
     _check(lib.b200q_selftest_q8(wait_ns, status))
+
+
+def selftest_moe(wait_ns: int = -1, withhold: bool = False) -> None:
+    """The limit of the waits of moe_experts (-1: its own 2 s), and whether they
+    are made to run out (b200q_selftest_moe)."""
+    _check(lib.b200q_selftest_moe(wait_ns, int(withhold)))
 
 
 def selftest_timeout(wait_us: int, stream=None) -> None:

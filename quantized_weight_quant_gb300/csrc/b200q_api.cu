@@ -1141,6 +1141,16 @@ extern "C" int b200q_selftest_q8(long long wait_ns, int status) {
     return B200Q_OK;
 }
 
+extern "C" int b200q_selftest_moe(long long wait_ns, int withhold) {
+    const char *who = "b200q_selftest_moe";
+    if (wait_ns < -1 || wait_ns > 2000000000ll)
+        return fail(B200Q_EINVAL, "%s: wait_ns must be in [-1, 2 * 10^9] (got %lld)", who, wait_ns);
+    if (withhold && (wait_ns < 0 || wait_ns > 100000000ll))
+        return fail(B200Q_EINVAL, "%s: withholding needs a limit of at most 10^8 ns (got %lld)", who, wait_ns);
+    moe_selftest(wait_ns, withhold != 0);
+    return B200Q_OK;
+}
+
 extern "C" int b200q_selftest_timeout(int wait_us, void *stream) {
     if (wait_us < 1 || wait_us > 1000000)
         return fail(B200Q_EINVAL, "b200q_selftest_timeout: wait_us must be in [1, 1000000] (got %d)", wait_us);

@@ -29,6 +29,8 @@ struct MoeStream {
     // prepared: rows in f16 pieces, their scales and sums
     const uint8_t *cols;                      // as moe_prepare_kernel lays them out
     const float2 *info;                       // inverse scale, zero point times sum
+    unsigned long long wait_ns;               // limit of any wait for a copy
+    int withheld;                             // bytes that prepared columns are waited for and do not come: 0, but in the self test
 };
 
 // How a product is launched: its kernel, columns of a chunk, slices, shared memory.

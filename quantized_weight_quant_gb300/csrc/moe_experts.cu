@@ -30,6 +30,8 @@
 //   * Many columns (moe_many_kernel), where there are tiles for all SMs: the rows are prepared once, in a launch before
 //     each product, and come line by line beside the codes.
 // No sum depends on the order in which blocks run.
+#include <atomic>
+
 #include "moe.h"
 #include "qmat_q8.h"
 
@@ -37,6 +39,9 @@ namespace qwq {
 namespace {
 
 __device__ unsigned int g_moe_err = 0;        // first error a kernel recorded (a B200Q_E* code, negated)
+constexpr long long kMoeWaitNs = 2000000000;
+std::atomic<long long> g_moe_wait_ns{kMoeWaitNs};   // b200q_selftest_moe shortens it
+std::atomic<int> g_moe_withheld{0};
 
 // ---------------------------------------------------------------- the weighted sum
 struct Sum {
@@ -210,6 +215,8 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.cols = cols;
         p.info = info;
         p.prepared = prepare;
+        p.wait_ns = (unsigned long long)g_moe_wait_ns.load(std::memory_order_relaxed);
+        p.withheld = g_moe_withheld.load(std::memory_order_relaxed);
         if (prepare) e = moe_launch_prepare<FMT>(p, n, kind == 2, cols, info, st);
         if (e == cudaSuccess) e = moe_launch_stream<FMT>(p, wi, n_sms, st);
         if (e != cudaSuccess) break;
@@ -240,6 +247,11 @@ cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st) {
     case B200Q_I4: return run<B200Q_I4>(a, st);
     default: return run<B200Q_I2>(a, st);
     }
+}
+
+void moe_selftest(long long wait_ns, bool withhold) {
+    g_moe_wait_ns.store(wait_ns < 0 ? kMoeWaitNs : wait_ns, std::memory_order_relaxed);
+    g_moe_withheld.store(withhold ? 16 : 0, std::memory_order_relaxed);
 }
 
 // Reads and clears the error word (0: none).

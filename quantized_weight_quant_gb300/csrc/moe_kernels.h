@@ -401,7 +401,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
     }
 }
 
-constexpr unsigned long long kMoeWaitNs = 2000000000ull;               // 2 s bound on any wait
+constexpr unsigned long long kMoeDrainNs = 250000000ull;               // for copies in flight, after giving up
 
 // The tensor maps lie in memory that a copy wrote (cudaMemcpyAsync, when the handle
 // was made), not in a kernel's parameters: a thread acquires a map before its first
@@ -612,8 +612,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
             __syncthreads();
         } else if (p.prepared) {
             const int bytes = (l1 - l0) * (16 * KC);
-            if (tid == 0) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(colbar), "r"(columns * PC * bytes) : "memory");
+            if (tid == 0 && ok) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(colbar), "r"(columns * PC * bytes + p.withheld) : "memory");
 #pragma unroll 1
                 for (int c = 0; c < columns * PC; ++c) {               // first pieces, then second ones
                     const int col = c < columns ? c : c - columns;
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                 cl.unscale[tid] = i.x;
                 cl.zero[tid] = slice == 0 ? i.y : 0.f;                 // of the whole row: taken off once
             }
-            if (ok) ok = mbar_wait(colbar, colparity, kMoeWaitNs);
+            if (ok) ok = mbar_wait(colbar, colparity, p.wait_ns);
             colparity ^= 1;
             __syncthreads();
         } else {
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
             const uint8_t *xb = B + column(min(g, n - 1)) * p.pitch + tig * 16 + kw * (16 * KC);
 #pragma unroll 1
             for (int line = l0 + kw; line < l1; line += wk, xb += wk * (16 * KC)) {
-                if (ok) ok = mbar_wait(bars + 8 * slot, parity, kMoeWaitNs);
+                if (ok) ok = mbar_wait(bars + 8 * slot, parity, p.wait_ns);
                 const uint8_t *from = mine + slot * 2048, *from2 = reinterpret_cast<const uint8_t *>((uintptr_t)from ^ 64);
                 uint4 q[1][2], next[1][2];     // [tile][row half]
 #pragma unroll
@@ -653,9 +653,11 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                     q[0][i] = *reinterpret_cast<const uint4 *>(from + i * 1024);
                     next[0][i] = *reinterpret_cast<const uint4 *>(from2 + i * 1024);
                 }
-                if (++slot == AHEAD) slot = 0, parity ^= 1;
                 __syncwarp();                  // the slot is read
-                if (ok) copy_line();
+                if (ok) {                      // otherwise what is in flight stays as it is told below
+                    if (++slot == AHEAD) slot = 0, parity ^= 1;
+                    copy_line();
+                }
                 constexpr int NA = PC == 2 ? 2 : 4;
                 float acc[NA][1][1][4] = {}, rest[PC == 2 ? NA : 1][1][1][4] = {};
                 chunk_products<FMT, 1, 1, 1, PC, RAW, NA>(q, [&](int) { return xb; }, p.held * p.pitch, sum, acc, rest);
@@ -696,7 +698,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
         // gave up: say so, and let the copies in flight land
         if (lane == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_ETIMEOUT));
 #pragma unroll 1
-        for (int i = 0; i < AHEAD; ++i) mbar_wait(bars + 8 * i, i < slot ? parity ^ 1 : parity, kMoeWaitNs / 8);
+        for (int i = 0; i < AHEAD; ++i) mbar_wait(bars + 8 * i, i < slot ? parity ^ 1 : parity, kMoeDrainNs);
+        if (p.prepared) mbar_wait(colbar, colparity ^ 1, kMoeDrainNs);
     }
 }
 
@@ -871,7 +874,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
     auto copy_stage = [&]() {                  // lane 0 of the first five warps
         if (fu >= hi) return;
         const uint32_t to = base + fstage * Sh::kStage, bar = full + 8 * fstage;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(warp < 4 ? fbytes : PC * fbytes) : "memory");
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(warp < 4 ? fbytes : PC * fbytes + p.withheld) : "memory");
         if (warp < 4) {
             if (fbytes) copy_box(to + warp * 8192, map, fline * 128, fy, bar, policy);
         } else {
@@ -911,7 +914,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         }
 #pragma unroll 1
         for (int line = 0; line < p.lines; ++line) {
-            if (ok) ok = mbar_wait(full + 8 * stage, parity, kMoeWaitNs);
+            if (ok) ok = mbar_wait(full + 8 * stage, parity, p.wait_ns);
             const uint8_t *at = smem + stage * Sh::kStage;
             // N: the tiles of columns that the chunk has; without a branch between their instructions
             auto products = [&](auto tiles) {
@@ -943,16 +946,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
                 else products(Count<NT>{});
             }
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty + 8 * stage) : "memory");
                 // the stage before this one is let go by all, or soon: filled again
                 if (warp < 5 && (u != lo || line)) {
-                    if (fu < hi && ok) ok = mbar_wait(empty + 8 * before, parity_before, kMoeWaitNs);
+                    if (fu < hi) ok = mbar_wait(empty + 8 * before, parity_before, p.wait_ns);
                     if (ok) copy_stage();
                 }
             }
-            before = stage, parity_before = parity;
-            if (++stage == STAGES) stage = 0, parity ^= 1;
+            if (ok) {                          // otherwise what is in flight stays as it is told below
+                before = stage, parity_before = parity;
+                if (++stage == STAGES) stage = 0, parity ^= 1;
+            }
             if constexpr (PC == 1) {
                 if ((line + 1) % kManyHeld == 0 || line + 1 == p.lines) {
 #pragma unroll
@@ -983,7 +988,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         // gave up: say so, and let the copies in flight land
         if (lane == 0) atomicCAS(p.err, 0u, (unsigned)(-B200Q_ETIMEOUT));
 #pragma unroll 1
-        for (int i = 0; i < STAGES; ++i) mbar_wait(full + 8 * i, i < stage ? parity ^ 1 : parity, kMoeWaitNs / 8);
+        for (int i = 0; i < STAGES; ++i) mbar_wait(full + 8 * i, i < stage ? parity ^ 1 : parity, kMoeDrainNs);
     }
 }
 

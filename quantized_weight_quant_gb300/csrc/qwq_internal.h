@@ -214,6 +214,7 @@ struct Moe {
 };
 cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st);
 cudaError_t moe_take_error(unsigned int *code);
+void moe_selftest(long long wait_ns, bool withhold);
 
 // p = m [* w_post / rms(m)], h' = res_scale h + out_scale gate p, y = h' w / rms(h').
 struct BlockNorm {

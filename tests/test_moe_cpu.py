@@ -85,3 +85,11 @@ def test_binding_refusals(q):
         q.block_norm(a, 4, 64, 1e-6, y=a, w=a[0])
     with pytest.raises(TypeError):
         q.moe_experts(7, a, ids, a, a, 4, 2)
+
+
+def test_self_test_refusals(q):
+    for bad in ((-2, False), (2 * 10 ** 9 + 1, False), (-1, True), (10 ** 8 + 1, True)):
+        with pytest.raises(q.B200QError):
+            q.selftest_moe(*bad)
+    q.selftest_moe(5, True)
+    q.selftest_moe()

@@ -732,3 +732,23 @@ def test_layers_made_where_freed_ones_were(q):
                 torch.cuda.synchronize()
                 assert torch.equal(args[2], y)
         layer.free()
+
+
+@pytest.mark.parametrize("S,k", [(5, 2), (64, 4)])
+def test_experts_that_give_up_report_it(q, S, k):
+    """Prepared rows that never come whole, for few and for many columns: the call ends, says so, and the next one is right."""
+    layer = Layer(q, "i4", 8, 1024, 640, seed=31)
+    _check(q, layer, S, k, "bf16")
+    x = _dev(synth.normal_f32((S, 1024), 3, 1), "bf16")
+    ids, wts = _pick(S, k, 8, 3)
+    q.selftest_moe(1000000, True)
+    try:
+        _moe(q, layer, x, ids, wts, "bf16")
+        with pytest.raises(q.B200QError) as e:
+            q.device_status()
+        assert e.value.status == q.ETIMEOUT
+    finally:
+        q.selftest_moe()
+    assert q.device_status() == q.OK
+    _check(q, layer, S, k, "bf16")
+    layer.free()
