@@ -652,7 +652,10 @@ void b200q_experts_free(b200q_experts *ex);
  * y must not overlap x, ids or wts; ids and wts may be what b200q_moe_route has
  * just written on the stream.  Rows do not depend on each other, and the same
  * call gives the same bits.  Each product is within 1e-5 of scale * sum |deq x| (down:
- * of h), sums are f32, h is rounded to 11 bits where the rows are bf16, and y once.
+ * of h), however large the values are that meet a weight of 0; sums are f32, h is
+ * rounded to 11 bits where the rows are bf16, and y once.  What a row (or an h) has beside
+ * much larger values is held to a part of its largest magnitude: 2^-50 (f32 rows,
+ * their h and that of f16 rows), 2^-40 (bf16 rows), 2^-39 (their h); f16 rows are exact.
  * Asynchronous, with a stream-ordered workspace of the library's pool; for decode steps:
  * more than 64 tokens (or 1024 slots) run in turns of that many, each of which
  * reads its experts again.

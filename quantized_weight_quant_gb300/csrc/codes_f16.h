@@ -53,23 +53,6 @@ __device__ __forceinline__ void fields(uint32_t w, int t, uint32_t &a, uint32_t 
     }
 }
 
-// As fields(), unsigned and without arithmetic: a field at bit b of an f16
-// subnormal is (c + zero point) 2^(b - 24); b = kShift<FMT> * t.
-template <int FMT> constexpr int kShift = FMT == B200Q_I4 ? 4 : FMT == B200Q_I2 ? 2 : 0;
-template <int FMT> constexpr float kZeroPoint = FMT == B200Q_I4 ? 8.f : FMT == B200Q_I2 ? 2.f : 128.f;
-template <int FMT>
-__device__ __forceinline__ void raw_fields(uint32_t w, int t, uint32_t &a, uint32_t &b) {
-    if constexpr (FMT == B200Q_I8) {
-        const uint32_t u = w ^ 0x80808080u;
-        a = __byte_perm(u, 0u, 0x4140);
-        b = __byte_perm(u, 0u, 0x4342);
-    } else {
-        const uint32_t mask = (FMT == B200Q_I4 ? 0x000F000Fu : 0x00030003u) << (kShift<FMT> * t);
-        a = w & mask;
-        b = (w >> 8) & mask;
-    }
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(

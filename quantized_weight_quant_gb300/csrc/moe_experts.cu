@@ -11,15 +11,15 @@
 //   * A tile is 16 rows for the warp-level tensor instruction m16n8k16: 16 rows
 //     of down, or 8 of gate and the same 8 of up, whose sums then meet in one
 //     thread.  A column is scaled by a power of two into f16's range, in two
-//     pieces (22 bits) where its type needs them.  Sums are f32, taken out of the
+//     pieces where its type needs them (moe_pieces).  Sums are f32, taken out of the
 //     tensor instruction's accumulator, which truncates, every 128 bytes of a row
 //     (1024 where there are many columns, every 4 where there are two pieces).
-//   * Codes meet f16 and bf16 rows as unsigned f16 subnormals, one AND for two of
-//     them, and the zero point times the column's sum is taken off at the end: the
-//     instruction aligns its products by their operands' exponents, so that the
-//     sums lose up to 10 of their bits (1e-6 to 1e-5 of a result, below the types'
-//     rounding).  f32 rows meet signed codes, exact in f16, one AND and one packed
-//     f16 FMA for two of them.
+//   * Codes are signed, exact in f16: one AND and one packed f16 FMA for two of them.
+//     A code of 0 then adds nothing, whatever it meets.  (Unsigned ones, the zero
+//     point times the column's sum taken off at the end, save the FMA, 4 to 8 % of a
+//     call; but their error goes by the column's largest value instead of by sum |deq x|:
+//     a value 10^3 times the rest on a weight of 0 took results 1 to 11 times the stated
+//     error away, one of 2^30 times took all of them.)
 //   * Few columns (moe_few_kernel, up to 8 per expert): the columns stay in shared
 //     memory.  A warp has its own ring of codes, brought by its own TMA boxes of 8
 //     rows x 128 bytes several lines ahead and across the tiles of the run: no
@@ -141,9 +141,11 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         wi = moe_way<FMT>(kind, pc_in, S, in_lines), wo = moe_way<FMT>(kind, pc_out, S, out_lines);
         if (kind == 2) {
             // What staging costs the kernel for few columns is about three steps; two pieces cost the other a quarter more.
-            // int8 6144 / 256, 8 experts, f32, 64 tokens of 2: 51 us with few, 100 with many (19 and 52 steps); int8
-            // 2048 / 1024, 4 experts, f32, 64 tokens of 2: 44 and 59 (23 and 24); int4 2048 / 1024, 32 experts, bf16, 64
-            // tokens of 4: 57 and 47 (30 and 24); int4 1024 / 512, 16 experts, bf16, 32 tokens of 4: 22 and 20 (4 and 6).
+            // Few and many columns, us (steps): int8 6144 / 256, 8 experts, f32, 64 tokens of 2: 52 and 102 (19 and 52); int8
+            // 2048 / 1024, 4 experts, f32, 64 of 2: 46 and 59 (23 and 24); int8 1024 / 2048, 4 experts, f16, 48 of 2: 39 and
+            // 51; int4 2048 / 1024, 32 experts, bf16, 64 of 4: 60 and 52 (30 and 24); int4 1024 / 512, 16 experts, bf16, 32
+            // of 4: 23 and 21 (4 and 6); int4 4096 / 4096, 8 experts, bf16, 64 of 2: 135 and 93; int2 2048 / 2048, 8
+            // experts, bf16, 40 of 4: 48 and 36.
             const Steps i = steps_of(S, a.k, ex.E, (int)((ex.F + 7ll) / 8), in_lines, wi.nc, n_sms);
             const Steps o = steps_of(S, a.k, ex.E, (int)((ex.D + 15ll) / 16), out_lines, wo.nc, n_sms);
             if (i.few + o.few + 3. < (pc_in == 2 ? 1.25 : 1.) * i.many + (pc_out == 2 ? 1.25 : 1.) * o.many) {
@@ -181,12 +183,12 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
     const bool prepare = kind != 1 && S > 2;
     const size_t n_x = kind == 2 ? (size_t)P * pc_in * in_lines * (16 * KC + 64) : prepare ? (size_t)S * pc_in * in_lines * 16 * KC : 0;
     const size_t n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * (16 * KC + 64) : 0;
-    const size_t n_info = prepare ? up16((size_t)P * 8) : 0;
+    const size_t n_info = prepare ? up16((size_t)P * 4) : 0;
     uint8_t *ws = nullptr;
     e = workspace_alloc((void **)&ws, n_h + n_part + (n_x > n_hc ? n_x : n_hc) + n_info, st);
     if (e != cudaSuccess) return e;
     float *h = (float *)ws, *sums = (float *)(ws + n_h);
-    float2 *info = (float2 *)(ws + n_h + n_part);
+    float *info = (float *)(ws + n_h + n_part);
     uint8_t *cols = ws + n_h + n_part + n_info;
     for (int s0 = 0; s0 < a.S && e == cudaSuccess; s0 += part) {
         const int n = a.S - s0 < part ? a.S - s0 : part;

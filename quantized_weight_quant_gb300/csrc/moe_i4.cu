@@ -4,7 +4,7 @@
 namespace qwq {
 
 template cudaError_t moe_launch_stream<B200Q_I4>(const MoeStream &, const MoeWay &, int, cudaStream_t);
-template cudaError_t moe_launch_prepare<B200Q_I4>(const MoeStream &, int, bool, uint8_t *, float2 *, cudaStream_t);
+template cudaError_t moe_launch_prepare<B200Q_I4>(const MoeStream &, int, bool, uint8_t *, float *, cudaStream_t);
 template <> MoeWay moe_way<B200Q_I4>(int kind, int pieces, int S, int lines) { return moe_way_of<B200Q_I4>(kind, pieces, S, lines); }
 
 }  // namespace qwq

@@ -129,9 +129,10 @@ template <> __device__ __forceinline__ float as_float<__half>(__half v) { return
 template <> __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // Where a product's columns come from: eight values of row `row` from c on, 0
-// from K on.  kExact: f16 holds them, scaled.  The tokens' rows:
+// from K on.  kTop: what the exponent of a column's largest value is brought to,
+// 15 where rounding to f16 cannot carry it past 65504.  The tokens' rows:
 template <class T> struct TokenRows {
-    static constexpr bool kExact = sizeof(T) == 2;
+    static constexpr int kTop = sizeof(T) == 2 ? 15 : 14;
     static __device__ __forceinline__ const T *at(const MoeStream &p, int row, int c) { return (const T *)p.x + row * p.ldx + c; }
     static __device__ __forceinline__ void load(const MoeStream &p, int row, int c, float (&v)[8]) {
         const T *r = at(p, row, c);
@@ -152,7 +153,7 @@ template <class T> struct TokenRows {
 };
 // h of the slots, in rows of ldh floats, a multiple of 8:
 struct GatedRows {
-    static constexpr bool kExact = false;
+    static constexpr int kTop = 14;
     static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
         if (c < p.K) {
@@ -166,7 +167,7 @@ struct GatedRows {
 };
 // act(gate) * up of the slices' sums, [ns_in][P][2][ldh]:
 struct SlicedRows {
-    static constexpr bool kExact = false;
+    static constexpr int kTop = 14;
     static __device__ __forceinline__ void load(const MoeStream &p, int slot, int c, float (&v)[8]) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
@@ -185,8 +186,8 @@ struct SlicedRows {
 };
 
 // The power of two that brings a column's largest magnitude (its bits) to
-// [2^14, 2^15); at most 2^126, so that the inverse is a normal number.
-__device__ __forceinline__ int exponent_for(unsigned top) { return top ? min(126, 14 + 127 - (int)(top >> 23)) : 0; }
+// [2^to, 2^(to + 1)); at most 2^126, so that the inverse is a normal number.
+__device__ __forceinline__ int exponent_for(unsigned top, int to) { return top ? min(126, to + 127 - (int)(top >> 23)) : 0; }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((unsigned)(127 + e) << 23); }
 
 __device__ __forceinline__ unsigned largest(const float (&v)[8]) {
@@ -225,49 +226,28 @@ __device__ __forceinline__ int unit_at(int u) {
     return u / (4 * V) * (64 * V) + u % V * 64 + u / V % 4 * 16;
 }
 
-// A unit's values, scaled, as 16 bytes of f16 in the order in which fields()
-// takes a word of codes apart, and what is left of them to `rest`; their sum as
-// they are then.  RAW: two by two they meet fields 0 0 1 1 of a word, or 2 2 3 3
-// (odd units of int2), and are divided by 2^b for a field at bit b.
-template <int FMT, int PC, bool RAW, bool EXACT>
-__device__ __forceinline__ float split(const float (&v)[8], float scale, int u, uint4 &hi, uint4 &rest) {
-    const float d0 = RAW && FMT == B200Q_I2 && (u & 1) ? 1.f / 16.f : 1.f;
-    const float d1 = RAW ? d0 / (float)(1 << kShift<FMT>) : 1.f;
+// A unit's values, scaled, as 16 bytes of f16 in the order in which fields() takes a
+// word of codes apart, and kRest times what is left of them to `rest`: a second
+// piece for what the first one rounds off, subnormal first pieces included.
+constexpr float kRest = 2048.f;
+template <int FMT, int PC>
+__device__ __forceinline__ void split(const float (&v)[8], float scale, uint4 &hi, uint4 &rest) {
     constexpr int kOrder[8] = {0, FMT == B200Q_I4 ? 4 : 1, 2, FMT == B200Q_I4 ? 6 : 3,
                                FMT == B200Q_I4 ? 1 : 4, 5, FMT == B200Q_I4 ? 3 : 6, 7};
     uint32_t h[4], l[4];
-    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float d = i < 2 ? d0 : d1;
-        float a = v[kOrder[2 * i]] * scale, b = v[kOrder[2 * i + 1]] * scale;
-        if constexpr (PC == 1 && EXACT) {      // rounds only what is 2^-38 of the column's largest or less
-            sum += a + b;
-            const __half2 t = __floats2half2_rn(a * d, b * d);
-            h[i] = *reinterpret_cast<const uint32_t *>(&t);
-        } else {
-            const __half2 t = __floats2half2_rn(a, b), td = RAW ? __hmul2(t, __float2half2_rn(d)) : t;
+        const float a = v[kOrder[2 * i]] * scale, b = v[kOrder[2 * i + 1]] * scale;
+        const __half2 t = __floats2half2_rn(a, b);
+        h[i] = *reinterpret_cast<const uint32_t *>(&t);
+        if constexpr (PC == 2) {
             const float2 f = __half22float2(t);
-            sum += f.x + f.y;
-            h[i] = *reinterpret_cast<const uint32_t *>(&td);
-            if constexpr (PC == 2) {
-                const __half2 r = __floats2half2_rn(a - f.x, b - f.y), rd = RAW ? __hmul2(r, __float2half2_rn(d)) : r;
-                const float2 rf = __half22float2(r);
-                sum += rf.x + rf.y;
-                l[i] = *reinterpret_cast<const uint32_t *>(&rd);
-            }
+            const __half2 r = __floats2half2_rn((a - f.x) * kRest, (b - f.y) * kRest);
+            l[i] = *reinterpret_cast<const uint32_t *>(&r);
         }
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     if constexpr (PC == 2) rest = make_uint4(l[0], l[1], l[2], l[3]);
-    return sum;
-}
-
-// Sum of a row's products with a column, from the accumulators' a: RAW codes are
-// 2^-24 of theirs, and the zero point times the column's sum comes off.
-template <bool RAW>
-__device__ __forceinline__ float product(float a, float zero, float scale, float unscale) {
-    return (RAW ? fmaf(a, 16777216.f, -zero) : a) * scale * unscale;
 }
 
 // The sums of rows r and r + 8 of a tile (8 of gate and up, or 16 of down) with
@@ -296,8 +276,8 @@ __device__ __forceinline__ void put(const MoeStream &p, int slice, int slot, int
 // further.  The words take NA accumulators in turn: an instruction waits for the
 // one before it on the same accumulator.  Two pieces: the first ones' sums are
 // taken out of the accumulator after every word of codes, the second ones are in
-// `rest`.
-template <int FMT, int N, int NT, int MT, int PC, bool RAW, int NA, class From>
+// `rest`, kRest times.
+template <int FMT, int N, int NT, int MT, int PC, int NA, class From>
 __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], From from, int plane, float (&sum)[MT][NT][4],
                                                float (&accs)[NA][MT][NT][4],
                                                float (&rests)[PC == 2 ? NA : 1][PC == 2 ? MT : 1][PC == 2 ? NT : 1][4]) {
@@ -314,13 +294,8 @@ __device__ __forceinline__ void chunk_products(const uint4 (&q)[MT][2], From fro
             const uint32_t w1 = w == 0 ? c1.x : w == 1 ? c1.y : w == 2 ? c1.z : c1.w;
 #pragma unroll
             for (int t = 0; t < MMAS; ++t) {
-                if constexpr (RAW) {
-                    raw_fields<FMT>(w0, t, a[m][t][0], a[m][t][2]);
-                    raw_fields<FMT>(w1, t, a[m][t][1], a[m][t][3]);
-                } else {
-                    fields<FMT>(w0, t, a[m][t][0], a[m][t][2]);
-                    fields<FMT>(w1, t, a[m][t][1], a[m][t][3]);
-                }
+                fields<FMT>(w0, t, a[m][t][0], a[m][t][2]);
+                fields<FMT>(w1, t, a[m][t][1], a[m][t][3]);
             }
         }
 #pragma unroll
@@ -361,9 +336,8 @@ constexpr int kFewColumns = kMoeFewColumns, kFewHeld = 16;  // of a chunk; of th
 
 struct FewColumns {
     unsigned top[kFewHeld];                    // the largest magnitude
-    float unscale[kFewHeld], zero[kFewHeld];   // the inverse scale; the zero point times the sum
+    float unscale[kFewHeld];                   // the inverse scale
     const float *scales[kFewHeld][2];          // of a chunk: its rows' scales, gate and up, or down twice
-    float part[kFewHeld][16];                  // the warps' sums
 };
 
 // W: warps of a block; AHEAD: lines in a warp's ring.
@@ -435,7 +409,7 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, int byt
 // n rows, lines l0 .. l1-1 of them, into shared memory as columns; row_of(c) is
 // column c's.  First their largest magnitudes, then once more to scale them.
 // Called by the whole block; ends with a barrier.
-template <int FMT, int PC, bool RAW, class Src, class RowOf>
+template <int FMT, int PC, class Src, class RowOf>
 __device__ __forceinline__ void stage_from(const MoeStream &p, RowOf row_of, int n, int l0, int l1, uint8_t *B, FewColumns &cl) {
     constexpr int KC = Fmt<FMT>::KC;
     const int units = (l1 - l0) * KC;          // of a column: KC to a line
@@ -461,52 +435,37 @@ __device__ __forceinline__ void stage_from(const MoeStream &p, RowOf row_of, int
     __syncthreads();
 #pragma unroll 1
     for (int c = c0; c < n; c += step) {
-        const int row = row_of(c), up = exponent_for(cl.top[c]);
+        const int row = row_of(c), up = exponent_for(cl.top[c], Src::kTop);
         const float scale = power(up);
-        float sum = 0.f;
         uint8_t *to = B + c * p.pitch;
 #pragma unroll 1
         for (int u = sub; u < units; u += 1 << lg) {
             float v[8];
             uint4 hi, rest;
             unit8<FMT, Src>(p, row, k0, u, v);
-            sum += split<FMT, PC, RAW, Src::kExact>(v, scale, u, hi, rest);
+            split<FMT, PC>(v, scale, hi, rest);
             *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u)) = hi;
             if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + unit_at<FMT>(u) + p.held * p.pitch) = rest;
-        }
-        if constexpr (RAW) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            if (lane == 0) cl.part[c][sub >> 5] = sum;
         }
         if (sub == 0) cl.unscale[c] = power(-up);
     }
     __syncthreads();
-    if (tid < n) {
-        float sum = 0.f;
-        if constexpr (RAW) {
-#pragma unroll 1
-            for (int w = 0; w < 1 << (lg - 5); ++w) sum += cl.part[tid][w];
-        }
-        cl.zero[tid] = sum * kZeroPoint<FMT>;
-    }
-    __syncthreads();
 }
 
-template <int FMT, int PC, bool RAW, class RowOf>
+template <int FMT, int PC, class RowOf>
 __device__ __forceinline__ void stage(const MoeStream &p, RowOf row_of, int n, int l0, int l1, uint8_t *B, FewColumns &cl) {
     if (p.down) {
-        if (p.ns_in == 1) stage_from<FMT, PC, RAW, GatedRows>(p, row_of, n, l0, l1, B, cl);
-        else stage_from<FMT, PC, RAW, SlicedRows>(p, row_of, n, l0, l1, B, cl);
-    } else if constexpr (!RAW) {
-        stage_from<FMT, PC, RAW, TokenRows<float>>(p, row_of, n, l0, l1, B, cl);
-    } else if constexpr (PC == 1) {            // with two pieces 16-bit rows are only h
-        if (p.type == B200Q_T_F16) stage_from<FMT, PC, RAW, TokenRows<__half>>(p, row_of, n, l0, l1, B, cl);
-        else stage_from<FMT, PC, RAW, TokenRows<__nv_bfloat16>>(p, row_of, n, l0, l1, B, cl);
+        if (p.ns_in == 1) stage_from<FMT, PC, GatedRows>(p, row_of, n, l0, l1, B, cl);
+        else stage_from<FMT, PC, SlicedRows>(p, row_of, n, l0, l1, B, cl);
+    } else if constexpr (PC == 2) {            // with two pieces 16-bit rows are only h
+        stage_from<FMT, PC, TokenRows<float>>(p, row_of, n, l0, l1, B, cl);
+    } else {
+        if (p.type == B200Q_T_F16) stage_from<FMT, PC, TokenRows<__half>>(p, row_of, n, l0, l1, B, cl);
+        else stage_from<FMT, PC, TokenRows<__nv_bfloat16>>(p, row_of, n, l0, l1, B, cl);
     }
 }
 
-template <int FMT, int PC, bool RAW, int W, int AHEAD>
+template <int FMT, int PC, int W, int AHEAD>
 __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_constant__ MoeStream p) {
     using Sh = FewShape<W, AHEAD>;
     constexpr int KC = Fmt<FMT>::KC;
@@ -625,16 +584,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                     copy_bulk((uint32_t)__cvta_generic_to_shared(B) + (col + (c < columns ? 0 : p.held)) * p.pitch, from, bytes, colbar);
                 }
             }
-            if (tid < columns) {
-                const float2 i = p.info[row_of(tid)];
-                cl.unscale[tid] = i.x;
-                cl.zero[tid] = slice == 0 ? i.y : 0.f;                 // of the whole row: taken off once
-            }
+            if (tid < columns) cl.unscale[tid] = p.info[row_of(tid)];
             if (ok) ok = mbar_wait(colbar, colparity, p.wait_ns);
             colparity ^= 1;
             __syncthreads();
         } else {
-            stage<FMT, PC, RAW>(p, row_of, columns, l0, l1, B, cl);
+            stage<FMT, PC>(p, row_of, columns, l0, l1, B, cl);
         }
 #pragma unroll 1
         for (; u < u1; u += groups) {
@@ -664,11 +619,11 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                 }
                 constexpr int NA = PC == 2 ? 2 : 4;
                 float acc[NA][1][1][4] = {}, rest[PC == 2 ? NA : 1][1][1][4] = {};
-                chunk_products<FMT, 1, 1, 1, PC, RAW, NA>(q, [&](int) { return xb; }, p.held * p.pitch, sum, acc, rest);
-                chunk_products<FMT, 1, 1, 1, PC, RAW, NA>(next, [&](int) { return xb + 8 * KC; }, p.held * p.pitch, sum, acc, rest);
+                chunk_products<FMT, 1, 1, 1, PC, NA>(q, [&](int) { return xb; }, p.held * p.pitch, sum, acc, rest);
+                chunk_products<FMT, 1, 1, 1, PC, NA>(next, [&](int) { return xb + 8 * KC; }, p.held * p.pitch, sum, acc, rest);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (PC == 2) sum[0][0][i] += rest[0][0][0][i] + rest[1][0][0][i];
+                    if constexpr (PC == 2) sum[0][0][i] = fmaf(rest[0][0][0][i] + rest[1][0][0][i], 1.f / kRest, sum[0][0][i]);
                     else sum[0][0][i] += (acc[0][0][0][i] + acc[1][0][0][i]) + (acc[2][0][0][i] + acc[3][0][0][i]);
                 }
             }
@@ -691,8 +646,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) moe_few_kernel(const __grid_co
                     for (int w = 0; w < wk; ++w) a0 += part[col * kRedPitch + w * Sh::kRedTile], b0 += part[col * kRedPitch + w * Sh::kRedTile + 8];
                 }
                 const int b = column(col);
-                const float un = cl.unscale[b], z = cl.zero[b];
-                put(p, slice, order[first + col], tile, r, product<RAW>(a0, z, sa, un), product<RAW>(b0, z, sb, un));
+                const float un = cl.unscale[b];
+                put(p, slice, order[first + col], tile, r, a0 * sa * un, b0 * sb * un);
                 a0 = a1, b0 = b1;
             }
         }
@@ -728,16 +683,15 @@ template <int FMT, int PC> struct ManyShape {
     static constexpr int kBytes = kPlanAt + (int)sizeof(Plan);
 };
 
-// A row of the tokens, or of h, per block, as pieces of f16 in the order of the
-// instructions; what the sums need of it to info.  Few columns read rows: [row]
+// A row of the tokens, or of h, per block, as pieces in the order of the
+// instructions; its inverse scale to info.  Few columns read rows: [row]
 // [piece][line][16 KC].  ORDERED, for many: where the plan has the row's slots, a
 // line of all of them side by side, [piece][line][place][kPitch], so that one copy
 // brings a chunk's.
-template <int FMT, int PC, bool RAW, bool ORDERED, class Src>
-__global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant__ MoeStream p, uint8_t *cols, float2 *info) {
+template <int FMT, int PC, bool ORDERED, class Src>
+__global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant__ MoeStream p, uint8_t *cols, float *info) {
     constexpr int KC = Fmt<FMT>::KC, kPitch = ManyShape<FMT, PC>::kPitch;
     __shared__ unsigned tops[8];
-    __shared__ float sums[8];
     __shared__ int places[kMoeMaxK];
     dependency_wait();
     let_dependents_start();
@@ -779,15 +733,14 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
     if (lane == 0) tops[warp] = m;
     __syncthreads();
     m = __reduce_max_sync(kAll, tops[lane & 7]);
-    const int up = exponent_for(m);
+    const int up = exponent_for(m, Src::kTop);
     const float scale = power(up);
-    float sum = 0.f;
 #pragma unroll 1
     for (int u = threadIdx.x; u < units; u += 256) {
         float v[8];
         uint4 hi, rest;
         unit8<FMT, Src>(p, row, 0, u, v);
-        sum += split<FMT, PC, RAW, Src::kExact>(v, scale, u, hi, rest);
+        split<FMT, PC>(v, scale, hi, rest);
         if constexpr (ORDERED) {
             const int line = unit_at<FMT>(u) / (16 * KC), in = unit_at<FMT>(u) - line * (16 * KC);
 #pragma unroll 1
@@ -803,20 +756,13 @@ __global__ void __launch_bounds__(256) moe_prepare_kernel(const __grid_constant_
             if constexpr (PC == 2) *reinterpret_cast<uint4 *>(to + (long long)p.lines * (16 * KC)) = rest;
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) sums[warp] = sum;
-    __syncthreads();
     if (threadIdx.x < slots) {
-        sum = 0.f;
-#pragma unroll 1
-        for (int w = 0; w < 8; ++w) sum += sums[w];
         const int at = ORDERED ? places[threadIdx.x] : row;
-        if (at >= 0) info[at] = make_float2(power(-up), RAW ? sum * kZeroPoint<FMT> : 0.f);
+        if (at >= 0) info[at] = power(-up);
     }
 }
 
-template <int FMT, int PC, bool RAW>
+template <int FMT, int PC>
 __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_constant__ MoeStream p) {
     using Sh = ManyShape<FMT, PC>;
     constexpr int KC = Fmt<FMT>::KC, NT = kManyColumns<FMT, PC> / 8, STAGES = kManyStages<FMT, PC>;
@@ -905,8 +851,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         const bool mine = warp < tiles_of(u, chunk, first);
         const int n = pl.n[chunk], tile = first + warp;
         // One piece: the sums are taken out of the accumulators after every kManyHeld lines.  An instruction drops up to
-        // an accumulator's last place, so that what is lost of a sum grows with the instructions between (64 of int4:
-        // 4e-6 of sum |x w| at most); over the whole row it would grow with the row.  Two: after every word of codes.
+        // an accumulator's last place, so that what is lost of a sum grows with the instructions between (64 of int4: 4e-6
+        // of their sum |deq x|); over the whole row it would grow with the row.  Two: after every word of codes.
         constexpr int NA = PC == 2 ? 1 : 2;
         float sum[1][NT][4] = {}, acc[NA][1][NT][4] = {}, sa = 0.f, sb = 0.f;
         if (mine) {
@@ -933,13 +879,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 #pragma unroll
                     for (int i = 0; i < 2; ++i) q[0][i] = *reinterpret_cast<const uint4 *>(from + i * second);
                     const uint8_t *b = at + Sh::kCodes + g * Sh::kPitch + half * (8 * KC) + tig * 16;
-                    chunk_products<FMT, N, NT, 1, PC, RAW, NA>(q, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
+                    chunk_products<FMT, N, NT, 1, PC, NA>(q, [&](int nt) { return b + nt * (8 * Sh::kPitch); }, Sh::kPlane, sum, acc, rest);
                 }
                 if constexpr (PC == 2) {
 #pragma unroll
                     for (int nt = 0; nt < N; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sum[0][nt][i] += rest[0][0][nt][i];
+                        for (int i = 0; i < 4; ++i) sum[0][nt][i] = fmaf(rest[0][0][nt][i], 1.f / kRest, sum[0][nt][i]);
                 }
             };
             if (mine) {
@@ -981,8 +927,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
                 for (int j = 0; j < 2; ++j) {
                     const int c = nt * 8 + 2 * tig + j;
                     if (c < n) {
-                        const float2 i = p.info[pl.first[chunk] + c];
-                        put(p, 0, order[c], tile, row, product<RAW>(sum[0][nt][j], i.y, sa, i.x), product<RAW>(sum[0][nt][2 + j], i.y, sb, i.x));
+                        const float un = p.info[pl.first[chunk] + c];
+                        put(p, 0, order[c], tile, row, sum[0][nt][j] * sa * un, sum[0][nt][2 + j] * sb * un);
                     }
                 }
         }
@@ -998,34 +944,34 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 }  // namespace
 
 // ---------------------------------------------------------------- launches
-template <int FMT, int PC, bool RAW>
+template <int FMT, int PC>
 cudaError_t moe_start(const MoeStream &p, const MoeWay &w, int n_sms, cudaStream_t st) {
     auto go = [&](auto kernel) {
         cudaError_t e = allow_dynamic_smem((const void *)kernel, 227 * 1024);
         return e != cudaSuccess ? e : launch_dependent(kernel, dim3(n_sms * w.blocks), 32 * w.warps, w.smem, st, p);
     };
-    if (w.kind == 2) return go(moe_many_kernel<FMT, PC, RAW>);
-    if (w.kind == 1) return go(moe_few_kernel<FMT, PC, RAW, 8, 4>);
-    return go(moe_few_kernel<FMT, PC, RAW, 16, 3>);
+    if (w.kind == 2) return go(moe_many_kernel<FMT, PC>);
+    if (w.kind == 1) return go(moe_few_kernel<FMT, PC, 8, 4>);
+    return go(moe_few_kernel<FMT, PC, 16, 3>);
 }
 
 template <int FMT>
 cudaError_t moe_launch_stream(const MoeStream &p, const MoeWay &w, int n_sms, cudaStream_t st) {
-    if (p.type == B200Q_T_F32) return moe_start<FMT, 2, false>(p, w, n_sms, st);
-    return moe_pieces(p.type, p.down) == 2 ? moe_start<FMT, 2, true>(p, w, n_sms, st) : moe_start<FMT, 1, true>(p, w, n_sms, st);
+    return moe_pieces(p.type, p.down) == 2 ? moe_start<FMT, 2>(p, w, n_sms, st) : moe_start<FMT, 1>(p, w, n_sms, st);
 }
 
 template <int FMT>
-cudaError_t moe_launch_prepare(const MoeStream &p, int rows, bool ordered, uint8_t *cols, float2 *info, cudaStream_t st) {
+cudaError_t moe_launch_prepare(const MoeStream &p, int rows, bool ordered, uint8_t *cols, float *info, cudaStream_t st) {
     auto go = [&](auto kernel) { return launch_dependent(kernel, dim3(rows), 256, 0, st, p, cols, info); };
     if (!ordered) {                            // few columns: the tokens' rows
-        if (p.type == B200Q_T_F32) return go(moe_prepare_kernel<FMT, 2, false, false, TokenRows<float>>);
-        if (p.type == B200Q_T_F16) return go(moe_prepare_kernel<FMT, 1, true, false, TokenRows<__half>>);
-        return go(moe_prepare_kernel<FMT, 1, true, false, TokenRows<__nv_bfloat16>>);
+        if (p.type == B200Q_T_F32) return go(moe_prepare_kernel<FMT, 2, false, TokenRows<float>>);
+        if (p.type == B200Q_T_F16) return go(moe_prepare_kernel<FMT, 1, false, TokenRows<__half>>);
+        return go(moe_prepare_kernel<FMT, 1, false, TokenRows<__nv_bfloat16>>);
     }
-    if (p.type == B200Q_T_F32) return p.down ? go(moe_prepare_kernel<FMT, 2, false, true, GatedRows>) : go(moe_prepare_kernel<FMT, 2, false, true, TokenRows<float>>);
-    if (p.type == B200Q_T_F16) return p.down ? go(moe_prepare_kernel<FMT, 2, true, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, true, TokenRows<__half>>);
-    return p.down ? go(moe_prepare_kernel<FMT, 1, true, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, true, TokenRows<__nv_bfloat16>>);
+    if (p.down) return moe_pieces(p.type, true) == 2 ? go(moe_prepare_kernel<FMT, 2, true, GatedRows>) : go(moe_prepare_kernel<FMT, 1, true, GatedRows>);
+    if (p.type == B200Q_T_F32) return go(moe_prepare_kernel<FMT, 2, true, TokenRows<float>>);
+    if (p.type == B200Q_T_F16) return go(moe_prepare_kernel<FMT, 1, true, TokenRows<__half>>);
+    return go(moe_prepare_kernel<FMT, 1, true, TokenRows<__nv_bfloat16>>);
 }
 
 // kind 0 and 1: as many columns as there are tokens, at most 8, and slices that

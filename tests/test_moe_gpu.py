@@ -752,3 +752,140 @@ def test_experts_that_give_up_report_it(q, S, k):
     assert q.device_status() == q.OK
     _check(q, layer, S, k, "bf16")
     layer.free()
+
+
+# ---------------------------------------------------------------- accuracy of the products
+def _pack(v, fmt):
+    """Host codes of whole numbers [O, I]."""
+    b = BITS[fmt]
+    c = (v + ZERO[fmt]).astype(np.uint8) if fmt != "i8" else v.astype(np.int8).view(np.uint8)
+    n = 8 // b
+    c = np.pad(c, ((0, 0), (0, -c.shape[1] % n)), constant_values=ZERO[fmt]).reshape(c.shape[0], -1, n).astype(np.uint32)
+    return (c << (b * np.arange(n, dtype=np.uint32))).sum(-1).astype(np.uint8)
+
+
+class Given:
+    """One expert of given whole numbers: gate and up [F, D], down [D, F], with one scale per row."""
+
+    def __init__(self, q, fmt, mats):
+        self.F, self.D = mats[0][0].shape
+        self.t = [q.tensor_upload(FMTS[fmt], *v.shape, _pack(v, fmt), np.asarray(s, np.float32)) for v, s in mats]
+        self.ex = q.Experts(*([t] for t in self.t))
+
+    def free(self):
+        self.ex.free()
+        for t in self.t:
+            t.free()
+
+
+def _given(q, layer, x, kind):
+    import torch
+    S = x.shape[0]
+    xd = torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda().to(_type(kind))
+    y = torch.full((S, layer.D), float("nan"), dtype=_type(kind), device="cuda")
+    q.moe_experts(layer.ex, xd, torch.zeros(S, 1, dtype=torch.int32, device="cuda"), torch.ones(S, 1, device="cuda"), y, S, 1, act=q.ACT_NONE)
+    torch.cuda.synchronize()
+    return _np64(xd), _np64(y)
+
+
+def _opposite(O, I, fmt, rng, zeros=0.0):
+    """Random whole numbers whose second half is the first's with the other sign: a row that repeats its first half in the second has product 0."""
+    top = {"i8": 127, "i4": 7, "i2": 1}[fmt]
+    half = rng.integers(-top, top + 1, (O, I // 2))
+    half[rng.random(half.shape) < zeros] = 0
+    return np.concatenate([half, -half], 1)
+
+
+def _one_of(O, I, of):
+    """[O, I] with a 1 in column of(o) of row o."""
+    v = np.zeros((O, I), np.int64)
+    v[np.arange(O), of(np.arange(O))] = 1
+    return v
+
+
+# tokens and sizes: one token, few columns, many columns (rows enough for all SMs)
+PRODUCTS = [(1, 2048, 48), (8, 2048, 48), (64, 8192, 2432)]
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("S,D,F", PRODUCTS)
+def test_experts_a_large_value_on_a_weight_of_zero(q, S, D, F, fmt):
+    """gate's product is 0 by opposite halves and a row's largest values meet codes of 0, so that sum |deq x| is that of the others alone; u = 1 and
+    y[d] = h[d % F] are exact.  The error has to stay within 1e-5 of that sum however large those values are."""
+    rng = np.random.default_rng(D + S)
+    gate, large = _opposite(F, D, fmt, rng, 0.3), rng.permutation(np.arange(1, D))[:3]
+    large[2] = D - 1                                             # in the last piece of the row
+    gate[:, 0] = gate[:, D // 2] = 0
+    gate[:, large] = gate[:, (large + D // 2) % D] = 0
+    layer = Given(q, fmt, [(gate, np.ones(F)), (_one_of(F, D, lambda o: 0 * o), np.ones(F)), (_one_of(D, F, lambda o: o % F), np.ones(D))])
+    for kind in TYPES:
+        for ratio in (1e3, 1e4, 2.0 ** 30):
+            x = synth.normal_f32((S, D), D, 1)
+            x[:, D // 2:] = x[:, :D // 2]
+            if kind == "f16":                                    # the largest of the type's values is 65504
+                x *= np.float32(min(1.0, 2.0 ** 15 / ratio))
+            x[:, large] = np.array([1, -1, 0.75]) * ratio * (min(1.0, 2.0 ** 15 / ratio) if kind == "f16" else 1.0)
+            x[:, 0] = 1
+            x, y = _given(q, layer, x, kind)
+            x[:, large] = 0
+            tol = 1e-5 * (np.abs(x) @ np.abs(gate).T.astype(np.float64))
+            worst = (np.abs(y) / tol[:, np.arange(D) % F]).max()
+            assert worst <= 1.01, "%s, largest %g times the rest: %g of the tolerance" % (kind, ratio, worst)
+    layer.free()
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("zeros", [0.5, 0.9, 0.999])
+@pytest.mark.parametrize("S,D,F", PRODUCTS)
+def test_experts_weights_near_zero(q, S, D, F, zeros, fmt):
+    """Rows of one sign on codes most of which are 0: the products' error goes by sum |deq x|, not by sum |x|."""
+    rng = np.random.default_rng(D + S)
+    gate = np.sign(_opposite(F, D, fmt, rng, zeros))
+    gate[:, 0] = gate[:, D // 2] = 0
+    layer = Given(q, fmt, [(gate, np.ones(F)), (_one_of(F, D, lambda o: 0 * o), np.ones(F)), (_one_of(D, F, lambda o: o % F), np.ones(D))])
+    for kind in TYPES:
+        x = 0.25 + np.abs(synth.normal_f32((S, D), D, 1))
+        x[:, D // 2:] = x[:, :D // 2]
+        x[:, 0] = 1
+        x, y = _given(q, layer, x, kind)
+        tol = 1e-5 * (np.abs(x) @ np.abs(gate).T.astype(np.float64))[:, np.arange(D) % F]
+        assert (np.abs(y) <= 1.01 * tol).all(), "%s: %g" % (kind, (np.abs(y) / np.maximum(tol, 1e-30)).max())
+    layer.free()
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("S,D,F", PRODUCTS)
+def test_experts_down_of_a_large_h_on_a_weight_of_zero(q, S, D, F, fmt):
+    """As above for down: h repeats its first half, two of its values are 2^10, 2^14 or 2^30 times the rest and meet codes of 0."""
+    rng = np.random.default_rng(D + S + 1)
+    down, large = _opposite(D, F, fmt, rng, 0.3), np.array([3, F - 2])
+    down[:, large] = down[:, (large + F // 2) % F] = 0
+    for log in (10, 14, 30):
+        scale = np.ones(F)
+        scale[large] = 2.0 ** (log // 2)
+        layer = Given(q, fmt, [(_one_of(F, D, lambda o: 1 + o % (F // 2)), scale), (_one_of(F, D, lambda o: 0 * o), scale), (down, np.ones(D))])
+        for kind in TYPES:
+            x = np.abs(synth.normal_f32((S, D), D, 1)) + 0.25
+            x[:, 0] = 1
+            x, y = _given(q, layer, x, kind)
+            h = x[:, 1 + np.arange(F) % (F // 2)]
+            tol = 1e-5 * (np.abs(h) @ np.abs(down).T.astype(np.float64))
+            worst = (np.abs(y) / tol).max()
+            assert worst <= 1.01, "%s, largest 2^%d times the rest: %g of the tolerance" % (kind, log, worst)
+        layer.free()
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("S,D,F", PRODUCTS)
+def test_experts_matrix_of_zeros(q, S, D, F, fmt):
+    """A matrix of zeros with scales that are not: y is 0."""
+    rng = np.random.default_rng(5)
+    some = lambda O, I: _opposite(O, I, fmt, rng)  # noqa: E731
+    zero = lambda O, I: np.zeros((O, I), np.int64)  # noqa: E731
+    for m in range(3):
+        mats = [(zero if m == j else some)(*s) for j, s in enumerate([(F, D), (F, D), (D, F)])]
+        layer = Given(q, fmt, [(v, np.full(v.shape[0], 0.37)) for v in mats])
+        for kind in TYPES:
+            x, y = _given(q, layer, synth.normal_f32((S, D), D, 1) + 0.5, kind)
+            assert (y == 0).all(), "%s: %g" % (kind, np.abs(y).max())
+        layer.free()
