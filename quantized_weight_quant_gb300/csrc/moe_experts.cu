@@ -16,10 +16,9 @@
 //     (1024 where there are many columns, every 4 where there are two pieces).
 //   * Codes are signed, exact in f16: one AND and one packed f16 FMA for two of them.
 //     A code of 0 then adds nothing, whatever it meets.  (Unsigned ones, the zero
-//     point times the column's sum taken off at the end, save the FMA, 4 to 8 % of a
+//     point times the column's sum taken off at the end, save the FMA, 5 to 10 % of a
 //     call; but their error goes by the column's largest value instead of by sum |deq x|:
-//     a value 10^3 times the rest on a weight of 0 took results 1 to 11 times the stated
-//     error away, one of 2^30 times took all of them.)
+//     a value 10^3 times the rest on a weight of 0 left errors 1 to 11 times the stated ones.)
 //   * Few columns (moe_few_kernel, up to 8 per expert): the columns stay in shared
 //     memory.  A warp has its own ring of codes, brought by its own TMA boxes of 8
 //     rows x 128 bytes several lines ahead and across the tiles of the run: no

@@ -82,11 +82,12 @@ template <int NV> struct Row {
 
 __device__ __forceinline__ unsigned first_lane(bool is) { return __ffs(__ballot_sync(kAll, is)) - 1; }
 
-// The values of the groups, lane g that of group g, from c's keys: of groups of
+// The values of the groups, lane g that of group g, from c's keys, and the sums of the
+// magnitudes in them, by which they are rounded (their signs may differ): of groups of
 // 32 m neighbours the m registers' two largest over the warp; of 2, 4, 8 or 16 neighbours
 // over as many lanes; of another number by a walk over c in shared memory.
 template <int NV>
-__device__ __forceinline__ float group_values(const Route &p, int lane, int n, const unsigned (&kc)[NV], float *by) {
+__device__ __forceinline__ float group_values(const Route &p, int lane, int n, const unsigned (&kc)[NV], float *by, float &size) {
     unsigned a = 0, b = 0;                   // of this lane's group: the two largest keys
     if (n % 32 == 0) {
         unsigned ga = 0, gb = 0;
@@ -135,11 +136,14 @@ __device__ __forceinline__ float group_values(const Route &p, int lane, int n, c
         }
         __syncwarp();
     }
+    size = 0.f;
     if (a == 0) return -INFINITY;
-    return value_of(a) + (p.group_top > 1 && b ? value_of(b) : 0.f);
+    const float va = value_of(a), vb = p.group_top > 1 && b ? value_of(b) : 0.f;
+    size = fabsf(va) + fabsf(vb);
+    return va + vb;
 }
 template <int NV>
-__device__ __forceinline__ double group_values(const Route &p, int lane, int n, const unsigned long long (&kc)[NV], double *by) {
+__device__ __forceinline__ double group_values(const Route &p, int lane, int n, const unsigned long long (&kc)[NV], double *by, double &) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (lane + 32 * i < p.E) by[lane + 32 * i] = __longlong_as_double((long long)kc[i]);
@@ -188,7 +192,8 @@ __device__ __forceinline__ void keys_of(const Route &p, const Row<NV> &r, int la
     }
     if (p.n_group == 1) return;
     const int n = p.E / p.n_group;
-    const V value = group_values<NV>(p, lane, n, kc, reinterpret_cast<V *>(r.sm + p.E + (p.E & 1)));
+    V size = 0;
+    const V value = group_values<NV>(p, lane, n, kc, reinterpret_cast<V *>(r.sm + p.E + (p.E & 1)), size);
     // place: how many groups have a larger value, or the same and a lower index
     int place = 0;
     V least = INFINITY;                      // to the next lower or equal value
@@ -199,11 +204,12 @@ __device__ __forceinline__ void keys_of(const Route &p, const Row<NV> &r, int la
         else if (g != lane) least = value - o < least ? value - o : least;
     }
     const unsigned stays = __ballot_sync(kAll, lane < p.n_group && place < p.topk_group);
-    if (near && scored) {
-        // only the last group that stays has to be told from the next.  A value that is infinite or NaN is left to f64.
-        const bool last = lane < p.n_group && place == p.topk_group - 1 && p.topk_group < p.n_group && value > -INFINITY;
-        const float eps = (p.score == B200Q_SCORE_SOFTMAX ? 1.2e-5f : 1.8e-6f) + 3e-7f * fabsf((float)value);
-        if (__any_sync(kAll, last && !((float)least > eps))) *near = true;
+    if (near && scored && p.topk_group < p.n_group) {
+        // Only the last group that stays has to be told from the next.  Sums that are infinite or NaN are left to f64.
+        const bool last = lane < p.n_group && place == p.topk_group - 1 && value > -INFINITY;
+        const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint((float)size)));
+        const float eps = (p.score == B200Q_SCORE_SOFTMAX ? 1.2e-5f : 1.8e-6f) + 3e-7f * most;
+        if (__any_sync(kAll, (last && !((float)least > eps)) || !(most < INFINITY))) *near = true;
     }
     const Quotient &by_n = p.by_group;
 #pragma unroll

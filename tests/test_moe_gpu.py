@@ -889,3 +889,36 @@ def test_experts_matrix_of_zeros(q, S, D, F, fmt):
             x, y = _given(q, layer, synth.normal_f32((S, D), D, 1) + 0.5, kind)
             assert (y == 0).all(), "%s: %g" % (kind, np.abs(y).max())
         layer.free()
+
+
+# ---------------------------------------------------------------- decisions and sums where f32 alone is not enough
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("size", [0.5, 32.0, 100.0, 1000.0])
+@pytest.mark.parametrize("n,per,keep", [(2, 2, 1), (8, 8, 3), (4, 33, 2), (32, 32, 5), (16, 3, 4)])
+def test_route_groups_whose_biases_cancel(q, n, per, keep, size, score):
+    """Every group has one large positive bias and for the rest the same negative one: its value is a small sum of two large c, and neighbouring
+    groups' values are nearer than the roundings of those."""
+    E, S = n * per, 24
+    bias = np.full(E, -size, np.float32)
+    bias[np.arange(n) * per + (np.arange(n) * 7) % per] = size
+    l = synth.normal_f32((S, E), E, 1)
+    l[1::3] = 0.01 * l[1::3]
+    l[2::3] = np.float32(1e-4) * l[2::3] + 0.5
+    for norm in (False, True):
+        _route(q, _dev(l), min(2, per), score, bias, n, keep, 2, norm)
+
+
+def test_route_two_groups_that_f32_takes_for_the_wrong_order(q):
+    l = np.array([[-0.81081446, 0.75224382, 0.25344652, -0.30490190]], np.float32)
+    got = _route(q, _dev(l), 2, 1, np.array([32, -32, 32, -32], np.float32), 2, 1, 2)
+    assert got[0].tolist() == [[0, 1]]
+
+
+@pytest.mark.parametrize("big", [3.0e38, 2.0e38])
+def test_route_group_values_past_f32(q, big):
+    """Sums of two biases that f32 does not hold, of either sign."""
+    l = synth.normal_f32((6, 16), 1, 1)
+    for signs in ((1, 1, -1, -1), (-1, -1, -1, -1), (1, 1, 1, 1), (-1, 1, -1, 1)):
+        bias = np.repeat(np.array(signs, np.float32) * np.float32(big), 4) * (1 - np.float32(1e-6) * (np.arange(16, dtype=np.float32) % 5))
+        for keep in (1, 2, 3):
+            _route(q, _dev(l), 4, 1, bias.astype(np.float32), 4, keep, 2)
