@@ -684,7 +684,8 @@ int b200q_moe_experts(const b200q_experts *ex, const void *x, int type, long lon
  * must not overlap gate, w_post or w.  Everything is f32 between the reads and
  * the writes: y comes from the f32 h', which is rounded to `type` only where it is
  * stored.  Within 1e-5 of the formula, |h'| taken as res_scale |h| + |out_scale
- * gate p|.  A NaN or an infinity in a row makes that row's y not finite or
+ * gate p|, for finite rows of any size (a row whose squares f32 does not hold is
+ * summed again, scaled).  A NaN or an infinity in a row makes that row's y not finite or
  * NaN.  S = 0 is a no-op.  One launch, no workspace.
  */
 int b200q_block_norm(const void *m, int type, long long ldm, const void *h, long long ldh, const void *gate,

@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "launch.h"
 #include "qwq_internal.h"
 
@@ -68,21 +70,23 @@ __device__ __forceinline__ void store(T *p, const float (&v)[VE]) {
     o.put(p);
 }
 
-// Sum over the threads of a row: a warp, or the block.  `set` alternates from one
-// sum of the block to the next: the barrier of each keeps the one before it apart
-// from the one after.
+// Sum, or maximum of what is not negative, over the threads of a row: a warp, or the
+// block.  `set` alternates from one of the block to the next: the barrier of each
+// keeps the one before it apart from the one after.  Every thread has the same bits.
+template <bool MAX = false>
 __device__ __forceinline__ float row_sum(float v, int &set) {
     __shared__ float red[2][32];
+    auto with = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v = with(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (warps == 1) return v;
     if (lane == 0) red[set][threadIdx.x >> 5] = v;
     __syncthreads();
     v = lane < warps ? red[set][lane] : 0.f;
     set ^= 1;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v = with(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
@@ -91,8 +95,25 @@ __device__ __forceinline__ float row_sum(float v, int &set) {
 constexpr int most_threads(int nv) { return nv == 1 ? 1024 : nv == 2 ? 384 : 512; }
 constexpr int least_blocks(int nv) { return nv == 2 ? 3 : 1; }
 
-// 1 / rms of D values whose squares' sum is ss.
-__device__ __forceinline__ float inverse_rms(float ss, const BlockNorm &a) { return rsqrtf(__fdividef(ss, (float)a.D) + a.eps); }
+// 1 / rms of D values whose squares' sum is ss, all of them times pre, as their root is.
+__device__ __forceinline__ float inverse_rms(float ss, const BlockNorm &a, float pre = 1.f) {
+    return rsqrtf(__fdividef(ss, (float)a.D) + a.eps * pre * pre);
+}
+
+// Whether f32 does not hold the squares of a row: their sum is past its largest number,
+// or so small that single ones vanish (with an eps above 2^-100 they may).  Such a row
+// is summed once more times a power of two; its largest magnitude tells which: it or
+// sqrt(eps) comes near 2^40.  Not where it is 0 or infinite, nor for a NaN.
+__device__ __forceinline__ bool out_of_range(float ss, const BlockNorm &a) {
+    const float t = __fdividef(ss, (float)a.D) + a.eps;
+    return t < 0x1p-100f || t > 0x1.fffffep127f;
+}
+__device__ __forceinline__ float factor_for(float top, const BlockNorm &a) {
+    if (!(top > 0.f && top < INFINITY)) return 1.f;
+    const int of_top = (int)(__float_as_uint(top) >> 23) - 127, of_eps = ((int)(__float_as_uint(a.eps) >> 23) - 127) >> 1;
+    const int e = min(127, 40 - (a.eps > 0.f ? max(of_top, of_eps) : of_top));
+    return __uint_as_float((unsigned)(127 + e) << 23);
+}
 
 // A thread's values: NV vectors of VE neighbours, the threads' next to each other,
 // and where the vectors leave a row's first and last few out, one of those (a path
@@ -169,14 +190,36 @@ __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) block_norm
         float scale = a.out_scale;
         if (a.gate && !each) scale *= to_f(((const T *)a.gate)[row * a.ldg]);
         if (a.w_post) {
-            float ss = ed >= 0 ? to_f(me) * to_f(me) : 0.f;
+            auto squares = [&]() {
+                float ss = ed >= 0 ? to_f(me) * to_f(me) : 0.f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if (k * (int)blockDim.x + tid < nv) {
+                for (int k = 0; k < NV; ++k)
+                    if (k * (int)blockDim.x + tid < nv) {
 #pragma unroll
-                    for (int j = 0; j < VE; ++j) ss = fmaf(to_f(mv[k].e[j]), to_f(mv[k].e[j]), ss);
+                        for (int j = 0; j < VE; ++j) ss = fmaf(to_f(mv[k].e[j]), to_f(mv[k].e[j]), ss);
+                    }
+                return row_sum(ss, set);
+            };
+            float ss = squares(), pre = 1.f;
+            if constexpr (!std::is_same<T, __half>::value) {               // f32 holds the squares of f16
+                if (out_of_range(ss, a)) {
+                    float top = ed >= 0 ? fabsf(to_f(me)) : 0.f;
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+                        if (k * (int)blockDim.x + tid < nv) {
+#pragma unroll
+                            for (int j = 0; j < VE; ++j) top = fmaxf(top, fabsf(to_f(mv[k].e[j])));
+                        }
+                    pre = factor_for(row_sum<true>(top, set), a);
+                    if (ed >= 0) me = from_f<T>(to_f(me) * pre);           // exact, but for what is below the row's last place
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int j = 0; j < VE; ++j) mv[k].e[j] = from_f<T>(to_f(mv[k].e[j]) * pre);
+                    ss = squares();
                 }
-            scale *= inverse_rms(row_sum(ss, set), a);
+            }
+            scale *= inverse_rms(ss, a, pre);
         }
         float v[NV][VE], ve = 0.f, ss = 0.f;
 #pragma unroll
@@ -222,7 +265,28 @@ __global__ void __launch_bounds__(most_threads(NV), least_blocks(NV)) block_norm
             if (ed >= 0) o[ed] = from_f<T>(ve);
         }
         if (a.y) {
-            const float root = inverse_rms(row_sum(ss, set), a);
+            float pre = 1.f;
+            ss = row_sum(ss, set);
+            if (out_of_range(ss, a)) {
+                float top = ed >= 0 ? fabsf(ve) : 0.f;
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (k * (int)blockDim.x + tid < nv) {
+#pragma unroll
+                        for (int j = 0; j < VE; ++j) top = fmaxf(top, fabsf(v[k][j]));
+                    }
+                pre = factor_for(row_sum<true>(top, set), a);
+                ve *= pre;
+                ss = ed >= 0 ? ve * ve : 0.f;
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (k * (int)blockDim.x + tid < nv) {
+#pragma unroll
+                        for (int j = 0; j < VE; ++j) v[k][j] *= pre, ss = fmaf(v[k][j], v[k][j], ss);
+                    }
+                ss = row_sum(ss, set);
+            }
+            const float root = inverse_rms(ss, a, pre);
             Y *y = (Y *)a.y + now * a.ldy;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -253,32 +317,36 @@ __global__ void __launch_bounds__(kLongThreads) block_norm_long_kernel(const __g
     T *o = a.h_out ? (T *)a.h_out + row * a.ldo : nullptr;
     Y *y = a.y ? (Y *)a.y + row * a.ldy : nullptr;
     const unsigned D = a.D;                      // d passes 2^31 - 1 by up to a block
-    float post = a.out_scale;
+    // 1 / rms of the values of(d), times the power of two `pre` where f32 does not hold their squares
     int set = 0;
-    if (a.w_post) {
+    auto root_of = [&](auto of, float &pre) {
+        pre = 1.f;
         float ss = 0.f;
-        for (unsigned d = threadIdx.x; d < D; d += kLongThreads) ss = fmaf(to_f(m[d]), to_f(m[d]), ss);
-        post *= inverse_rms(row_sum(ss, set), a);
-    }
+        for (unsigned d = threadIdx.x; d < D; d += kLongThreads) ss = fmaf(of(d), of(d), ss);
+        ss = row_sum(ss, set);
+        if (out_of_range(ss, a)) {
+            float top = 0.f;
+            for (unsigned d = threadIdx.x; d < D; d += kLongThreads) top = fmaxf(top, fabsf(of(d)));
+            pre = factor_for(row_sum<true>(top, set), a);
+            ss = 0.f;
+            for (unsigned d = threadIdx.x; d < D; d += kLongThreads) ss = fmaf(of(d) * pre, of(d) * pre, ss);
+            ss = row_sum(ss, set);
+        }
+        return inverse_rms(ss, a, pre);
+    };
+    float post = a.out_scale, pre_m = 1.f, pre_h = 1.f, root = 0.f;
+    if (a.w_post) post *= root_of([&](unsigned d) { return to_f(m[d]); }, pre_m);
     auto next = [&](unsigned d) {
-        float p = to_f(m[d]) * post;
+        float p = to_f(m[d]) * pre_m * post;
         if (a.w_post) p *= a.w_post[d];
         if (g) p *= to_f(g[a.gate_cols == 1 ? 0 : d]);
         return h ? fmaf(a.res_scale, to_f(h[d]), p) : p;
     };
-    float root = 0.f;
-    if (y) {
-        float ss = 0.f;
-        for (unsigned d = threadIdx.x; d < D; d += kLongThreads) {
-            const float v = next(d);
-            ss = fmaf(v, v, ss);
-        }
-        root = inverse_rms(row_sum(ss, set), a);
-    }
+    if (y) root = root_of(next, pre_h);
     for (unsigned d = threadIdx.x; d < D; d += kLongThreads) {
         const float v = next(d);                 // before this thread's write of h_out[d], which may be h or m
         if (o) o[d] = from_f<T>(v);
-        if (y) y[d] = from_f<Y>(v * (root * a.w[d]));
+        if (y) y[d] = from_f<Y>(v * pre_h * (root * a.w[d]));
     }
 }
 

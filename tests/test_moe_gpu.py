@@ -922,3 +922,33 @@ def test_route_group_values_past_f32(q, big):
         bias = np.repeat(np.array(signs, np.float32) * np.float32(big), 4) * (1 - np.float32(1e-6) * (np.arange(16, dtype=np.float32) % 5))
         for keep in (1, 2, 3):
             _route(q, _dev(l), 4, 1, bias.astype(np.float32), 4, keep, 2)
+
+
+RANGES = [(1, 6144), (5, 8), (400, 64), (310, 96), (311, 1003), (400, 6144), (2, 16385), (1, 40000)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("S,D", RANGES)
+def test_norm_rows_of_any_finite_size(q, S, D, kind):
+    """Squares that f32 does not hold, too large and (eps = 0, or as small) too small; rows of ordinary size among them; zeros stay zeros."""
+    a, b = (synth.normal_f32((S, D), D, j) for j in (1, 2))
+    wp, w = (_dev(0.5 + np.abs(synth.normal_f32((D,), D, j))) for j in (3, 4))
+    for log, eps in ((62, 1e-6), (62, 0.0), (120, 1e-6), (-63, 1e-38), (-80, 0.0), (-80, 1e-35), (-80, 1e-6), (-100, 0.0)):
+        size = np.exp2(np.where(np.arange(S) % 3 == 1, 0, log)).astype(np.float32)[:, None]
+        m, h = _dev(a * size, kind), _dev(b * size, kind)
+        _norm(q, m, h, None, wp, w, 1.0, 0.5, kind, "f32", eps=eps)              # p of ordinary size beside h
+        _norm(q, m, h, None, None, w, 1.0, 0.5, kind, kind, eps=eps)
+        _norm(q, m, None, None, wp, w, kind=kind, ykind="f32", eps=eps)
+        _norm(q, m, None, _dev(synth.normal_f32((S, 1), D, 5), kind), None, w, kind=kind, ykind="f32", eps=eps, out=False)
+
+
+def test_norm_one_large_value_and_subnormal_rows(q):
+    S, D = 3, 1024
+    m = 0.1 * synth.normal_f32((S, D), 1, 1)
+    m[0, 77] = 3.0e38
+    m[1] *= np.float32(2.0 ** -140)
+    m[2, 0] = -2.0 ** 70
+    w = _dev(np.ones(D))
+    for eps in (0.0, 1e-6):
+        _norm(q, _dev(m), None, None, w, w, eps=eps)
+        _norm(q, _dev(m), None, None, None, w, eps=eps)
