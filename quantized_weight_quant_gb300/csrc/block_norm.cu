@@ -376,7 +376,7 @@ cudaError_t start(const BlockNorm &a, cudaStream_t st) {
     const dim3 grid((unsigned)(rows < (long long)on_sm * sms ? rows : (long long)on_sm * sms));
     const size_t smem = SHIFT ? (size_t)3 * VE * (a.D / VE + 1) * 4 : 0;
     auto go = [&](auto kernel) {
-        if (smem > 48 * 1024) {
+        if (smem > 40 * 1024) {                  // 48 KB in all without asking, the sums' own included
             cudaError_t r = allow_dynamic_smem((const void *)kernel, (int)smem);
             if (r != cudaSuccess) return r;
         }

@@ -952,3 +952,12 @@ def test_norm_one_large_value_and_subnormal_rows(q):
     for eps in (0.0, 1e-6):
         _norm(q, _dev(m), None, None, w, w, eps=eps)
         _norm(q, _dev(m), None, None, None, w, eps=eps)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("D", [4069, 4073, 4081, 4087, 4093, 4095])
+def test_norm_odd_rows_whose_weights_fill_48_kb(q, D, kind):
+    """Rows of an odd stride keep their weights in shared memory: about what a kernel may have without asking for more."""
+    m, h = (_dev(synth.normal_f32((3, D), D, j), kind) for j in (1, 2))
+    wp, w = (_dev(0.5 + np.abs(synth.normal_f32((D,), D, j))) for j in (3, 4))
+    _norm(q, m, h, _dev(synth.normal_f32((1, D), D, 5), kind), wp, w, 0.7, 0.25, kind, kind)
