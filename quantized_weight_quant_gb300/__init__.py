@@ -542,7 +542,8 @@ def experts_create(gate, up, down) -> int:
     h = lib.b200q_experts_create(*(_ptr_array(a, _h) for a in (gate, up, down)), len(gate))
     if not h:
         msg = last_error()
-        raise B200QError(ENOMEM if "memory" in msg else EINVAL, msg)
+        cuda = "cudaError" in msg or "tensor map" in msg
+        raise B200QError(ENOMEM if "memory" in msg else ECUDA if cuda else EINVAL, msg)
     return h
 
 

@@ -93,3 +93,18 @@ def test_self_test_refusals(q):
             q.selftest_moe(*bad)
     q.selftest_moe(5, True)
     q.selftest_moe()
+
+
+def test_experts_create_tells_a_failed_call_from_a_bad_argument(q, monkeypatch):
+    class Failing:
+        def b200q_experts_create(self, *a):
+            return None
+    monkeypatch.setattr(q, "lib", Failing())
+    for msg, status in (("b200q_experts_create: out of host memory", q.ENOMEM), ("b200q_experts_create: out of memory (cudaErrorMemoryAllocation)", q.ENOMEM),
+                        ("b200q_experts_create: encoding a tensor map failed", q.ECUDA),
+                        ("b200q_experts_create: unspecified launch failure (cudaErrorLaunchFailure)", q.ECUDA),
+                        ("b200q_experts_create: gate 0 is not [8, 8] in the first tensor's format", q.EINVAL)):
+        monkeypatch.setattr(q, "last_error", lambda: msg)
+        with pytest.raises(q.B200QError) as e:
+            q.experts_create([1], [2], [3])
+        assert e.value.status == status
