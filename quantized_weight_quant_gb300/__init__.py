@@ -543,7 +543,7 @@ def experts_create(gate, up, down) -> int:
     if not h:
         msg = last_error()
         cuda = "cudaError" in msg or "tensor map" in msg
-        raise B200QError(ENOMEM if "memory" in msg else ECUDA if cuda else EINVAL, msg)
+        raise B200QError(ENOMEM if "out of" in msg else ECUDA if cuda else EINVAL, msg)
     return h
 
 

@@ -103,6 +103,7 @@ def test_experts_create_tells_a_failed_call_from_a_bad_argument(q, monkeypatch):
     for msg, status in (("b200q_experts_create: out of host memory", q.ENOMEM), ("b200q_experts_create: out of memory (cudaErrorMemoryAllocation)", q.ENOMEM),
                         ("b200q_experts_create: encoding a tensor map failed", q.ECUDA),
                         ("b200q_experts_create: unspecified launch failure (cudaErrorLaunchFailure)", q.ECUDA),
+                        ("b200q_experts_create: a message on memory (cudaErrorInvalidValue)", q.ECUDA),
                         ("b200q_experts_create: gate 0 is not [8, 8] in the first tensor's format", q.EINVAL)):
         monkeypatch.setattr(q, "last_error", lambda: msg)
         with pytest.raises(q.B200QError) as e:
