@@ -602,10 +602,11 @@ def block_norm(m, S: int, D: int, eps: float, h=None, h_out=None, w_post=None, g
     yp, ty, ldy = _wide(y, S, D, "y") if y is not None else (0, t, 0)
     gp, ldg, gc = 0, 0, D
     if gate is not None:
-        if gate.dim() == 1:
-            gate = gate[None]
-        gc = gate.shape[1] if gate.dim() == 2 and gate.shape[1] == 1 else D
-        rows = 1 if gate.shape[0] == 1 else S
+        shape = tuple(getattr(gate, "shape", ()))
+        if len(shape) == 1:
+            gate, shape = gate[None], (1, *shape)
+        rows = 1 if shape[:1] == (1,) else S
+        gc = 1 if shape[1:] == (1,) else D
         gp, _, ldg = _wide(gate, rows, gc, "gate", t)
         if rows == 1:
             ldg = 0

@@ -961,3 +961,13 @@ def test_norm_odd_rows_whose_weights_fill_48_kb(q, D, kind):
     m, h = (_dev(synth.normal_f32((3, D), D, j), kind) for j in (1, 2))
     wp, w = (_dev(0.5 + np.abs(synth.normal_f32((D,), D, j))) for j in (3, 4))
     _norm(q, m, h, _dev(synth.normal_f32((1, D), D, 5), kind), wp, w, 0.7, 0.25, kind, kind)
+
+
+def test_norm_gates_that_are_refused(q):
+    import torch
+    m, o, one = _dev(np.ones((3, 8))), _dev(np.ones((3, 8))), torch.ones
+    for gate, what in ((2.0, TypeError), (np.ones(8, np.float32), TypeError), (one((), device="cuda"), ValueError), (one(3, 8, 1, device="cuda"), ValueError),
+                       (one(7, device="cuda"), ValueError), (one(2, 8, device="cuda"), ValueError), (one(2, 1, device="cuda"), ValueError),
+                       (one(3, 8), ValueError), (one(3, 8, device="cuda").half(), ValueError), (one(8, 3, device="cuda").t(), ValueError)):
+        with pytest.raises(what):
+            q.block_norm(m, 3, 8, 1e-6, h_out=o, gate=gate)
