@@ -1001,7 +1001,6 @@ b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q
             };
             if (rc == B200Q_OK && !(encode(&host[e].map[m], 8) && encode(&host[e].wide[m], 64)))
                 rc = fail(B200Q_ECUDA, "%s: encoding a tensor map failed", who);
-            host[e].codes[m] = t.codes;
             host[e].scales[m] = t.scales;
         }
     if (rc == B200Q_OK) {

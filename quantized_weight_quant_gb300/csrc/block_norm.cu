@@ -363,7 +363,6 @@ cudaError_t start(const BlockNorm &a, cudaStream_t st) {
     int nv = 1;
     auto threads = [&](int n) { return ((units + n - 1) / n + 31) / 32 * 32; };
     while (nv < 4 && threads(nv) > (many && nv == 1 ? 128 : most_threads(nv))) nv *= 2;
-    if (nv == 4 && threads(4) > most_threads(4) && threads(1) <= most_threads(1)) nv = 1;
     dim3 block(threads(nv));
     if ((int)block.x > most_threads(nv))
         return launch_dependent(block_norm_long_kernel<T, Y>, dim3(a.S), kLongThreads, 0, st, a);

@@ -187,8 +187,7 @@ cudaError_t launch_moe_route(const Route &a, cudaStream_t st);
 struct Expert {
     CUtensorMap map[3];        // codes as bytes, box 8 rows x 128 bytes, 128-byte swizzle
     CUtensorMap wide[3];       // the same, box 64 rows
-    const uint8_t *codes[3];   // gate, up [F, D], down [D, F]
-    const float *scales[3];
+    const float *scales[3];    // gate, up [F, D], down [D, F]
 };
 struct Experts {
     int E, D, F, fmt, device;
