@@ -170,9 +170,6 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.held = w.held;
         p.pitch = w.pitch;
     };
-    void *err = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&err, g_moe_err);
-    if (e != cudaSuccess) return e;
     const int ldh = (ex.F + 7) / 8 * 8;
     // h, the down sums, and for many columns the prepared rows
     auto up16 = [](size_t n) { return (n + 15) / 16 * 16; };
@@ -184,7 +181,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
     const size_t n_hc = kind == 2 ? (size_t)P * pc_out * out_lines * (16 * KC + 64) : 0;
     const size_t n_info = prepare ? up16((size_t)P * 4) : 0;
     uint8_t *ws = nullptr;
-    e = workspace_alloc((void **)&ws, n_h + n_part + (n_x > n_hc ? n_x : n_hc) + n_info, st);
+    cudaError_t e = workspace_alloc((void **)&ws, n_h + n_part + (n_x > n_hc ? n_x : n_hc) + n_info, st);
     if (e != cudaSuccess) return e;
     float *h = (float *)ws, *sums = (float *)(ws + n_h);
     float *info = (float *)(ws + n_h + n_part);
@@ -197,7 +194,7 @@ cudaError_t run(const Moe &a, cudaStream_t st) {
         p.x = (const char *)a.x + s0 * a.ldx * b;
         p.in = h;
         p.out = h;
-        p.err = (unsigned int *)err;
+        p.err = ex.err;
         p.ldx = a.ldx;
         p.S = n;
         p.P = n * a.k;
@@ -248,6 +245,17 @@ cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st) {
     case B200Q_I4: return run<B200Q_I4>(a, st);
     default: return run<B200Q_I2>(a, st);
     }
+}
+
+// What a call could not do while its stream is captured, done when the handle is
+// made: the lookup of the error word, which may load device code, and the
+// making of the workspaces' pool.
+cudaError_t moe_prepare(unsigned int **err, cudaStream_t st) {
+    void *ws = nullptr;
+    cudaError_t e = cudaGetSymbolAddress((void **)err, g_moe_err);
+    if (e == cudaSuccess) e = workspace_alloc(&ws, 16, st);
+    if (e == cudaSuccess) e = workspace_free(ws, st);
+    return e;
 }
 
 void moe_selftest(long long wait_ns, bool withhold) {

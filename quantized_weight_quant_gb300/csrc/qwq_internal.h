@@ -193,6 +193,7 @@ struct Experts {
     int E, D, F, fmt, device;
     long long ld_in, ld_out;   // row strides of gate / up and of down, bytes
     Expert *table;             // device, [E]
+    unsigned int *err;         // device: where a kernel records an error
 };
 constexpr int kMoeMaxExperts = 1024, kMoeMaxK = 32, kMoeMaxSize = 1 << 24;
 
@@ -212,6 +213,7 @@ struct Moe {
     int S;
 };
 cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st);
+cudaError_t moe_prepare(unsigned int **err, cudaStream_t st);
 cudaError_t moe_take_error(unsigned int *code);
 void moe_selftest(long long wait_ns, bool withhold);
 

@@ -971,3 +971,46 @@ def test_norm_gates_that_are_refused(q):
                        (one(3, 8), ValueError), (one(3, 8, device="cuda").half(), ValueError), (one(8, 3, device="cuda").t(), ValueError)):
         with pytest.raises(what):
             q.block_norm(m, 3, 8, 1e-6, h_out=o, gate=gate)
+
+
+@pytest.mark.parametrize("n,keep", [(1, 1), (32, 5), (8, 8)])
+def test_route_many_tokens_of_many_experts(q, n, keep):
+    """1024 experts for more tokens than one to a block: the most shared memory that routing takes."""
+    l = _dev(synth.normal_f32((400, 1024), n, 1))
+    bias = (0.1 * synth.normal_f32((1024,), n, 2)).astype(np.float32)
+    _route(q, l, 8, 1, bias, n, keep, 2)
+    _route(q, l, 8, 0, bias, n, keep, 1)
+
+
+FIRST = """
+import sys
+sys.path.insert(0, %r)
+import numpy as np, torch
+import quantized_weight_quant_gb300 as q
+S, E, D, F, k = %d, 4, 320, 192, 2
+g, u, d = ([q.tensor_upload(q.I4, O, I, np.full((O, I // 2), 0x99, np.uint8), np.full(O, 1 / 64, np.float32)) for _ in range(E)]
+           for O, I in ((F, D), (F, D), (D, F)))
+ex = q.Experts(g, u, d)
+x, h, y = torch.ones(S, D, device="cuda"), torch.empty(S, D, device="cuda"), torch.empty(S, D, device="cuda")
+l, ids, wts = torch.zeros(S, E, device="cuda"), torch.zeros(S, k, dtype=torch.int32, device="cuda"), torch.zeros(S, k, device="cuda")
+w = torch.ones(D, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q.moe_route(l, ids, wts, S, E, k)
+    q.moe_experts(ex, x, ids, wts, h, S, k, act=q.ACT_NONE)
+    q.block_norm(h, S, D, 0.0, w=w, y=y)
+graph.replay()
+torch.cuda.synchronize()
+assert (h == 25.0 * F / 64).all() and (y - 1).abs().max() < 1e-5, (h, y)
+"""
+
+
+@pytest.mark.parametrize("S", [1, 5, 64])
+def test_first_calls_of_a_process_may_be_captured(S):
+    """1 * 320 / 64 = 5 for gate and for up, h = 25, y = 25 * 192 / 64 with weights that add up to 1."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % (root, S)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
