@@ -1007,7 +1007,7 @@ b200q_experts *b200q_experts_create(const b200q_tensor *const *gate, const b200q
         cudaStream_t st = nullptr;
         cudaError_t c = cudaMalloc((void **)&ex->table, (size_t)E * sizeof(Expert));
         if (c == cudaSuccess) c = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
-        if (c == cudaSuccess) c = moe_prepare(&ex->err, st);
+        if (c == cudaSuccess) c = moe_make_ready(&ex->err, st);
         if (c == cudaSuccess) c = cudaMemcpyAsync(ex->table, host, (size_t)E * sizeof(Expert), cudaMemcpyHostToDevice, st);
         if (c == cudaSuccess) c = cudaStreamSynchronize(st);
         if (st) cudaStreamDestroy(st);

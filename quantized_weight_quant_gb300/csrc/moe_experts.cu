@@ -250,7 +250,7 @@ cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st) {
 // What a call could not do while its stream is captured, done when the handle is
 // made: the lookup of the error word, which may load device code, and the
 // making of the workspaces' pool.
-cudaError_t moe_prepare(unsigned int **err, cudaStream_t st) {
+cudaError_t moe_make_ready(unsigned int **err, cudaStream_t st) {
     void *ws = nullptr;
     cudaError_t e = cudaGetSymbolAddress((void **)err, g_moe_err);
     if (e == cudaSuccess) e = workspace_alloc(&ws, 16, st);

@@ -213,7 +213,7 @@ struct Moe {
     int S;
 };
 cudaError_t launch_moe_experts(const Moe &a, cudaStream_t st);
-cudaError_t moe_prepare(unsigned int **err, cudaStream_t st);
+cudaError_t moe_make_ready(unsigned int **err, cudaStream_t st);
 cudaError_t moe_take_error(unsigned int *code);
 void moe_selftest(long long wait_ns, bool withhold);
 
