@@ -1014,3 +1014,26 @@ def test_first_calls_of_a_process_may_be_captured(S):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST % (root, S)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("S,D,F", PRODUCTS)
+def test_experts_small_values_beside_a_large_one(q, S, D, F, fmt):
+    """Products that do not cancel, of rows whose largest value, 2^30 times the rest, meets a code of 0: what f32 rows have beside it is held
+    to 2^-50 of it, what bf16 rows have to 2^-40."""
+    rng = np.random.default_rng(D + S + 2)
+    top = {"i8": 127, "i4": 7, "i2": 1}[fmt]
+    gate, large = rng.integers(-top, top + 1, (F, D)), D // 3
+    gate[:, 0] = gate[:, large] = 0
+    layer = Given(q, fmt, [(gate, np.ones(F)), (_one_of(F, D, lambda o: 0 * o), np.ones(F)), (_one_of(D, F, lambda o: o % F), np.ones(D))])
+    for kind, part in (("f32", 2.0 ** -50), ("bf16", 2.0 ** -40)):
+        x = synth.normal_f32((S, D), D, 1)
+        x[:, 0], x[:, large] = 1, 2.0 ** 30
+        x, y = _given(q, layer, x, kind)
+        g = (x @ gate.T.astype(np.float64))
+        x[:, large] = 0
+        tol = 1e-5 * (np.abs(x) @ np.abs(gate).T.astype(np.float64)) + part * 2.0 ** 30 * np.abs(gate).sum(1)
+        tol = tol + (2.0 ** -11 if kind == "bf16" else 2.0 ** -22) * (np.abs(g) + tol)          # h
+        g, tol = (v[:, np.arange(D) % F] for v in (g, tol))
+        assert (np.abs(y - g) <= tol + _half_step(kind) * (np.abs(g) + tol)).all(), "%s: %g" % (kind, (np.abs(y - g) / tol).max())
+    layer.free()
